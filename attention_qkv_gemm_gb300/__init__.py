@@ -26,6 +26,9 @@ TFL_ERR_CUDA = -4
 TFL_ERR_DEVICE_TIMEOUT = -5
 TFL_ERR_BAD_LENGTHS = -6
 
+# element types of the operators that stand on their own
+TFL_F32, TFL_F16, TFL_BF16, TFL_E4M3 = 0, 1, 2, 3
+
 KIND_NAMES = {1: "rownorm", 2: "gemm_qkv", 3: "attention", 4: "gemm_oproj", 5: "gemm_ffn1", 6: "gemm_ffn2",
               7: "postchain", 8: "stack"}
 
@@ -33,7 +36,8 @@ EXPORTS = ("tfl_default_options", "tfl_workspace_bytes", "tfl_create", "tfl_forw
            "tfl_forward_host", "tfl_forward_streamed",
            "tfl_attn_create", "tfl_attn_forward", "tfl_attn_backward", "tfl_attn_status", "tfl_attn_destroy",
            "tfl_status", "tfl_destroy", "tfl_last_error", "tfl_profile_forward", "tfl_launch_count",
-           "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu")
+           "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu",
+           "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy")
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -125,6 +129,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.tfl_selftest_gelu.restype = ctypes.c_int
     lib.tfl_probe_wait_timeout.argtypes = [i64, vp]
     lib.tfl_probe_wait_timeout.restype = ctypes.c_int
+    lib.tfl_rmsnorm_create.argtypes = [i32, i32, i32, i32, ctypes.c_float, ctypes.POINTER(vp)]
+    lib.tfl_rmsnorm_create.restype = ctypes.c_int
+    lib.tfl_rmsnorm_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_rmsnorm_forward.restype = ctypes.c_int
+    lib.tfl_rmsnorm_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_rmsnorm_backward.restype = ctypes.c_int
+    lib.tfl_rmsnorm_destroy.argtypes = [vp]
+    lib.tfl_rmsnorm_destroy.restype = None
     _lib = lib
     return lib
 
@@ -215,6 +227,31 @@ def tfl_attn_status(handle: int, stream: int = 0) -> int:
 def tfl_attn_destroy(handle: int) -> None:
     if handle:
         load().tfl_attn_destroy(handle)
+
+
+def tfl_rmsnorm_create(d_model: int, x_type: int, res_type: int, y_type: int, eps: float = 1e-5) -> int:
+    """A root-mean-square norm with the residual's addition; types are ``TFL_F32`` and so on."""
+    h = ctypes.c_void_p()
+    _check(load().tfl_rmsnorm_create(int(d_model), int(x_type), int(res_type), int(y_type), float(eps),
+                                     ctypes.byref(h)))
+    return h.value
+
+
+def tfl_rmsnorm_forward(handle: int, rows: int, x: int, res: Optional[int], gamma: int, res_out: Optional[int],
+                        y: int, y_scale: Optional[int] = None, stream: int = 0) -> None:
+    """res_out = x + res; y = its norm times gamma (device pointers to [rows, d_model])."""
+    _check(load().tfl_rmsnorm_forward(handle, rows, x, res, gamma, res_out, y, y_scale, stream))
+
+
+def tfl_rmsnorm_backward(handle: int, rows: int, sum: int, gamma: int, dy: int, dres: Optional[int],
+                         dx: Optional[int], dsum: Optional[int], dgamma: int, stream: int = 0) -> None:
+    """The gradient of x + res (as dx in x's type, as dsum in the residual's) and of gamma."""
+    _check(load().tfl_rmsnorm_backward(handle, rows, sum, gamma, dy, dres, dx, dsum, dgamma, stream))
+
+
+def tfl_rmsnorm_destroy(handle: int) -> None:
+    if handle:
+        load().tfl_rmsnorm_destroy(handle)
 
 
 def tfl_status(handle: int, stream: int = 0) -> int:

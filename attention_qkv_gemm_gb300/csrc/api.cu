@@ -20,41 +20,12 @@
 #include <vector>
 
 #include "tfl.h"
+#include "host.h"
 #include "kernels.h"
 
 using namespace tfl;
 
 namespace {
-
-thread_local std::string g_err;
-
-int fail(int code, const std::string& msg) {
-  g_err = msg;
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(TFL_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
-
-#define TFL_CUDA(call, what)                         \
-  do {                                               \
-    cudaError_t e_ = (call);                         \
-    if (e_ != cudaSuccess) return cuda_fail(e_, what); \
-  } while (0)
-
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
 
 // 2D fp16 map over a row-major [rows, cols] matrix, box {64, box_rows}, 128B swizzle.
 bool make_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {

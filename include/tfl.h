@@ -343,6 +343,78 @@ int tfl_attn_status(tfl_attn* a, tfl_stream stream);
 
 void tfl_attn_destroy(tfl_attn* a);
 
+/*
+ * The rest of a block on its own, beside the attention above: the
+ * root-mean-square norm in front of a sublayer and the gated feed-forward
+ * ("Training throughput baseline" trains a model of such blocks).
+ *
+ * Element types of these operators.
+ */
+#define TFL_F32  0
+#define TFL_F16  1
+#define TFL_BF16 2
+#define TFL_E4M3 3   /* 8 bits: 4 exponent, 3 mantissa, largest value 448 */
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   s = x + res,   r = 1 / sqrt(mean(s^2) + eps),   y = s r gamma   (per row)
+ * s, the sums and y are fp32 inside; res_out is s and y is y, each rounded once
+ * to its type (y is taken from the unrounded s).
+ *
+ * e4m3 output: y_scale[row] = max(max|y|, 2^-100) / 448 and y holds
+ * e4m3(y / y_scale[row]), so y_scale[row] times the stored value is the norm's
+ * output; a row with a NaN has a NaN scale.
+ *
+ * Types: x fp32, fp16 or bf16; the residual fp32 or x's type; y x's type or
+ * e4m3, and for fp32 x also fp16 or bf16.  gamma is fp32.
+ */
+typedef struct tfl_rmsnorm tfl_rmsnorm;
+
+/* d_model in 1 .. 2^24, eps >= 0 and finite.  Unless y is e4m3 the handle also holds the
+ * backward's scratch (at most max(64 MiB, 4 d_model bytes)).
+ * Errors: INVALID_ARG, UNSUPPORTED (types, device), OOM, CUDA. */
+int tfl_rmsnorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int32_t y_type, float eps,
+                       tfl_rmsnorm** out);
+
+/*
+ * Asynchronous on `stream`.  Device pointers, rows of d_model values one after
+ * the other, 0 <= rows < 2^31 (0: nothing is done):
+ *   x        [rows, d_model]
+ *   res      [rows, d_model] of the residual's type, or NULL (s = x)
+ *   gamma    fp32 [d_model]
+ *   res_out  [rows, d_model] of the residual's type, or NULL (s is not stored);
+ *            may be res, or x when the types are the same
+ *   y        [rows, d_model]; may be x when the types are the same (and res_out is not x)
+ *   y_scale  fp32 [rows] for an e4m3 y, else NULL
+ * Other overlaps of an output are refused.  Any element-aligned buffers and
+ * widths; 16-byte aligned buffers (y: 8 bytes for e4m3) and a d_model that is a
+ * multiple of 8 up to 32768 take the kernels that keep a row in registers.
+ * Calls on one handle may overlap.
+ * Errors: INVALID_ARG (also when the current device is not the handle's), CUDA.
+ */
+int tfl_rmsnorm_forward(tfl_rmsnorm* n, int64_t rows, const void* x, const void* res, const float* gamma,
+                        void* res_out, void* y, float* y_scale, tfl_stream stream);
+
+/*
+ * The gradients, with a = dy gamma and r as above (recomputed from s):
+ *   ds = dres + r a - s r^3 mean(a s),   dgamma = sum over rows of dy s r
+ *   sum     [rows, d_model] of the residual's type: the forward's res_out (x if it had no residual)
+ *   dy      [rows, d_model] of y's type (which must be x's type)
+ *   dres    [rows, d_model] of the residual's type: the gradient that reaches s past the norm, or NULL
+ *   dx      ds in x's type, or NULL;  dsum  ds in the residual's type, or NULL
+ *           (s = x + res, so ds is the gradient of both; at least one is given)
+ *   dgamma  fp32 [d_model], written in full (zeros for rows = 0)
+ * dx or dsum may be dy, dres or sum where the types are the same; other overlaps
+ * are refused.  No atomics: the same inputs give the same bits.  Calls on one
+ * handle share its scratch and must not overlap on the GPU (graphs that hold such
+ * calls included).  Errors: INVALID_ARG, UNSUPPORTED (y is not of x's type), CUDA.
+ */
+int tfl_rmsnorm_backward(tfl_rmsnorm* n, int64_t rows, const void* sum, const float* gamma, const void* dy,
+                         const void* dres, void* dx, void* dsum, float* dgamma, tfl_stream stream);
+
+/* Free what the handle owns.  Synchronizes the device.  NULL is a no-op. */
+void tfl_rmsnorm_destroy(tfl_rmsnorm* n);
+
 #ifdef __cplusplus
 }
 #endif
