@@ -28,6 +28,7 @@ TFL_ERR_BAD_LENGTHS = -6
 
 # element types of the operators that stand on their own
 TFL_F32, TFL_F16, TFL_BF16, TFL_E4M3 = 0, 1, 2, 3
+TFL_ACT_SILU, TFL_ACT_GELU = 0, 1
 
 KIND_NAMES = {1: "rownorm", 2: "gemm_qkv", 3: "attention", 4: "gemm_oproj", 5: "gemm_ffn1", 6: "gemm_ffn2",
               7: "postchain", 8: "stack"}
@@ -37,7 +38,8 @@ EXPORTS = ("tfl_default_options", "tfl_workspace_bytes", "tfl_create", "tfl_forw
            "tfl_attn_create", "tfl_attn_forward", "tfl_attn_backward", "tfl_attn_status", "tfl_attn_destroy",
            "tfl_status", "tfl_destroy", "tfl_last_error", "tfl_profile_forward", "tfl_launch_count",
            "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu",
-           "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy")
+           "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy",
+           "tfl_glu_create", "tfl_glu_forward", "tfl_glu_backward", "tfl_glu_status", "tfl_glu_destroy")
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -137,6 +139,16 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.tfl_rmsnorm_backward.restype = ctypes.c_int
     lib.tfl_rmsnorm_destroy.argtypes = [vp]
     lib.tfl_rmsnorm_destroy.restype = None
+    lib.tfl_glu_create.argtypes = [i32, i32, i32, i32, i32, i64, ctypes.POINTER(vp)]
+    lib.tfl_glu_create.restype = ctypes.c_int
+    lib.tfl_glu_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_glu_forward.restype = ctypes.c_int
+    lib.tfl_glu_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_glu_backward.restype = ctypes.c_int
+    lib.tfl_glu_status.argtypes = [vp, vp]
+    lib.tfl_glu_status.restype = ctypes.c_int
+    lib.tfl_glu_destroy.argtypes = [vp]
+    lib.tfl_glu_destroy.restype = None
     _lib = lib
     return lib
 
@@ -252,6 +264,36 @@ def tfl_rmsnorm_backward(handle: int, rows: int, sum: int, gamma: int, dy: int, 
 def tfl_rmsnorm_destroy(handle: int) -> None:
     if handle:
         load().tfl_rmsnorm_destroy(handle)
+
+
+def tfl_glu_create(d_model: int, d_ff: int, in_type: int, out_type: int, act: int = TFL_ACT_SILU,
+                   max_grad_tokens: int = 0) -> int:
+    """A gated feed-forward block; types are ``TFL_F16`` and so on, act ``TFL_ACT_SILU`` or ``TFL_ACT_GELU``."""
+    h = ctypes.c_void_p()
+    _check(load().tfl_glu_create(int(d_model), int(d_ff), int(in_type), int(out_type), int(act),
+                                 int(max_grad_tokens), ctypes.byref(h)))
+    return h.value
+
+
+def tfl_glu_forward(handle: int, tokens: int, x: int, x_scale: Optional[int], wg: int, wg_scale: Optional[int],
+                    wu: int, wu_scale: Optional[int], h: int, stream: int = 0) -> None:
+    """h = act(x Wg^T) * (x Wu^T) (device pointers; scales for e4m3 operands only)."""
+    _check(load().tfl_glu_forward(handle, tokens, x, x_scale, wg, wg_scale, wu, wu_scale, h, stream))
+
+
+def tfl_glu_backward(handle: int, tokens: int, x: int, wg: int, wu: int, dh: int, dx: int, dwg: int, dwu: int,
+                     stream: int = 0) -> None:
+    """dx, dwg and dwu from the forward's inputs and dh."""
+    _check(load().tfl_glu_backward(handle, tokens, x, wg, wu, dh, dx, dwg, dwu, stream))
+
+
+def tfl_glu_status(handle: int, stream: int = 0) -> int:
+    return load().tfl_glu_status(handle, stream)
+
+
+def tfl_glu_destroy(handle: int) -> None:
+    if handle:
+        load().tfl_glu_destroy(handle)
 
 
 def tfl_status(handle: int, stream: int = 0) -> int:

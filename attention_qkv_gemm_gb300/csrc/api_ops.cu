@@ -1,5 +1,7 @@
 // api_ops.cu -- the C ABI of the operators that stand on their own (include/tfl.h): the
-// root-mean-square norm.
+// root-mean-square norm and the gated feed-forward.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <new>
 
@@ -199,6 +201,228 @@ void tfl_rmsnorm_destroy(tfl_rmsnorm* n) {
   cudaDeviceSynchronize();
   if (n->partial) cudaFree(n->partial);
   delete n;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Gated feed-forward.
+struct tfl_glu {
+  int D = 0, F = 0, in_type = 0, out_type = 0, act = 0;
+  int64_t max_grad_tokens = 0;
+  int device = 0, num_sms = 0;
+  int* status = nullptr;                          // status word (256 bytes), then dg and du
+  uint16_t *dg = nullptr, *du = nullptr;          // [max_grad_tokens, F]
+};
+
+namespace {
+
+// A row-major [rows, cols] matrix in boxes of 128 bytes of columns by box_rows, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, uint32_t box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(cols * elem)};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / elem), box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return get_encode()(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                      const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMnBox = 64;  // MN-major operands come in boxes of 64 k rows
+
+int check_tokens(const tfl_glu* g, int64_t tokens) {
+  if (tokens < 0 || tokens > INT32_MAX - 512) return fail(TFL_ERR_INVALID_ARG, "tokens must be in 0 .. 2^31 - 513");
+  if ((tokens + 127) / 128 * ((g->F + 31) / 32) > INT32_MAX || (tokens + 127) / 128 * ((g->D + 31) / 32) > INT32_MAX)
+    return fail(TFL_ERR_UNSUPPORTED, "too many tokens for this width");
+  return TFL_OK;
+}
+
+GluArgs glu_args(const tfl_glu* g) {
+  GluArgs a;
+  a.act = g->act;
+  a.bf16_operands = g->in_type == TFL_BF16;
+  a.bf16_out = g->out_type == TFL_BF16;
+  a.status = g->status;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_type, int32_t act,
+                   int64_t max_grad_tokens, tfl_glu** out) {
+  g_err.clear();
+  if (!out) return fail(TFL_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (d_model < 1 || d_ff < 1) return fail(TFL_ERR_INVALID_ARG, "d_model and d_ff must be >= 1");
+  if (act != TFL_ACT_SILU && act != TFL_ACT_GELU) return fail(TFL_ERR_INVALID_ARG, "no such activation");
+  if (max_grad_tokens < 0 || max_grad_tokens > INT32_MAX - 512)
+    return fail(TFL_ERR_INVALID_ARG, "max_grad_tokens must be in 0 .. 2^31 - 513");
+  if (!type_16bit(out_type) || !(in_type == out_type || in_type == TFL_E4M3))
+    return fail(TFL_ERR_UNSUPPORTED, "the output must be fp16 or bf16, the operands of its type or e4m3");
+  if (in_type == TFL_E4M3 && max_grad_tokens) return fail(TFL_ERR_UNSUPPORTED, "e4m3 operands have no backward");
+  const int step = in_type == TFL_E4M3 ? 16 : 8;
+  if (d_model % step || d_ff % step || d_model > (1 << 24) || d_ff > (1 << 24))
+    return fail(TFL_ERR_UNSUPPORTED,
+                "d_model and d_ff must be multiples of 8 (16 for e4m3 operands), at most 2^24");
+  int dev = 0, sms = 0;
+  if (int rc = usable_device(&dev, &sms)) return rc;
+  if (!get_encode()) return fail(TFL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  TFL_CUDA(prepare_glu_kernels(), "feed-forward kernel attributes");
+  tfl_glu* g = new (std::nothrow) tfl_glu();
+  if (!g) return fail(TFL_ERR_OOM, "handle allocation failed");
+  g->D = d_model;
+  g->F = d_ff;
+  g->in_type = in_type;
+  g->out_type = out_type;
+  g->act = act;
+  g->max_grad_tokens = max_grad_tokens;
+  g->device = dev;
+  g->num_sms = sms;
+  const size_t each = ((size_t)max_grad_tokens * d_ff * 2 + 255) / 256 * 256;
+  if (cudaMalloc(&g->status, 256 + 2 * each) != cudaSuccess) {
+    cudaGetLastError();
+    delete g;
+    return fail(TFL_ERR_OOM, "scratch allocation for the feed-forward failed");
+  }
+  g->dg = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(g->status) + 256);
+  g->du = g->dg + each / 2;
+  if (cudaMemset(g->status, 0, 256) != cudaSuccess) {
+    cudaFree(g->status);
+    delete g;
+    return fail(TFL_ERR_CUDA, "status word clear failed");
+  }
+  *out = g;
+  return TFL_OK;
+}
+
+int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_scale, const void* wg,
+                    const float* wg_scale, const void* wu, const float* wu_scale, void* h, tfl_stream stream) {
+  g_err.clear();
+  if (!g) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  if (int rc = check_tokens(g, tokens)) return rc;
+  if (tokens == 0) return TFL_OK;
+  if (!x || !wg || !wu || !h) return fail(TFL_ERR_INVALID_ARG, "x, wg, wu and h must be non-NULL device pointers");
+  const bool f8 = g->in_type == TFL_E4M3;
+  if (f8 ? !(x_scale && wg_scale && wu_scale) : (x_scale || wg_scale || wu_scale))
+    return fail(TFL_ERR_INVALID_ARG, "scales go with e4m3 operands, and only with them");
+  if (misaligned(x, 16) || misaligned(wg, 16) || misaligned(wu, 16) || misaligned(h, 16) ||
+      misaligned(x_scale, 4) || misaligned(wg_scale, 16) || misaligned(wu_scale, 16))
+    return fail(TFL_ERR_INVALID_ARG, "x, wg, wu, h and the weights' scales must be 16-byte aligned");
+  const size_t es = f8 ? 1 : 2, T = (size_t)tokens, D = g->D, F = g->F;
+  const Span sh{h, T * F * 2, g->out_type};
+  const Span in[6] = {{x, T * D * es, 0},      {wg, F * D * es, 0},    {wu, F * D * es, 0},
+                      {x_scale, T * 4, 0}, {wg_scale, F * 4, 0}, {wu_scale, F * 4, 0}};
+  for (const Span& i : in)
+    if (overlap(sh, i, false)) return fail(TFL_ERR_INVALID_ARG, "h overlaps another buffer");
+  if (int rc = same_device(g->device)) return rc;
+  const GluPlan p = glu_plan(GLU_FORWARD, f8, tokens, g->F, g->num_sms);
+  GluMaps mp;
+  if (!make_map(&mp.a0, x, tokens, g->D, (int)es, kGluRows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bn / 2) ||
+      !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bn / 2))
+    return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
+  mp.a1 = mp.a0;
+  GluArgs a = glu_args(g);
+  a.M = (int)tokens;
+  a.N = g->F;
+  const int ke = f8 ? 128 : 64;
+  a.num_k = (g->D + ke - 1) / ke;
+  a.x_scale = x_scale;
+  a.g_scale = wg_scale;
+  a.u_scale = wu_scale;
+  a.out = static_cast<uint16_t*>(h);
+  TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, g->num_sms, static_cast<cudaStream_t>(stream)), "feed-forward");
+  return TFL_OK;
+}
+
+int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, const void* wu, const void* dh,
+                     void* dx, void* dwg, void* dwu, tfl_stream stream) {
+  g_err.clear();
+  if (!g) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  if (int rc = check_tokens(g, tokens)) return rc;
+  if (g->in_type == TFL_E4M3) return fail(TFL_ERR_UNSUPPORTED, "e4m3 operands have no backward");
+  if (tokens > g->max_grad_tokens)
+    return fail(TFL_ERR_INVALID_ARG, "more tokens than the max_grad_tokens the handle was created with");
+  if (!dwg || !dwu) return fail(TFL_ERR_INVALID_ARG, "dwg and dwu must be non-NULL device pointers");
+  const size_t T = (size_t)tokens, D = g->D, F = g->F;
+  if (misaligned(dwg, 16) || misaligned(dwu, 16)) return fail(TFL_ERR_INVALID_ARG, "every buffer must be 16-byte aligned");
+  const Span outs[3] = {{dx, T * D * 2, 0}, {dwg, F * D * 2, 0}, {dwu, F * D * 2, 0}};
+  if (overlap(outs[1], outs[2], false)) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+  if (int rc = same_device(g->device)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    TFL_CUDA(cudaMemsetAsync(dwg, 0, F * D * 2, st), "dwg clear");
+    TFL_CUDA(cudaMemsetAsync(dwu, 0, F * D * 2, st), "dwu clear");
+    return TFL_OK;
+  }
+  if (!x || !wg || !wu || !dh || !dx)
+    return fail(TFL_ERR_INVALID_ARG, "x, wg, wu, dh and dx must be non-NULL device pointers");
+  if (misaligned(x, 16) || misaligned(wg, 16) || misaligned(wu, 16) || misaligned(dh, 16) || misaligned(dx, 16))
+    return fail(TFL_ERR_INVALID_ARG, "every buffer must be 16-byte aligned");
+  const Span ins[4] = {{x, T * D * 2, 0}, {wg, F * D * 2, 0}, {wu, F * D * 2, 0}, {dh, T * F * 2, 0}};
+  bool bad = overlap(outs[0], outs[1], false) || overlap(outs[0], outs[2], false);
+  for (const Span& o : outs)
+    for (const Span& i : ins) bad = bad || overlap(o, i, false);
+  if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+
+  const int Di = g->D, Fi = g->F, Ti = (int)tokens;
+  const GluPlan p1 = glu_plan(GLU_SLOPES, false, tokens, Fi, g->num_sms);
+  const GluPlan p2 = glu_plan(GLU_DX, false, tokens, Di, g->num_sms);
+  const GluPlan p3 = glu_plan(GLU_DW, false, Fi, Di, g->num_sms);
+  GluMaps m1, m2, m3;
+  bool ok = make_map(&m1.a0, x, tokens, Di, 2, kGluRows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bn / 2) &&
+            make_map(&m1.b1, wu, Fi, Di, 2, p1.bn / 2);
+  m1.a1 = m1.a0;
+  ok = ok && make_map(&m2.a0, g->dg, tokens, Fi, 2, kGluRows) && make_map(&m2.a1, g->du, tokens, Fi, 2, kGluRows) &&
+       make_map(&m2.b0, wg, Fi, Di, 2, kMnBox) && make_map(&m2.b1, wu, Fi, Di, 2, kMnBox);
+  ok = ok && make_map(&m3.a0, g->dg, tokens, Fi, 2, kMnBox) && make_map(&m3.a1, g->du, tokens, Fi, 2, kMnBox) &&
+       make_map(&m3.b0, x, tokens, Di, 2, kMnBox);
+  m3.b1 = m3.b0;
+  if (!ok) return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
+
+  GluArgs a = glu_args(g);
+  a.M = Ti;
+  a.N = Fi;
+  a.num_k = (Di + 63) / 64;
+  a.dh = static_cast<const uint16_t*>(dh);
+  a.out = g->dg;
+  a.out2 = g->du;
+  TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, g->num_sms, st), "feed-forward slopes");
+  a = glu_args(g);
+  a.M = Ti;
+  a.N = Di;
+  a.k_half = (Fi + 63) / 64;
+  a.num_k = 2 * a.k_half;
+  a.out = static_cast<uint16_t*>(dx);
+  TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, g->num_sms, st), "feed-forward dx");
+  a = glu_args(g);
+  a.M = Fi;
+  a.N = Di;
+  a.num_k = (Ti + 63) / 64;
+  a.out = static_cast<uint16_t*>(dwg);
+  a.out2 = static_cast<uint16_t*>(dwu);
+  TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, g->num_sms, st), "feed-forward weight gradients");
+  return TFL_OK;
+}
+
+int tfl_glu_status(tfl_glu* g, tfl_stream stream) {
+  g_err.clear();
+  if (!g) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  TFL_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)), "cudaStreamSynchronize");
+  int v = 0;
+  TFL_CUDA(cudaMemcpy(&v, g->status, sizeof(int), cudaMemcpyDeviceToHost), "status read");
+  if (v) TFL_CUDA(cudaMemset(g->status, 0, sizeof(int)), "status clear");
+  if (v & TFL_DEV_TIMEOUT) return fail(TFL_ERR_DEVICE_TIMEOUT, "a device-side wait ran out of time");
+  return TFL_OK;
+}
+
+void tfl_glu_destroy(tfl_glu* g) {
+  if (!g) return;
+  cudaDeviceSynchronize();
+  if (g->status) cudaFree(g->status);
+  delete g;
 }
 
 }  // extern "C"

@@ -1,0 +1,475 @@
+// glu.cu -- the gated feed-forward block h = act(x Wg^T) * (x Wu^T), forward and backward.
+//
+// One persistent tcgen05 GEMM kernel in four modes, fp32 accumulation in tensor memory:
+//   GLU_FORWARD   both projections of a tile at once: the accumulator's first half of columns
+//                 is x Wg^T, its second half x Wu^T of the same output columns, so the
+//                 activation and the product run in the epilogue and only h is written.
+//                 16-bit operands, or e4m3 with one scale a row of x, Wg and Wu (the scales
+//                 factor out of the sums, so the epilogue applies them).
+//   GLU_SLOPES    the same two products; with dh the epilogue forms dg = dh u act'(g) and
+//                 du = dh act(g) from the fp32 accumulators.  Nothing of the forward is kept:
+//                 reading back 16-bit g and u would cost 4 bytes a value of memory and round
+//                 them once more, where recomputing rounds only dg and du (once, to the
+//                 operand type the tensor cores take).
+//   GLU_DX        dx = dg Wg + du Wu: one sum over 2 d_ff, W read as [k, n] (MN-major).
+//   GLU_DW        dWg = dg^T x and dWu = du^T x: sums over the tokens, both operands MN-major.
+//
+// Structure: warp 0 feeds a ring of k-blocks (128 bytes of k a row, 128-byte swizzle) by TMA,
+// warp 1 issues the MMAs, warps 2-9 are the epilogue (two per tensor-memory lane quarter), two
+// accumulators so that a tile's epilogue runs under the next tile's MMAs.
+// Ragged sizes: TMA fills what lies outside a matrix with zeros (zero rows and zero k add
+// nothing), and the epilogue stores only rows and columns that exist.
+#include "cluster.cuh"
+#include "mathfn.cuh"
+#include "ops.h"
+#include "xpose.cuh"
+
+namespace tfl {
+
+namespace {
+
+constexpr int kGluEpiWarps = 8;
+constexpr int kGluThreads = 64 + 32 * kGluEpiWarps;
+constexpr int kKBytes = 128;       // bytes of k a row and stage
+constexpr int kMnChunk = 64 * 128; // MN-major operands: 64 k rows of 64 values
+
+template <int CG, int BN>
+struct GluCfg {
+  static constexpr int A_BYTES = kGluRows * kKBytes;
+  static constexpr int B_ROWS = BN / CG;  // rows of B this CTA supplies
+  static constexpr int B_BYTES = B_ROWS * kKBytes;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int XPOSE_BYTES = kGluEpiWarps * 32 * 128;
+  static constexpr int RING_MAX = 232448 - 1024 - XPOSE_BYTES - 256;
+  static constexpr int STAGES = RING_MAX / STAGE > 8 ? 8 : RING_MAX / STAGE;
+  static constexpr int TMEM_COLS = 2 * BN;  // 128, 256 or 512
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + XPOSE_BYTES + 256;
+};
+
+// act(g) and act'(g).  SiLU: g p with p = 1 / (1 + e^-g), slope p (1 + g (1 - p)).  GELU (exact
+// erf form, erf as in gelu_as7126): g Phi(g), slope Phi(g) + g phi(g).
+__device__ __forceinline__ void act_and_slope(float g, int act, float& a, float& slope) {
+  if (act == TFL_ACT_SILU) {
+    const float p = rcp_approx(1.0f + ex2(g * -1.4426950408889634f));
+    a = g * p;
+    slope = p * fmaf(g, 1.0f - p, 1.0f);
+  } else {
+    constexpr float p_s = 0.3275911f * 0.7071067811865476f;
+    constexpr float h1 = 0.5f * 0.254829592f, h2 = 0.5f * -0.284496736f, h3 = 0.5f * 1.421413741f,
+                    h4 = 0.5f * -1.453152027f, h5 = 0.5f * 1.061405429f;
+    const float e = ex2((g * g) * -0.7213475204444817f);
+    const float t = rcp_approx(fmaf(p_s, fabsf(g), 1.0f));
+    const float half_erfc = t * fmaf(fmaf(fmaf(fmaf(h5, t, h4), t, h3), t, h2), t, h1) * e;
+    const float cdf = g >= 0.f ? 1.0f - half_erfc : half_erfc;
+    a = g * cdf;
+    slope = fmaf(g * 0.3989422804014327f, e, cdf);
+  }
+}
+__device__ __forceinline__ float act_only(float g, int act) {
+  return act == TFL_ACT_SILU ? g * rcp_approx(1.0f + ex2(g * -1.4426950408889634f)) : gelu_as7126(g);
+}
+
+template <int N>
+__device__ __forceinline__ void pack16(const float* v, uint4* o, int bf16) {
+  if (bf16)
+    pack_bf16<N>(v, o);
+  else
+    pack_f16<N>(v, o, false);
+}
+__device__ __forceinline__ void unpack16(const uint4& w, float* v, int bf16) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf16) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+// W 16-bit columns of the warp's 32 rows through the stage to global memory; rows by mask,
+// columns (8 a chunk) below `cols`.
+template <int W>
+__device__ __forceinline__ void store_cols(uint8_t* st, int lane, const uint4* v, uint16_t* row0, size_t pitch,
+                                           uint32_t rows, int cols) {
+  using X = XStage<W * 2>;
+  X::put_row(st, lane, v);
+  __syncwarp();
+  uint4 o[X::CPR];
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k)
+    o[k] = *reinterpret_cast<const uint4*>(st + X::off(X::RPI * k + lane / X::CPR, lane % X::CPR));
+  const int q = lane % X::CPR;
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k) {
+    const int i = X::RPI * k + lane / X::CPR;
+    if (((rows >> i) & 1u) && q * 8 < cols) *reinterpret_cast<uint4*>(row0 + (size_t)i * pitch + q * 8) = o[k];
+  }
+  __syncwarp();
+}
+// The same way back: this thread's row of W 16-bit columns (zeros outside).
+template <int W>
+__device__ __forceinline__ void load_cols(uint8_t* st, int lane, uint4* v, const uint16_t* row0, size_t pitch,
+                                          uint32_t rows, int cols) {
+  using X = XStage<W * 2>;
+  const int q = lane % X::CPR;
+  uint4 f[X::CPR];
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k) {
+    const int i = X::RPI * k + lane / X::CPR;
+    f[k] = ((rows >> i) & 1u) && q * 8 < cols
+               ? *reinterpret_cast<const uint4*>(row0 + (size_t)i * pitch + q * 8)
+               : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k)
+    *reinterpret_cast<uint4*>(st + X::off(X::RPI * k + lane / X::CPR, q)) = f[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k) v[k] = *reinterpret_cast<const uint4*>(st + X::off(lane, k));
+  __syncwarp();
+}
+
+struct Tile {
+  int m, n, z;
+};
+
+// Tiles in groups of kGroupM row blocks, column by column inside a group, so that the tiles in
+// flight share operands through L2.  DW: first all of dWg, then all of dWu.
+constexpr int kGroupM = 8;
+__device__ __forceinline__ Tile tile_at(int t, int num_m, int num_n) {
+  Tile r;
+  const int per = num_m * num_n;
+  r.z = t / per;
+  t -= r.z * per;
+  const int g = t / (kGroupM * num_n), first = g * kGroupM;
+  const int gm = min(num_m - first, kGroupM);
+  t -= g * kGroupM * num_n;
+  r.n = t / gm;
+  r.m = first + t - r.n * gm;
+  return r;
+}
+
+template <int CG, int BN, int MODE, bool F8>
+__global__ void __launch_bounds__(kGluThreads, 1)
+    glu_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+               const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GluArgs args) {
+  using C = GluCfg<CG, BN>;
+  constexpr bool TWO = MODE == GLU_FORWARD || MODE == GLU_SLOPES;  // two products side by side
+  constexpr int BNO = TWO ? BN / 2 : BN;                           // output columns a tile
+  constexpr bool A_MN = MODE == GLU_DW, B_MN = MODE == GLU_DX || MODE == GLU_DW;
+  constexpr int KE = F8 ? 128 : 64;                                // k elements a stage
+  extern __shared__ uint8_t smem_raw[];
+  grid_launch_dependents();
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* xpose = smem + (size_t)C::STAGES * C::STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + C::XPOSE_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* accf = empty + C::STAGES;
+  uint64_t* acce = accf + 2;
+  uint64_t* drain = acce + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  int* never_flag = abort_flag + 1;  // stays 0: lets the drain waits ignore abort_flag
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&accf[a], 1);
+      mbar_init(&acce[a], CG * kGluEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA0);
+    tma_prefetch_desc(&tmB0);
+  }
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // the peer's barriers exist before anything reaches them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const WaitCtl wc{args.status, abort_flag, args.timeout_ns};
+  grid_wait_prior();  // everything below reads or writes what earlier kernels use
+
+  const int num_m = (args.M + kGluRows * CG - 1) / (kGluRows * CG), num_n = (args.N + BNO - 1) / BNO;
+  const int total = num_m * num_n * (MODE == GLU_DW ? 2 : 1);
+  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
+  const int num_k = args.num_k;
+
+  uint32_t issued_mask = 0, issued_par = 0;  // stages with loads in flight (abort path)
+  bool mma_issued = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        const Tile tl = tile_at(t, num_m, num_n);
+        const int m0 = (tl.m * CG + rank) * kGluRows;
+        for (int kb = 0; kb < num_k; ++kb) {
+          if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + (size_t)stage * C::STAGE;
+          uint8_t* sb = sa + C::A_BYTES;
+          uint64_t* bar = &full[stage];
+          // both CTAs' loads complete on the leader's barrier, which expects the pair's bytes
+          if (rank == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
+          const uint32_t pair_bar = CG == 2 ? map_rank(bar, 0) : 0;
+          auto load = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
+            if constexpr (CG == 2)
+              tma_load_2d_pair(dst, m, pair_bar, c0, c1);
+            else
+              tma_load_2d(dst, m, bar, c0, c1);
+          };
+          if constexpr (TWO) {
+            const int k = kb * KE, n0 = tl.n * BNO;
+            load(sa, &tmA0, k, m0);
+            if constexpr (CG == 2) {  // CTA 0 brings the gate's rows, CTA 1 the other projection's
+              load(sb, rank == 0 ? &tmB0 : &tmB1, k, n0);
+            } else {
+              load(sb, &tmB0, k, n0);
+              load(sb + BNO * kKBytes, &tmB1, k, n0);
+            }
+          } else if constexpr (MODE == GLU_DX) {
+            const bool second = kb >= args.k_half;
+            const int k = (second ? kb - args.k_half : kb) * KE, n0 = tl.n * BNO + rank * C::B_ROWS;
+            load(sa, second ? &tmA1 : &tmA0, k, m0);
+#pragma unroll
+            for (int c = 0; c < C::B_ROWS / 64; ++c)
+              load(sb + c * kMnChunk, second ? &tmB1 : &tmB0, n0 + c * 64, k);
+          } else {
+            const int k = kb * KE, n0 = tl.n * BNO + rank * C::B_ROWS;
+#pragma unroll
+            for (int c = 0; c < kGluRows / 64; ++c) load(sa + c * kMnChunk, tl.z ? &tmA1 : &tmA0, m0 + c * 64, k);
+#pragma unroll
+            for (int c = 0; c < C::B_ROWS / 64; ++c) load(sb + c * kMnChunk, &tmB0, n0 + c * 64, k);
+          }
+          issued_mask |= 1u << stage;
+          issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t idesc = (1u << 4) | (args.bf16_operands ? (1u << 7) | (1u << 10) : 0u) |
+                             ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) | ((uint32_t)(BN >> 3) << 17) |
+                             ((uint32_t)((kGluRows * CG) >> 4) << 24);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        if (!wait_bounded(&acce[acc], acc_phase ^ 1u, wc)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+        for (int kb = 0; kb < num_k; ++kb) {
+          if (!wait_bounded(&full[stage], phase, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + (size_t)stage * C::STAGE), sb = sa + C::A_BYTES;
+          // K-major: 8-row groups 1024 bytes apart, a k-step 32 bytes on; MN-major: chunks of 64
+          // values kMnChunk apart, 8-k groups 1024 bytes apart, a k-step 16 rows of 128 bytes on
+          const uint64_t ad = A_MN ? sdesc(sa, kMnChunk, 1024, kSw128) : sdesc(sa, 16, 1024, kSw128);
+          const uint64_t bd = B_MN ? sdesc(sb, kMnChunk, 1024, kSw128) : sdesc(sb, 16, 1024, kSw128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_cg<CG, F8>(d, ad + (uint32_t)(k * (A_MN ? 2048 : 32) >> 4), bd + (uint32_t)(k * (B_MN ? 2048 : 32) >> 4),
+                            idesc, (kb | k) != 0);
+          mma_issued = true;
+          umma_commit_cg<CG>(&empty[stage]);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_cg<CG>(&accf[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue (8 warps)
+    constexpr int CW = BNO / 2;              // output columns of this warp
+    constexpr int W = CW < 64 ? CW : 64;     // columns stored at a time
+    constexpr int LD = W < 32 ? W : 32;      // columns loaded from tensor memory at a time
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* st = xpose + (warp - 2) * 4096;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], 0) : 0, CG == 2 ? map_rank(&acce[1], 0) : 0};
+    for (int t = unit; t < total; t += units) {
+      const Tile tl = tile_at(t, num_m, num_n);
+      const int m0 = (tl.m * CG + rank) * kGluRows + q * 32, m = m0 + lane;
+      const uint32_t rows = __ballot_sync(0xffffffffu, m < args.M);
+      const bool ok = wait_bounded(&accf[acc], acc_phase, wc);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + half * CW);
+      float sx = 1.0f;
+      if constexpr (F8) sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < CW / W; ++c) {
+        const int n0 = tl.n * BNO + half * CW + c * W;  // first output column
+        const int cols = args.N - n0;
+        const size_t off = (size_t)m0 * args.N + n0;
+        uint4 o[W / 8], o2[W / 8];
+        if constexpr (MODE == GLU_SLOPES) load_cols<W>(st, lane, o2, args.dh + off, args.N, rows, cols);
+#pragma unroll
+        for (int b = 0; b < W / LD; ++b) {
+          float g[LD], u[LD];
+          const uint32_t ta = tb + c * W + b * LD;
+          if constexpr (LD == 32) {
+            tmem_ld32(ta, g);
+            if constexpr (TWO) tmem_ld32(ta + BNO, u);
+          } else {
+            tmem_ld16(ta, g);
+            if constexpr (TWO) tmem_ld16(ta + BNO, u);
+          }
+          tmem_wait_ld();
+          if constexpr (F8) {
+            // columns past the last read the last four scales again (they are not stored)
+#pragma unroll
+            for (int i = 0; i < LD / 4; ++i) {
+              const int n = min(n0 + b * LD + 4 * i, args.N - 4);
+              const float4 a = __ldg(reinterpret_cast<const float4*>(args.g_scale + n));
+              const float4 e = __ldg(reinterpret_cast<const float4*>(args.u_scale + n));
+              g[4 * i] *= sx * a.x, g[4 * i + 1] *= sx * a.y, g[4 * i + 2] *= sx * a.z, g[4 * i + 3] *= sx * a.w;
+              u[4 * i] *= sx * e.x, u[4 * i + 1] *= sx * e.y, u[4 * i + 2] *= sx * e.z, u[4 * i + 3] *= sx * e.w;
+            }
+          }
+          if constexpr (MODE == GLU_FORWARD) {
+#pragma unroll
+            for (int i = 0; i < LD; ++i) g[i] = act_only(g[i], args.act) * u[i];
+            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
+          } else if constexpr (MODE == GLU_SLOPES) {
+#pragma unroll
+            for (int i = 0; i < LD / 8; ++i) {
+              float dh[8];
+              unpack16(o2[b * (LD / 8) + i], dh, args.bf16_out);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                float a, slope;
+                act_and_slope(g[8 * i + e], args.act, a, slope);
+                g[8 * i + e] = dh[e] * u[8 * i + e] * slope;
+                u[8 * i + e] = dh[e] * a;
+              }
+            }
+            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
+            pack16<LD>(u, o2 + b * (LD / 8), args.bf16_out);
+          } else {
+            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
+          }
+        }
+        uint16_t* out = (MODE == GLU_DW && tl.z ? args.out2 : args.out) + off;
+        store_cols<W>(st, lane, o, out, args.N, rows, cols);
+        if constexpr (MODE == GLU_SLOPES) store_cols<W>(st, lane, o2, args.out2 + off, args.N, rows, cols);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(acce_addr[acc]);
+        else
+          mbar_arrive(&acce[acc]);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+
+  // ------------------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // Abort path: let the copies and MMAs in flight land before the shared and tensor memory
+    // are released (bounded as well).  A pair's copies complete on the leader's barriers.
+    const WaitCtl dc{args.status, never_flag, 100000000LL};
+    if (warp == 0 && lane == 0 && rank == 0) {
+      for (int s = 0; s < C::STAGES; ++s)
+        if (issued_mask & (1u << s)) wait_bounded(&full[s], (issued_par >> s) & 1u, dc);
+    }
+    if (warp == 1 && lane == 0 && mma_issued) {
+      umma_commit_cg<CG>(drain);
+      wait_bounded(drain, 0, dc);
+    }
+    __syncthreads();
+  }
+  if constexpr (CG == 2) cluster_sync();  // nothing of the peer reaches this CTA any more
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_cg<CG>(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <int CG, int BN, int MODE, bool F8>
+cudaError_t launch_one(const GluMaps& mp, const GluArgs& a, int num_sms, cudaStream_t s) {
+  using C = GluCfg<CG, BN>;
+  constexpr int BNO = (MODE == GLU_FORWARD || MODE == GLU_SLOPES) ? BN / 2 : BN;
+  const int64_t tiles = (int64_t)((a.M + kGluRows * CG - 1) / (kGluRows * CG)) * ((a.N + BNO - 1) / BNO) *
+                        (MODE == GLU_DW ? 2 : 1);
+  const int units = num_sms / CG;
+  const int grid = (int)(tiles < units ? tiles : units) * CG;
+  if (grid <= 0) return cudaSuccess;
+  return launch_dependent(glu_kernel<CG, BN, MODE, F8>, grid, kGluThreads, C::SMEM, s, mp.a0, mp.a1, mp.b0, mp.b1, a);
+}
+
+template <int CG, int BN, int MODE, bool F8>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(glu_kernel<CG, BN, MODE, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)GluCfg<CG, BN>::SMEM);
+}
+
+}  // namespace
+
+// Every (CTA group, tile width, mode, operand form) that glu_plan gives.
+#define TFL_GLU_VARIANTS(X)                                                            \
+  X(1, 256, GLU_FORWARD, false) X(1, 256, GLU_FORWARD, true) X(1, 256, GLU_SLOPES, false) \
+  X(1, 256, GLU_DX, false) X(1, 256, GLU_DW, false)
+
+cudaError_t prepare_glu_kernels() {
+  cudaError_t e = cudaSuccess;
+#define TFL_PREP(CG, BN, MODE, F8) \
+  if (e == cudaSuccess) e = prepare_one<CG, BN, MODE, F8>();
+  TFL_GLU_VARIANTS(TFL_PREP)
+#undef TFL_PREP
+  return e;
+}
+
+GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int num_sms) { return {1, 256}; }
+
+cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, int num_sms,
+                       cudaStream_t s) {
+#define TFL_LAUNCH(CG, BN, MODE, F8) \
+  if (p.cg == CG && p.bn == BN && mode == MODE && f8 == F8) return launch_one<CG, BN, MODE, F8>(mp, a, num_sms, s);
+  TFL_GLU_VARIANTS(TFL_LAUNCH)
+#undef TFL_LAUNCH
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tfl

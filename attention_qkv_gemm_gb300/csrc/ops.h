@@ -1,5 +1,6 @@
 // ops.h -- argument blocks and host launchers of the operators that stand on their own beside
-// the forward and its attention: the root-mean-square norm (rmsnorm.cu).
+// the forward and its attention: the root-mean-square norm (rmsnorm.cu) and the gated
+// feed-forward (glu.cu).
 #pragma once
 #include "kernels.h"
 #include "tfl.h"
@@ -39,5 +40,39 @@ struct RmsGradArgs {
 constexpr int kRmsMaxRegisterRow = 32768;  // widest row the forward holds in registers (the backward: half)
 cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_rms_backward(const RmsGradArgs& a, cudaStream_t s);
+
+// Gated feed-forward (glu.cu).
+enum GluMode : int {
+  GLU_FORWARD = 0,  // out[M, N] = act(A B0^T) * (A B1^T)
+  GLU_SLOPES = 1,   // out[M, N] = dh u act'(g), out2[M, N] = dh act(g), g = A B0^T, u = A B1^T
+  GLU_DX = 2,       // out[M, N] = A0 B0 + A1 B1
+  GLU_DW = 3,       // out[M, N] = A0^T B0, out2[M, N] = A1^T B0
+};
+struct GluArgs {
+  int M = 0, N = 0;              // rows and columns of the output
+  int num_k = 0;                 // k-blocks of a tile
+  int k_half = 0;                // DX: k-blocks of the first product
+  int act = 0;
+  int bf16_operands = 0;         // 16-bit operands: bf16, else fp16
+  int bf16_out = 0;              // 16-bit outputs (and dh): bf16, else fp16
+  const uint16_t* dh = nullptr;  // SLOPES: [M, N]
+  uint16_t* out = nullptr;
+  uint16_t* out2 = nullptr;
+  const float *x_scale = nullptr, *g_scale = nullptr, *u_scale = nullptr;  // e4m3: [M], [N], [N]
+  int* status = nullptr;
+  int64_t timeout_ns = 2000000000LL;
+};
+constexpr int kGluRows = 128;  // rows of A a CTA takes
+struct GluMaps {
+  CUtensorMap a0, a1, b0, b1;
+};
+// The kernel variant of a call: CTAs that share a tile, accumulator columns of a tile.
+struct GluPlan {
+  int cg, bn;
+};
+GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int num_sms);
+cudaError_t prepare_glu_kernels();
+cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, int num_sms,
+                       cudaStream_t s);
 
 }  // namespace tfl

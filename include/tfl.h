@@ -415,6 +415,62 @@ int tfl_rmsnorm_backward(tfl_rmsnorm* n, int64_t rows, const void* sum, const fl
 /* Free what the handle owns.  Synchronizes the device.  NULL is a no-op. */
 void tfl_rmsnorm_destroy(tfl_rmsnorm* n);
 
+/*
+ * Gated feed-forward block: both projections, the activation and the product
+ *   h = act(x Wg^T) * (x Wu^T)
+ * with Wg, Wu in nn.Linear layout [d_ff, d_model] (one packed [2 d_ff, d_model]
+ * weight is passed as its two halves).  Products accumulate in fp32 and h is
+ * rounded once.
+ *
+ * Operands (x, Wg, Wu): fp16 or bf16, the output's type; or e4m3 with one fp32
+ * scale a row (the stored value times its row's scale is the operand's value,
+ * as tfl_rmsnorm_forward writes x), and an fp16 or bf16 output.
+ */
+#define TFL_ACT_SILU 0   /* z / (1 + e^-z) */
+#define TFL_ACT_GELU 1   /* exact erf form */
+typedef struct tfl_glu tfl_glu;
+
+/* d_model and d_ff: multiples of 8 (16 for e4m3 operands) up to 2^24.
+ * max_grad_tokens: the most tokens tfl_glu_backward will be given (0: no
+ * backward; e4m3 operands have none); the handle holds 4 max_grad_tokens d_ff
+ * bytes of scratch for it.  Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
+int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_type, int32_t act,
+                   int64_t max_grad_tokens, tfl_glu** out);
+
+/*
+ * Asynchronous on `stream`.  Device pointers, 16-byte aligned, row-major and
+ * contiguous; any number of tokens from 0 (nothing is done):
+ *   x [tokens, d_model], wg and wu [d_ff, d_model], h [tokens, d_ff]
+ *   x_scale fp32 [tokens] (4-byte aligned), wg_scale and wu_scale fp32 [d_ff]
+ *   for e4m3 operands, else NULL
+ * h must not overlap an input.  Rows do not affect one another.  Calls on one
+ * handle may overlap.  Errors: INVALID_ARG (also when the current device is not
+ * the handle's), UNSUPPORTED, CUDA; a device-side wait that ran out surfaces
+ * through tfl_glu_status.
+ */
+int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_scale, const void* wg,
+                    const float* wg_scale, const void* wu, const float* wu_scale, void* h, tfl_stream stream);
+
+/*
+ * The gradients, from the forward's inputs (its products are computed again, so
+ * nothing is kept between the two calls) and dh [tokens, d_ff]:
+ *   dg = dh u act'(g),  du = dh act(g),  g = x Wg^T,  u = x Wu^T
+ *   dx = dg Wg + du Wu  [tokens, d_model],  dwg = dg^T x,  dwu = du^T x  [d_ff, d_model]
+ * All of the operands' 16-bit type; dg and du are rounded to it once, sums are
+ * fp32, each gradient is rounded once.  Outputs are written in full (dwg, dwu:
+ * zeros for 0 tokens) and must not overlap anything.  No atomics: the same
+ * inputs give the same bits.  Calls on one handle share its scratch and must not
+ * overlap on the GPU (graphs that hold such calls included).
+ * Errors: INVALID_ARG (also for more than max_grad_tokens), UNSUPPORTED, CUDA.
+ */
+int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, const void* wu, const void* dh,
+                     void* dx, void* dwg, void* dwu, tfl_stream stream);
+
+/* Synchronize `stream`, read and clear the status word: TFL_OK or TFL_ERR_DEVICE_TIMEOUT. */
+int tfl_glu_status(tfl_glu* g, tfl_stream stream);
+
+void tfl_glu_destroy(tfl_glu* g);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,7 +32,33 @@ def test_rmsnorm_create_refuses(lib, args, code):
     assert h.value is None and pkg.tfl_last_error() != ""
 
 
+@pytest.mark.parametrize("args,code", [
+    ((0, 64, 2, 2, 0, 0), pkg.TFL_ERR_INVALID_ARG),
+    ((64, -8, 2, 2, 0, 0), pkg.TFL_ERR_INVALID_ARG),
+    ((64, 64, 2, 2, 2, 0), pkg.TFL_ERR_INVALID_ARG),        # no such activation
+    ((64, 64, 2, 2, 0, -1), pkg.TFL_ERR_INVALID_ARG),
+    ((64, 64, 2, 2, 0, 1 << 31), pkg.TFL_ERR_INVALID_ARG),
+    ((64, 64, 0, 0, 0, 0), pkg.TFL_ERR_UNSUPPORTED),        # fp32
+    ((64, 64, 1, 2, 0, 0), pkg.TFL_ERR_UNSUPPORTED),        # fp16 operands, bf16 output
+    ((64, 64, 3, 3, 0, 0), pkg.TFL_ERR_UNSUPPORTED),        # an e4m3 output
+    ((64, 64, 3, 2, 0, 8), pkg.TFL_ERR_UNSUPPORTED),        # a backward of e4m3 operands
+    ((68, 64, 2, 2, 0, 0), pkg.TFL_ERR_UNSUPPORTED),
+    ((64, 60, 2, 2, 0, 0), pkg.TFL_ERR_UNSUPPORTED),
+    ((72, 64, 3, 2, 0, 0), pkg.TFL_ERR_UNSUPPORTED),        # 16 for e4m3
+    (((1 << 24) + 8, 64, 2, 2, 0, 0), pkg.TFL_ERR_UNSUPPORTED),
+])
+def test_glu_create_refuses(lib, args, code):
+    h = ctypes.c_void_p()
+    assert lib.tfl_glu_create(*args, ctypes.byref(h)) == code
+    assert h.value is None and pkg.tfl_last_error() != ""
+
+
 def test_null_handles_are_refused(lib):
+    assert lib.tfl_glu_create(64, 64, 2, 2, 0, 0, None) == pkg.TFL_ERR_INVALID_ARG
+    assert lib.tfl_glu_forward(None, 1, *[None] * 8) == pkg.TFL_ERR_INVALID_ARG
+    assert lib.tfl_glu_backward(None, 1, *[None] * 8) == pkg.TFL_ERR_INVALID_ARG
+    assert lib.tfl_glu_status(None, None) == pkg.TFL_ERR_INVALID_ARG
+    lib.tfl_glu_destroy(None)  # no-op
     assert lib.tfl_rmsnorm_create(64, 2, 2, 2, 1e-5, None) == pkg.TFL_ERR_INVALID_ARG
     assert lib.tfl_rmsnorm_forward(None, 1, *[None] * 7) == pkg.TFL_ERR_INVALID_ARG
     assert lib.tfl_rmsnorm_backward(None, 1, *[None] * 8) == pkg.TFL_ERR_INVALID_ARG
