@@ -210,7 +210,7 @@ void tfl_rmsnorm_destroy(tfl_rmsnorm* n) {
 struct tfl_glu {
   int D = 0, F = 0, in_type = 0, out_type = 0, act = 0;
   int64_t max_grad_tokens = 0;
-  int device = 0, num_sms = 0;
+  int device = 0, num_sms = 0, pairs = 0;
   int* status = nullptr;                          // status word (256 bytes), then dg and du
   uint16_t *dg = nullptr, *du = nullptr;          // [max_grad_tokens, F]
 };
@@ -270,7 +270,9 @@ int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_t
   int dev = 0, sms = 0;
   if (int rc = usable_device(&dev, &sms)) return rc;
   if (!get_encode()) return fail(TFL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  TFL_CUDA(prepare_glu_kernels(), "feed-forward kernel attributes");
+  int pairs = 0;
+  TFL_CUDA(prepare_glu_kernels(&pairs), "feed-forward kernel attributes");
+  if (pairs < 1) return fail(TFL_ERR_UNSUPPORTED, "the device runs no CTA pairs");
   tfl_glu* g = new (std::nothrow) tfl_glu();
   if (!g) return fail(TFL_ERR_OOM, "handle allocation failed");
   g->D = d_model;
@@ -281,6 +283,7 @@ int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_t
   g->max_grad_tokens = max_grad_tokens;
   g->device = dev;
   g->num_sms = sms;
+  g->pairs = pairs;
   const size_t each = ((size_t)max_grad_tokens * d_ff * 2 + 255) / 256 * 256;
   if (cudaMalloc(&g->status, 256 + 2 * each) != cudaSuccess) {
     cudaGetLastError();
@@ -333,7 +336,8 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   a.g_scale = wg_scale;
   a.u_scale = wu_scale;
   a.out = static_cast<uint16_t*>(h);
-  TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, g->num_sms, static_cast<cudaStream_t>(stream)), "feed-forward");
+  TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, g->num_sms, g->pairs, static_cast<cudaStream_t>(stream)),
+           "feed-forward");
   return TFL_OK;
 }
 
@@ -389,21 +393,21 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.dh = static_cast<const uint16_t*>(dh);
   a.out = g->dg;
   a.out2 = g->du;
-  TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, g->num_sms, st), "feed-forward slopes");
+  TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, g->num_sms, g->pairs, st), "feed-forward slopes");
   a = glu_args(g);
   a.M = Ti;
   a.N = Di;
   a.k_half = (Fi + 63) / 64;
   a.num_k = 2 * a.k_half;
   a.out = static_cast<uint16_t*>(dx);
-  TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, g->num_sms, st), "feed-forward dx");
+  TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, g->num_sms, g->pairs, st), "feed-forward dx");
   a = glu_args(g);
   a.M = Fi;
   a.N = Di;
   a.num_k = (Ti + 63) / 64;
   a.out = static_cast<uint16_t*>(dwg);
   a.out2 = static_cast<uint16_t*>(dwu);
-  TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, g->num_sms, st), "feed-forward weight gradients");
+  TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, g->num_sms, g->pairs, st), "feed-forward weight gradients");
   return TFL_OK;
 }
 

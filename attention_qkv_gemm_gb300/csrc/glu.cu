@@ -428,15 +428,25 @@ __global__ void __launch_bounds__(kGluThreads, 1)
 }
 
 template <int CG, int BN, int MODE, bool F8>
-cudaError_t launch_one(const GluMaps& mp, const GluArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_one(const GluMaps& mp, const GluArgs& a, int units, cudaStream_t s) {
   using C = GluCfg<CG, BN>;
   constexpr int BNO = (MODE == GLU_FORWARD || MODE == GLU_SLOPES) ? BN / 2 : BN;
   const int64_t tiles = (int64_t)((a.M + kGluRows * CG - 1) / (kGluRows * CG)) * ((a.N + BNO - 1) / BNO) *
                         (MODE == GLU_DW ? 2 : 1);
-  const int units = num_sms / CG;
-  const int grid = (int)(tiles < units ? tiles : units) * CG;
-  if (grid <= 0) return cudaSuccess;
-  return launch_dependent(glu_kernel<CG, BN, MODE, F8>, grid, kGluThreads, C::SMEM, s, mp.a0, mp.a1, mp.b0, mp.b1, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles < units ? tiles : units) * CG);
+  cfg.blockDim = dim3(kGluThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CG;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, glu_kernel<CG, BN, MODE, F8>, mp.a0, mp.a1, mp.b0, mp.b1, a);
 }
 
 template <int CG, int BN, int MODE, bool F8>
@@ -448,25 +458,46 @@ cudaError_t prepare_one() {
 }  // namespace
 
 // Every (CTA group, tile width, mode, operand form) that glu_plan gives.
-#define TFL_GLU_VARIANTS(X)                                                            \
-  X(1, 256, GLU_FORWARD, false) X(1, 256, GLU_FORWARD, true) X(1, 256, GLU_SLOPES, false) \
-  X(1, 256, GLU_DX, false) X(1, 256, GLU_DW, false)
+#define TFL_GLU_VARIANTS(X)                                                                  \
+  X(1, 256, GLU_FORWARD, false) X(1, 256, GLU_FORWARD, true) X(1, 256, GLU_SLOPES, false)    \
+  X(1, 256, GLU_DX, false) X(1, 256, GLU_DW, false)                                          \
+  X(2, 256, GLU_FORWARD, false) X(2, 256, GLU_FORWARD, true) X(2, 256, GLU_SLOPES, false)    \
+  X(2, 256, GLU_DX, false) X(2, 256, GLU_DW, false)
 
-cudaError_t prepare_glu_kernels() {
+cudaError_t prepare_glu_kernels(int* pairs) {
   cudaError_t e = cudaSuccess;
 #define TFL_PREP(CG, BN, MODE, F8) \
   if (e == cudaSuccess) e = prepare_one<CG, BN, MODE, F8>();
   TFL_GLU_VARIANTS(TFL_PREP)
 #undef TFL_PREP
-  return e;
+  if (e != cudaSuccess) return e;
+  // CTA pairs the GPU holds at once (a pair stays within a GPU processing cluster): one each
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kGluThreads);
+  cfg.dynamicSmemBytes = GluCfg<2, 256>::SMEM;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 2;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(pairs, glu_kernel<2, 256, GLU_FORWARD, false>, &cfg);
 }
 
-GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int num_sms) { return {1, 256}; }
+// CTA pairs take 256 x 256 tiles: each CTA stages half of B, so a k-block costs 32 KB of shared
+// memory writes and L2 reads a CTA where a lone CTA's 128 x 256 tile costs 48 KB for the same
+// products.
+GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int num_sms) {
+  if (M > kGluRows) return {2, 256};
+  return {1, 256};
+}
 
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, int num_sms,
-                       cudaStream_t s) {
-#define TFL_LAUNCH(CG, BN, MODE, F8) \
-  if (p.cg == CG && p.bn == BN && mode == MODE && f8 == F8) return launch_one<CG, BN, MODE, F8>(mp, a, num_sms, s);
+                       int pairs, cudaStream_t s) {
+#define TFL_LAUNCH(CG, BN, MODE, F8)                       \
+  if (p.cg == CG && p.bn == BN && mode == MODE && f8 == F8) \
+    return launch_one<CG, BN, MODE, F8>(mp, a, CG == 2 ? pairs : num_sms, s);
   TFL_GLU_VARIANTS(TFL_LAUNCH)
 #undef TFL_LAUNCH
   return cudaErrorInvalidValue;

@@ -71,8 +71,9 @@ struct GluPlan {
   int cg, bn;
 };
 GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int num_sms);
-cudaError_t prepare_glu_kernels();
+// Kernel attributes; *pairs: CTA pairs that the current device runs at once.
+cudaError_t prepare_glu_kernels(int* pairs);
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, int num_sms,
-                       cudaStream_t s);
+                       int pairs, cudaStream_t s);
 
 }  // namespace tfl
