@@ -349,6 +349,17 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             if constexpr (TWO) tmem_ld16(ta + BNO, u);
           }
           tmem_wait_ld();
+          if (c == CW / W - 1 && b == W / LD - 1) {
+            // the accumulator is in registers: hand it back before the arithmetic and the stores
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (CG == 2)
+                mbar_arrive_cluster_relaxed(acce_addr[acc]);
+              else
+                mbar_arrive(&acce[acc]);
+            }
+          }
           if constexpr (F8) {
             // columns past the last read the last four scales again (they are not stored)
 #pragma unroll
@@ -386,14 +397,6 @@ __global__ void __launch_bounds__(kGluThreads, 1)
         uint16_t* out = (MODE == GLU_DW && tl.z ? args.out2 : args.out) + off;
         store_cols<W>(st, lane, o, out, args.N, rows, cols);
         if constexpr (MODE == GLU_SLOPES) store_cols<W>(st, lane, o2, args.out2 + off, args.N, rows, cols);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (CG == 2)
-          mbar_arrive_cluster(acce_addr[acc]);
-        else
-          mbar_arrive(&acce[acc]);
       }
       if (++acc == 2) {
         acc = 0;
