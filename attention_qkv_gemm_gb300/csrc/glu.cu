@@ -46,27 +46,64 @@ struct GluCfg {
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + XPOSE_BYTES + 256;
 };
 
-// act(g) and act'(g).  SiLU: g p with p = 1 / (1 + e^-g), slope p (1 + g (1 - p)).  GELU (exact
-// erf form, erf as in gelu_as7126): g Phi(g), slope Phi(g) + g phi(g).
-__device__ __forceinline__ void act_and_slope(float g, int act, float& a, float& slope) {
-  if (act == TFL_ACT_SILU) {
-    const float p = rcp_approx(1.0f + ex2(g * -1.4426950408889634f));
-    a = g * p;
-    slope = p * fmaf(g, 1.0f - p, 1.0f);
+// The activation of a packed pair of fp32 values (FMA-pipe work runs two lanes an instruction;
+// the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
+// a = act(g) and, when wanted, slope = act'(g).
+//   SiLU  p = 1 / (1 + e^-g);  a = g p,  slope = p + p (g - a)
+//   GELU  exact erf form, erf from Abramowitz & Stegun 7.1.26 as in gelu2_as7126:
+//         a = g Phi(g),  slope = Phi(g) + g phi(g)
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ void act2(uint64_t g, uint64_t& a, uint64_t& slope) {
+  if constexpr (ACT == TFL_ACT_SILU) {
+    float e0, e1;
+    f2_unpack(f2_mul(g, f2_splat(-1.4426950408889634f)), e0, e1);
+    f2_unpack(f2_add(f2_pack(ex2(e0), ex2(e1)), f2_splat(1.0f)), e0, e1);
+    const uint64_t p = f2_pack(rcp_approx(e0), rcp_approx(e1));
+    a = f2_mul(g, p);
+    if constexpr (SLOPE) slope = f2_fma(p, f2_sub(g, a), p);
+  } else if constexpr (!SLOPE) {
+    a = gelu2_as7126(g);
   } else {
     constexpr float p_s = 0.3275911f * 0.7071067811865476f;
     constexpr float h1 = 0.5f * 0.254829592f, h2 = 0.5f * -0.284496736f, h3 = 0.5f * 1.421413741f,
                     h4 = 0.5f * -1.453152027f, h5 = 0.5f * 1.061405429f;
-    const float e = ex2((g * g) * -0.7213475204444817f);
-    const float t = rcp_approx(fmaf(p_s, fabsf(g), 1.0f));
-    const float half_erfc = t * fmaf(fmaf(fmaf(fmaf(h5, t, h4), t, h3), t, h2), t, h1) * e;
-    const float cdf = g >= 0.f ? 1.0f - half_erfc : half_erfc;
-    a = g * cdf;
-    slope = fmaf(g * 0.3989422804014327f, e, cdf);
+    float x0, x1, d0, d1;
+    f2_unpack(g, x0, x1);
+    f2_unpack(f2_fma(f2_pack(fabsf(x0), fabsf(x1)), f2_splat(p_s), f2_splat(1.0f)), d0, d1);
+    const uint64_t t = f2_pack(rcp_approx(d0), rcp_approx(d1));
+    uint64_t poly = f2_fma(f2_splat(h5), t, f2_splat(h4));
+    poly = f2_fma(poly, t, f2_splat(h3));
+    poly = f2_fma(poly, t, f2_splat(h2));
+    poly = f2_fma(poly, t, f2_splat(h1));
+    f2_unpack(f2_mul(f2_mul(g, g), f2_splat(-0.7213475204444817f)), d0, d1);
+    const uint64_t e = f2_pack(ex2(d0), ex2(d1));
+    f2_unpack(f2_mul(f2_mul(t, poly), e), d0, d1);  // erfc(|g| / sqrt 2) / 2
+    const uint64_t cdf = f2_pack(x0 >= 0.f ? 1.0f - d0 : d0, x1 >= 0.f ? 1.0f - d1 : d1);
+    a = f2_mul(g, cdf);
+    slope = f2_fma(f2_mul(g, f2_splat(0.3989422804014327f)), e, cdf);
   }
 }
-__device__ __forceinline__ float act_only(float g, int act) {
-  return act == TFL_ACT_SILU ? g * rcp_approx(1.0f + ex2(g * -1.4426950408889634f)) : gelu_as7126(g);
+// N outputs of a row: g <- act(g) u.
+template <int ACT, int N>
+__device__ __forceinline__ void forward_values(float* g, const float* u) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    uint64_t a, unused;
+    act2<ACT, false>(f2_pack(g[i], g[i + 1]), a, unused);
+    f2_unpack(f2_mul(a, f2_pack(u[i], u[i + 1])), g[i], g[i + 1]);
+  }
+}
+// g <- dh u act'(g), u <- dh act(g).
+template <int ACT, int N>
+__device__ __forceinline__ void slope_values(float* g, float* u, const float* dh) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    uint64_t a, slope;
+    act2<ACT, true>(f2_pack(g[i], g[i + 1]), a, slope);
+    const uint64_t d = f2_pack(dh[i], dh[i + 1]);
+    f2_unpack(f2_mul(f2_mul(d, f2_pack(u[i], u[i + 1])), slope), g[i], g[i + 1]);
+    f2_unpack(f2_mul(d, a), u[i], u[i + 1]);
+  }
 }
 
 template <int N>
@@ -273,6 +310,11 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       const uint32_t idesc = (1u << 4) | (args.bf16_operands ? (1u << 7) | (1u << 10) : 0u) |
                              ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) | ((uint32_t)(BN >> 3) << 17) |
                              ((uint32_t)((kGluRows * CG) >> 4) << 24);
+      // K-major: 8-row groups 1024 bytes apart, a k-step 32 bytes on; MN-major: chunks of 64
+      // values kMnChunk apart, 8-k groups 1024 bytes apart, a k-step 16 rows of 128 bytes on
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t ad0 = sdesc(s0, A_MN ? kMnChunk : 16, 1024, kSw128);
+      const uint64_t bd0 = sdesc(s0 + C::A_BYTES, B_MN ? kMnChunk : 16, 1024, kSw128);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -286,15 +328,12 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + (size_t)stage * C::STAGE), sb = sa + C::A_BYTES;
-          // K-major: 8-row groups 1024 bytes apart, a k-step 32 bytes on; MN-major: chunks of 64
-          // values kMnChunk apart, 8-k groups 1024 bytes apart, a k-step 16 rows of 128 bytes on
-          const uint64_t ad = A_MN ? sdesc(sa, kMnChunk, 1024, kSw128) : sdesc(sa, 16, 1024, kSw128);
-          const uint64_t bd = B_MN ? sdesc(sb, kMnChunk, 1024, kSw128) : sdesc(sb, 16, 1024, kSw128);
+          const uint64_t ad = ad0 + (uint32_t)(stage * (C::STAGE >> 4)), bd = bd0 + (uint32_t)(stage * (C::STAGE >> 4));
+          umma_cg<CG, F8>(d, ad, bd, idesc, kb != 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 1; k < 4; ++k)
             umma_cg<CG, F8>(d, ad + (uint32_t)(k * (A_MN ? 2048 : 32) >> 4), bd + (uint32_t)(k * (B_MN ? 2048 : 32) >> 4),
-                            idesc, (kb | k) != 0);
+                            idesc, 1u);
           mma_issued = true;
           umma_commit_cg<CG>(&empty[stage]);
           if (++stage == C::STAGES) {
@@ -372,22 +411,21 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             }
           }
           if constexpr (MODE == GLU_FORWARD) {
-#pragma unroll
-            for (int i = 0; i < LD; ++i) g[i] = act_only(g[i], args.act) * u[i];
+            // the activation is chosen once for all values: a branch at each would keep the
+            // compiler from interleaving their chains
+            if (args.act == TFL_ACT_SILU)
+              forward_values<TFL_ACT_SILU, LD>(g, u);
+            else
+              forward_values<TFL_ACT_GELU, LD>(g, u);
             pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
           } else if constexpr (MODE == GLU_SLOPES) {
+            float dh[LD];
 #pragma unroll
-            for (int i = 0; i < LD / 8; ++i) {
-              float dh[8];
-              unpack16(o2[b * (LD / 8) + i], dh, args.bf16_out);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float a, slope;
-                act_and_slope(g[8 * i + e], args.act, a, slope);
-                g[8 * i + e] = dh[e] * u[8 * i + e] * slope;
-                u[8 * i + e] = dh[e] * a;
-              }
-            }
+            for (int i = 0; i < LD / 8; ++i) unpack16(o2[b * (LD / 8) + i], dh + 8 * i, args.bf16_out);
+            if (args.act == TFL_ACT_SILU)
+              slope_values<TFL_ACT_SILU, LD>(g, u, dh);
+            else
+              slope_values<TFL_ACT_GELU, LD>(g, u, dh);
             pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
             pack16<LD>(u, o2 + b * (LD / 8), args.bf16_out);
           } else {
