@@ -233,7 +233,7 @@ constexpr int kMnBox = 64;  // MN-major operands come in boxes of 64 k rows
 
 int check_tokens(const tfl_glu* g, int64_t tokens) {
   if (tokens < 0 || tokens > INT32_MAX - 512) return fail(TFL_ERR_INVALID_ARG, "tokens must be in 0 .. 2^31 - 513");
-  if ((tokens + 127) / 128 * ((g->F + 31) / 32) > INT32_MAX || (tokens + 127) / 128 * ((g->D + 31) / 32) > INT32_MAX)
+  if ((tokens + 127) / 128 * ((g->F + 15) / 16) > INT32_MAX || (tokens + 127) / 128 * ((g->D + 31) / 32) > INT32_MAX)
     return fail(TFL_ERR_UNSUPPORTED, "too many tokens for this width");
   return TFL_OK;
 }
@@ -321,23 +321,22 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   for (const Span& i : in)
     if (overlap(sh, i, false)) return fail(TFL_ERR_INVALID_ARG, "h overlaps another buffer");
   if (int rc = same_device(g->device)) return rc;
-  const GluPlan p = glu_plan(GLU_FORWARD, f8, tokens, g->F, g->num_sms);
+  const int ke = f8 ? 128 : 64, num_k = (g->D + ke - 1) / ke;
+  const GluPlan p = glu_plan(GLU_FORWARD, f8, tokens, g->F, num_k, g->num_sms, g->pairs);
   GluMaps mp;
-  if (!make_map(&mp.a0, x, tokens, g->D, (int)es, kGluRows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bn / 2) ||
-      !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bn / 2))
+  if (!make_map(&mp.a0, x, tokens, g->D, (int)es, p.a_rows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bno) ||
+      !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bno))
     return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
   mp.a1 = mp.a0;
   GluArgs a = glu_args(g);
   a.M = (int)tokens;
   a.N = g->F;
-  const int ke = f8 ? 128 : 64;
-  a.num_k = (g->D + ke - 1) / ke;
+  a.num_k = num_k;
   a.x_scale = x_scale;
   a.g_scale = wg_scale;
   a.u_scale = wu_scale;
   a.out = static_cast<uint16_t*>(h);
-  TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, g->num_sms, g->pairs, static_cast<cudaStream_t>(stream)),
-           "feed-forward");
+  TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, static_cast<cudaStream_t>(stream)), "feed-forward");
   return TFL_OK;
 }
 
@@ -372,14 +371,15 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
 
   const int Di = g->D, Fi = g->F, Ti = (int)tokens;
-  const GluPlan p1 = glu_plan(GLU_SLOPES, false, tokens, Fi, g->num_sms);
-  const GluPlan p2 = glu_plan(GLU_DX, false, tokens, Di, g->num_sms);
-  const GluPlan p3 = glu_plan(GLU_DW, false, Fi, Di, g->num_sms);
+  const int kd = (Di + 63) / 64, kf = (Fi + 63) / 64, kt = (Ti + 63) / 64;
+  const GluPlan p1 = glu_plan(GLU_SLOPES, false, tokens, Fi, kd, g->num_sms, g->pairs);
+  const GluPlan p2 = glu_plan(GLU_DX, false, tokens, Di, 2 * kf, g->num_sms, g->pairs);
+  const GluPlan p3 = glu_plan(GLU_DW, false, Fi, Di, kt, g->num_sms, g->pairs);
   GluMaps m1, m2, m3;
-  bool ok = make_map(&m1.a0, x, tokens, Di, 2, kGluRows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bn / 2) &&
-            make_map(&m1.b1, wu, Fi, Di, 2, p1.bn / 2);
+  bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bno) &&
+            make_map(&m1.b1, wu, Fi, Di, 2, p1.bno);
   m1.a1 = m1.a0;
-  ok = ok && make_map(&m2.a0, g->dg, tokens, Fi, 2, kGluRows) && make_map(&m2.a1, g->du, tokens, Fi, 2, kGluRows) &&
+  ok = ok && make_map(&m2.a0, g->dg, tokens, Fi, 2, p2.a_rows) && make_map(&m2.a1, g->du, tokens, Fi, 2, p2.a_rows) &&
        make_map(&m2.b0, wg, Fi, Di, 2, kMnBox) && make_map(&m2.b1, wu, Fi, Di, 2, kMnBox);
   ok = ok && make_map(&m3.a0, g->dg, tokens, Fi, 2, kMnBox) && make_map(&m3.a1, g->du, tokens, Fi, 2, kMnBox) &&
        make_map(&m3.b0, x, tokens, Di, 2, kMnBox);
@@ -389,25 +389,25 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   GluArgs a = glu_args(g);
   a.M = Ti;
   a.N = Fi;
-  a.num_k = (Di + 63) / 64;
+  a.num_k = kd;
   a.dh = static_cast<const uint16_t*>(dh);
   a.out = g->dg;
   a.out2 = g->du;
-  TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, g->num_sms, g->pairs, st), "feed-forward slopes");
+  TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, st), "feed-forward slopes");
   a = glu_args(g);
   a.M = Ti;
   a.N = Di;
-  a.k_half = (Fi + 63) / 64;
-  a.num_k = 2 * a.k_half;
+  a.k_half = kf;
+  a.num_k = 2 * kf;
   a.out = static_cast<uint16_t*>(dx);
-  TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, g->num_sms, g->pairs, st), "feed-forward dx");
+  TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, st), "feed-forward dx");
   a = glu_args(g);
   a.M = Fi;
   a.N = Di;
-  a.num_k = (Ti + 63) / 64;
+  a.num_k = kt;
   a.out = static_cast<uint16_t*>(dwg);
   a.out2 = static_cast<uint16_t*>(dwu);
-  TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, g->num_sms, g->pairs, st), "feed-forward weight gradients");
+  TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, st), "feed-forward weight gradients");
   return TFL_OK;
 }
 

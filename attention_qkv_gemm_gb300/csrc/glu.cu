@@ -33,18 +33,11 @@ constexpr int kGluThreads = 64 + 32 * kGluEpiWarps;
 constexpr int kKBytes = 128;       // bytes of k a row and stage
 constexpr int kMnChunk = 64 * 128; // MN-major operands: 64 k rows of 64 values
 
-template <int CG, int BN>
-struct GluCfg {
-  static constexpr int A_BYTES = kGluRows * kKBytes;
-  static constexpr int B_ROWS = BN / CG;  // rows of B this CTA supplies
-  static constexpr int B_BYTES = B_ROWS * kKBytes;
-  static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int XPOSE_BYTES = kGluEpiWarps * 32 * 128;
-  static constexpr int RING_MAX = 232448 - 1024 - XPOSE_BYTES - 256;
-  static constexpr int STAGES = RING_MAX / STAGE > 8 ? 8 : RING_MAX / STAGE;
-  static constexpr int TMEM_COLS = 2 * BN;  // 128, 256 or 512
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + XPOSE_BYTES + 256;
-};
+constexpr int kMaxBN = 256;        // accumulator columns of a tile, at most
+constexpr int kMaxStages = 12;
+constexpr int kXposeBytes = kGluEpiWarps * 32 * 128;  // one 32 x 128 B transpose stage a warp
+constexpr int kRingBytes = 232448 - 1024 - kXposeBytes - 256;
+constexpr size_t kGluSmem = 1024 + kRingBytes + kXposeBytes + 256;
 
 // The activation of a packed pair of fp32 values (FMA-pipe work runs two lanes an instruction;
 // the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
@@ -191,32 +184,38 @@ __device__ __forceinline__ Tile tile_at(int t, int num_m, int num_n) {
   return r;
 }
 
-template <int CG, int BN, int MODE, bool F8>
+// WIDE: tiles of kMaxBN accumulator columns and 128 loaded rows of A, all sizes constants;
+// otherwise the plan's widths.
+template <int CG, int MODE, bool F8, bool WIDE>
 __global__ void __launch_bounds__(kGluThreads, 1)
     glu_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GluArgs args) {
-  using C = GluCfg<CG, BN>;
   constexpr bool TWO = MODE == GLU_FORWARD || MODE == GLU_SLOPES;  // two products side by side
-  constexpr int BNO = TWO ? BN / 2 : BN;                           // output columns a tile
   constexpr bool A_MN = MODE == GLU_DW, B_MN = MODE == GLU_DX || MODE == GLU_DW;
   constexpr int KE = F8 ? 128 : 64;                                // k elements a stage
   extern __shared__ uint8_t smem_raw[];
   grid_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* xpose = smem + (size_t)C::STAGES * C::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + C::XPOSE_BYTES);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* accf = empty + C::STAGES;
+  uint8_t* xpose = smem + kRingBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + kXposeBytes);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* accf = empty + kMaxStages;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* never_flag = abort_flag + 1;  // stays 0: lets the drain waits ignore abort_flag
 
+  constexpr int kWideStage = (kGluRows + kMaxBN / CG) * kKBytes;
+  const int bno = WIDE ? (TWO ? kMaxBN / 2 : kMaxBN) : args.bno;  // output columns of a tile
+  const int bn = TWO ? 2 * bno : bno;                             // accumulator columns
+  const int stages = WIDE ? kRingBytes / kWideStage : args.stages;
+  const int stage_bytes = WIDE ? kWideStage : args.stage_bytes;
+  const int a_bytes = WIDE ? kGluRows * kKBytes : args.a_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = CG == 2 ? (int)cluster_rank() : 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     tma_prefetch_desc(&tmA0);
     tma_prefetch_desc(&tmB0);
   }
-  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, C::TMEM_COLS);
+  if (warp == 1) tmem_alloc_cg<CG>(tmem_slot, 2 * kMaxBN);
   tc_fence_before();
   __syncthreads();
   if constexpr (CG == 2) cluster_sync();  // the peer's barriers exist before anything reaches them
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
   const WaitCtl wc{args.status, abort_flag, args.timeout_ns};
   grid_wait_prior();  // everything below reads or writes what earlier kernels use
 
-  const int num_m = (args.M + kGluRows * CG - 1) / (kGluRows * CG), num_n = (args.N + BNO - 1) / BNO;
+  const int num_m = (args.M + kGluRows * CG - 1) / (kGluRows * CG), num_n = (args.N + bno - 1) / bno;
   const int total = num_m * num_n * (MODE == GLU_DW ? 2 : 1);
   const int unit = blockIdx.x / CG, units = gridDim.x / CG;
   const int num_k = args.num_k;
@@ -250,6 +249,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      const int mn_chunks = (bn / CG + 63) / 64;  // MN-major B: 64-column boxes of this CTA
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -261,11 +261,11 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             ok = false;
             break;
           }
-          uint8_t* sa = smem + (size_t)stage * C::STAGE;
-          uint8_t* sb = sa + C::A_BYTES;
+          uint8_t* sa = smem + (size_t)stage * stage_bytes;
+          uint8_t* sb = sa + a_bytes;
           uint64_t* bar = &full[stage];
           // both CTAs' loads complete on the leader's barrier, which expects the pair's bytes
-          if (rank == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
+          if (rank == 0) mbar_arrive_expect_tx(bar, CG * stage_bytes);
           const uint32_t pair_bar = CG == 2 ? map_rank(bar, 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
             if constexpr (CG == 2)
@@ -274,31 +274,29 @@ __global__ void __launch_bounds__(kGluThreads, 1)
               tma_load_2d(dst, m, bar, c0, c1);
           };
           if constexpr (TWO) {
-            const int k = kb * KE, n0 = tl.n * BNO;
+            const int k = kb * KE, n0 = tl.n * bno;
             load(sa, &tmA0, k, m0);
             if constexpr (CG == 2) {  // CTA 0 brings the gate's rows, CTA 1 the other projection's
               load(sb, rank == 0 ? &tmB0 : &tmB1, k, n0);
             } else {
               load(sb, &tmB0, k, n0);
-              load(sb + BNO * kKBytes, &tmB1, k, n0);
+              load(sb + bno * kKBytes, &tmB1, k, n0);
             }
           } else if constexpr (MODE == GLU_DX) {
             const bool second = kb >= args.k_half;
-            const int k = (second ? kb - args.k_half : kb) * KE, n0 = tl.n * BNO + rank * C::B_ROWS;
+            const int k = (second ? kb - args.k_half : kb) * KE, n0 = tl.n * bno + rank * (bn / CG);
             load(sa, second ? &tmA1 : &tmA0, k, m0);
-#pragma unroll
-            for (int c = 0; c < C::B_ROWS / 64; ++c)
+            for (int c = 0; c < mn_chunks; ++c)
               load(sb + c * kMnChunk, second ? &tmB1 : &tmB0, n0 + c * 64, k);
           } else {
-            const int k = kb * KE, n0 = tl.n * BNO + rank * C::B_ROWS;
+            const int k = kb * KE, n0 = tl.n * bno + rank * (bn / CG);
 #pragma unroll
             for (int c = 0; c < kGluRows / 64; ++c) load(sa + c * kMnChunk, tl.z ? &tmA1 : &tmA0, m0 + c * 64, k);
-#pragma unroll
-            for (int c = 0; c < C::B_ROWS / 64; ++c) load(sb + c * kMnChunk, &tmB0, n0 + c * 64, k);
+            for (int c = 0; c < mn_chunks; ++c) load(sb + c * kMnChunk, &tmB0, n0 + c * 64, k);
           }
           issued_mask |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-          if (++stage == C::STAGES) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -308,27 +306,28 @@ __global__ void __launch_bounds__(kGluThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = (1u << 4) | (args.bf16_operands ? (1u << 7) | (1u << 10) : 0u) |
-                             ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) | ((uint32_t)(BN >> 3) << 17) |
+                             ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) | ((uint32_t)(bn >> 3) << 17) |
                              ((uint32_t)((kGluRows * CG) >> 4) << 24);
       // K-major: 8-row groups 1024 bytes apart, a k-step 32 bytes on; MN-major: chunks of 64
       // values kMnChunk apart, 8-k groups 1024 bytes apart, a k-step 16 rows of 128 bytes on
       const uint32_t s0 = smem_u32(smem);
       const uint64_t ad0 = sdesc(s0, A_MN ? kMnChunk : 16, 1024, kSw128);
-      const uint64_t bd0 = sdesc(s0 + C::A_BYTES, B_MN ? kMnChunk : 16, 1024, kSw128);
+      const uint64_t bd0 = sdesc(s0 + a_bytes, B_MN ? kMnChunk : 16, 1024, kSw128);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         if (!wait_bounded(&acce[acc], acc_phase ^ 1u, wc)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc * BN);
+        const uint32_t d = tmem_base + (uint32_t)(acc * kMaxBN);
         for (int kb = 0; kb < num_k; ++kb) {
           if (!wait_bounded(&full[stage], phase, wc)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = ad0 + (uint32_t)(stage * (C::STAGE >> 4)), bd = bd0 + (uint32_t)(stage * (C::STAGE >> 4));
+          const uint32_t at = (uint32_t)(stage * (stage_bytes >> 4));
+          const uint64_t ad = ad0 + at, bd = bd0 + at;
           umma_cg<CG, F8>(d, ad, bd, idesc, kb != 0);
 #pragma unroll
           for (int k = 1; k < 4; ++k)
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
                             idesc, 1u);
           mma_issued = true;
           umma_commit_cg<CG>(&empty[stage]);
-          if (++stage == C::STAGES) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -351,9 +350,8 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue (8 warps)
-    constexpr int CW = BNO / 2;              // output columns of this warp
-    constexpr int W = CW < 64 ? CW : 64;     // columns stored at a time
-    constexpr int LD = W < 32 ? W : 32;      // columns loaded from tensor memory at a time
+    constexpr int W = WIDE ? 64 : 32;  // columns stored at a time; the two warps of a lane quarter take turns
+    constexpr int LD = 32;             // columns computed at a time
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* st = xpose + (warp - 2) * 4096;
     int acc = 0;
@@ -366,39 +364,38 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       const bool ok = wait_bounded(&accf[acc], acc_phase, wc);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * BN + half * CW);
+      const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxBN);
       float sx = 1.0f;
       if constexpr (F8) sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
+      const int chunks = (bno + W - 1) / W;
+      const int last = chunks - 1 - ((chunks - 1 - half) & 1);  // this warp's last chunk (< 0: it has none)
+      auto hand_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2)
+            mbar_arrive_cluster_relaxed(acce_addr[acc]);
+          else
+            mbar_arrive(&acce[acc]);
+        }
+      };
+      if (half > last) hand_back();
 #pragma unroll 1
-      for (int c = 0; c < CW / W; ++c) {
-        const int n0 = tl.n * BNO + half * CW + c * W;  // first output column
-        const int cols = args.N - n0;
+      for (int c = half; c < chunks; c += 2) {
+        const int n0 = tl.n * bno + c * W;                   // first output column
+        const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
         const size_t off = (size_t)m0 * args.N + n0;
         uint4 o[W / 8], o2[W / 8];
         if constexpr (MODE == GLU_SLOPES) load_cols<W>(st, lane, o2, args.dh + off, args.N, rows, cols);
 #pragma unroll
         for (int b = 0; b < W / LD; ++b) {
+          const int col = c * W + b * LD;
           float g[LD], u[LD];
-          const uint32_t ta = tb + c * W + b * LD;
-          if constexpr (LD == 32) {
-            tmem_ld32(ta, g);
-            if constexpr (TWO) tmem_ld32(ta + BNO, u);
-          } else {
-            tmem_ld16(ta, g);
-            if constexpr (TWO) tmem_ld16(ta + BNO, u);
-          }
+          tmem_ld32(tb + col, g);
+          if constexpr (TWO) tmem_ld32(tb + bno + col, u);
           tmem_wait_ld();
-          if (c == CW / W - 1 && b == W / LD - 1) {
-            // the accumulator is in registers: hand it back before the arithmetic and the stores
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (CG == 2)
-                mbar_arrive_cluster_relaxed(acce_addr[acc]);
-              else
-                mbar_arrive(&acce[acc]);
-            }
-          }
+          // once the accumulator is in registers it is handed back, before arithmetic and stores
+          if (b == W / LD - 1 && c == last) hand_back();
           if constexpr (F8) {
             // columns past the last read the last four scales again (they are not stored)
 #pragma unroll
@@ -417,7 +414,6 @@ __global__ void __launch_bounds__(kGluThreads, 1)
               forward_values<TFL_ACT_SILU, LD>(g, u);
             else
               forward_values<TFL_ACT_GELU, LD>(g, u);
-            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
           } else if constexpr (MODE == GLU_SLOPES) {
             float dh[LD];
 #pragma unroll
@@ -426,11 +422,9 @@ __global__ void __launch_bounds__(kGluThreads, 1)
               slope_values<TFL_ACT_SILU, LD>(g, u, dh);
             else
               slope_values<TFL_ACT_GELU, LD>(g, u, dh);
-            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
             pack16<LD>(u, o2 + b * (LD / 8), args.bf16_out);
-          } else {
-            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
           }
+          pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
         }
         uint16_t* out = (MODE == GLU_DW && tl.z ? args.out2 : args.out) + off;
         store_cols<W>(st, lane, o, out, args.N, rows, cols);
@@ -452,7 +446,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     // are released (bounded as well).  A pair's copies complete on the leader's barriers.
     const WaitCtl dc{args.status, never_flag, 100000000LL};
     if (warp == 0 && lane == 0 && rank == 0) {
-      for (int s = 0; s < C::STAGES; ++s)
+      for (int s = 0; s < stages; ++s)
         if (issued_mask & (1u << s)) wait_bounded(&full[s], (issued_par >> s) & 1u, dc);
     }
     if (warp == 1 && lane == 0 && mma_issued) {
@@ -464,20 +458,23 @@ __global__ void __launch_bounds__(kGluThreads, 1)
   if constexpr (CG == 2) cluster_sync();  // nothing of the peer reaches this CTA any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_cg<CG>(tmem_base, C::TMEM_COLS);
+    tmem_dealloc_cg<CG>(tmem_base, 2 * kMaxBN);
   }
 }
 
-template <int CG, int BN, int MODE, bool F8>
-cudaError_t launch_one(const GluMaps& mp, const GluArgs& a, int units, cudaStream_t s) {
-  using C = GluCfg<CG, BN>;
-  constexpr int BNO = (MODE == GLU_FORWARD || MODE == GLU_SLOPES) ? BN / 2 : BN;
-  const int64_t tiles = (int64_t)((a.M + kGluRows * CG - 1) / (kGluRows * CG)) * ((a.N + BNO - 1) / BNO) *
-                        (MODE == GLU_DW ? 2 : 1);
+template <int CG, int MODE, bool F8, bool WIDE>
+cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStream_t s) {
+  a.bno = p.bno;
+  const int bn = (MODE == GLU_FORWARD || MODE == GLU_SLOPES) ? 2 * p.bno : p.bno;
+  const bool b_mn = MODE == GLU_DX || MODE == GLU_DW;
+  a.a_bytes = p.a_rows * kKBytes;
+  a.stage_bytes = a.a_bytes + (b_mn ? (bn / CG + 63) / 64 * kMnChunk : bn / CG * kKBytes);
+  a.stages = kRingBytes / a.stage_bytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles < units ? tiles : units) * CG);
+  cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * CG);
   cfg.blockDim = dim3(kGluThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = kGluSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -487,28 +484,30 @@ cudaError_t launch_one(const GluMaps& mp, const GluArgs& a, int units, cudaStrea
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, glu_kernel<CG, BN, MODE, F8>, mp.a0, mp.a1, mp.b0, mp.b1, a);
+  return cudaLaunchKernelEx(&cfg, glu_kernel<CG, MODE, F8, WIDE>, mp.a0, mp.a1, mp.b0, mp.b1, a);
 }
 
-template <int CG, int BN, int MODE, bool F8>
+template <int CG, int MODE, bool F8>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(glu_kernel<CG, BN, MODE, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)GluCfg<CG, BN>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(glu_kernel<CG, MODE, F8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)kGluSmem);
+  if (CG == 2 && e == cudaSuccess)
+    e = cudaFuncSetAttribute(glu_kernel<2, MODE, F8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGluSmem);
+  return e;
 }
 
 }  // namespace
 
-// Every (CTA group, tile width, mode, operand form) that glu_plan gives.
-#define TFL_GLU_VARIANTS(X)                                                                  \
-  X(1, 256, GLU_FORWARD, false) X(1, 256, GLU_FORWARD, true) X(1, 256, GLU_SLOPES, false)    \
-  X(1, 256, GLU_DX, false) X(1, 256, GLU_DW, false)                                          \
-  X(2, 256, GLU_FORWARD, false) X(2, 256, GLU_FORWARD, true) X(2, 256, GLU_SLOPES, false)    \
-  X(2, 256, GLU_DX, false) X(2, 256, GLU_DW, false)
+// Every (CTA group, mode, operand form); pairs also in the WIDE form.
+#define TFL_GLU_VARIANTS(X)                                                                         \
+  X(1, GLU_FORWARD, false) X(1, GLU_FORWARD, true) X(1, GLU_SLOPES, false) X(1, GLU_DX, false)      \
+  X(1, GLU_DW, false) X(2, GLU_FORWARD, false) X(2, GLU_FORWARD, true) X(2, GLU_SLOPES, false)      \
+  X(2, GLU_DX, false) X(2, GLU_DW, false)
 
 cudaError_t prepare_glu_kernels(int* pairs) {
   cudaError_t e = cudaSuccess;
-#define TFL_PREP(CG, BN, MODE, F8) \
-  if (e == cudaSuccess) e = prepare_one<CG, BN, MODE, F8>();
+#define TFL_PREP(CG, MODE, F8) \
+  if (e == cudaSuccess) e = prepare_one<CG, MODE, F8>();
   TFL_GLU_VARIANTS(TFL_PREP)
 #undef TFL_PREP
   if (e != cudaSuccess) return e;
@@ -516,29 +515,60 @@ cudaError_t prepare_glu_kernels(int* pairs) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(kGluThreads);
-  cfg.dynamicSmemBytes = GluCfg<2, 256>::SMEM;
+  cfg.dynamicSmemBytes = kGluSmem;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = 2;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, glu_kernel<2, 256, GLU_FORWARD, false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(pairs, glu_kernel<2, GLU_FORWARD, false, true>, &cfg);
 }
 
-// CTA pairs take 256 x 256 tiles: each CTA stages half of B, so a k-block costs 32 KB of shared
-// memory writes and L2 reads a CTA where a lone CTA's 128 x 256 tile costs 48 KB for the same
-// products.
-GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int num_sms) {
-  if (M > kGluRows) return {2, 256};
-  return {1, 256};
+// CTA pairs take tiles of 256 rows: each CTA stages half of B, so a k-block of a 256 x 256 tile
+// costs 32 KB of shared-memory writes and L2 reads a CTA where a lone CTA's 128 x 256 tile costs
+// 48 KB for the same products.
+//
+// Fewer than 128 rows of A: only those (to the next 8) are loaded and given room in the ring; the
+// MMA still reads 128, the others being whatever lies behind, and their results are not stored.
+//
+// The tile's width goes by rounds: a launch takes ceil(tiles / units) of them, each about as
+// long as a k-block's products (a 256-column accumulator: 555 cycles measured) or its operand
+// stream from L2 (62 bytes a cycle and SM measured), whichever is longer, and narrower tiles
+// can trade a mostly empty last round for a little more of either.
+GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, int num_sms, int pairs) {
+  const bool two = mode == GLU_FORWARD || mode == GLU_SLOPES;
+  GluPlan best;
+  double best_cost = 0;
+  for (int cg = M > kGluRows ? 2 : 1; cg >= 1; --cg) {
+    const int64_t units = cg == 2 ? pairs : num_sms, num_m = (M + kGluRows * cg - 1) / (kGluRows * cg);
+    const int64_t rows = M < kGluRows ? M : kGluRows;  // rows of A outside the matrix cost no reads
+    // tcgen05.mma takes N in steps of 16, a pair's in steps of 32
+    for (int bn = kMaxBN; bn >= 32; bn -= 16 * cg) {
+      const int bno = two ? bn / 2 : bn;
+      const int64_t tiles = num_m * ((N + bno - 1) / bno) * (mode == GLU_DW ? 2 : 1);
+      const int64_t rounds = (tiles + units - 1) / units;
+      const double products = 555.0 * bn / kMaxBN / (f8 ? 2 : 1);
+      const double stream = (double)(rows + bn / cg) * kKBytes / 62.0;
+      const double cost = rounds * (num_k * (products > stream ? products : stream) + 1500.0);
+      if (!best.cg || cost < best_cost * 0.97) {
+        best.cg = cg;
+        best.a_rows = M < kGluRows && mode != GLU_DW ? (int)((M + 7) / 8 * 8) : kGluRows;
+        best.bno = bno;
+        best.units = (int)units;
+        best.tiles = tiles;
+        best_cost = cost;
+      }
+    }
+  }
+  return best;
 }
 
-cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, int num_sms,
-                       int pairs, cudaStream_t s) {
-#define TFL_LAUNCH(CG, BN, MODE, F8)                       \
-  if (p.cg == CG && p.bn == BN && mode == MODE && f8 == F8) \
-    return launch_one<CG, BN, MODE, F8>(mp, a, CG == 2 ? pairs : num_sms, s);
+cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s) {
+  const bool wide = p.bno == (mode == GLU_FORWARD || mode == GLU_SLOPES ? kMaxBN / 2 : kMaxBN);
+#define TFL_LAUNCH(CG, MODE, F8)                               \
+  if (p.cg == CG && mode == MODE && f8 == F8)                  \
+    return CG == 2 && wide ? launch_one<CG, MODE, F8, CG == 2>(mp, a, p, s) : launch_one<CG, MODE, F8, false>(mp, a, p, s);
   TFL_GLU_VARIANTS(TFL_LAUNCH)
 #undef TFL_LAUNCH
   return cudaErrorInvalidValue;
