@@ -24,8 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
-SOURCES = ["gemm.cu", "attention.cu", "attention_bwd.cu", "postchain.cu", "stack.cu", "rows.cu", "rmsnorm.cu", "glu.cu",
-           "api.cu", "api_ops.cu"]
+SOURCES = ["gemm.cu", "attention.cu", "attention_bwd.cu", "postchain.cu", "stack.cu", "rows.cu", "rmsnorm.cu",
+           "glu.cu", "glu_few.cu", "api.cu", "api_ops.cu"]
 
 # The attention kernels that run two CTAs of 256 threads per SM move registers from their first
 # warpgroup to the second with setmaxnreg (64 and 192 a thread).  That balances only when the

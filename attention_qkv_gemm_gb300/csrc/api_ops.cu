@@ -321,6 +321,23 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   for (const Span& i : in)
     if (overlap(sh, i, false)) return fail(TFL_ERR_INVALID_ARG, "h overlaps another buffer");
   if (int rc = same_device(g->device)) return rc;
+  if (glu_few_fits(tokens, (int64_t)g->D * (int64_t)es)) {
+    GluFewArgs a;
+    a.tokens = (int)tokens;
+    a.d_ff = g->F;
+    a.row_bytes = g->D * (int)es;
+    a.act = g->act;
+    a.bf16_out = g->out_type == TFL_BF16;
+    a.x = static_cast<const uint8_t*>(x);
+    a.wg = static_cast<const uint8_t*>(wg);
+    a.wu = static_cast<const uint8_t*>(wu);
+    a.x_scale = x_scale;
+    a.g_scale = wg_scale;
+    a.u_scale = wu_scale;
+    a.out = static_cast<uint16_t*>(h);
+    TFL_CUDA(launch_glu_few(g->in_type, a, g->num_sms, static_cast<cudaStream_t>(stream)), "feed-forward");
+    return TFL_OK;
+  }
   const int ke = f8 ? 128 : 64, num_k = (g->D + ke - 1) / ke;
   const GluPlan p = glu_plan(GLU_FORWARD, f8, tokens, g->F, num_k, g->num_sms, g->pairs);
   GluMaps mp;

@@ -78,4 +78,17 @@ GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, int num
 cudaError_t prepare_glu_kernels(int* pairs);
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s);
 
+// The forward for at most kGluFewTokens tokens (glu_few.cu).
+constexpr int kGluFewTokens = 16;
+struct GluFewArgs {
+  int tokens = 0, d_ff = 0;
+  int row_bytes = 0;             // of x, Wg and Wu: d_model elements
+  int act = 0, bf16_out = 0;
+  const uint8_t *x = nullptr, *wg = nullptr, *wu = nullptr;
+  const float *x_scale = nullptr, *g_scale = nullptr, *u_scale = nullptr;  // e4m3
+  uint16_t* out = nullptr;
+};
+bool glu_few_fits(int64_t tokens, int64_t row_bytes);  // whether this kernel is the faster one
+cudaError_t launch_glu_few(int type, const GluFewArgs& a, int num_sms, cudaStream_t s);
+
 }  // namespace tfl
