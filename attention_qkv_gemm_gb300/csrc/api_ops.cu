@@ -192,7 +192,7 @@ int tfl_rmsnorm_backward(tfl_rmsnorm* n, int64_t rows, const void* sum, const fl
   a.dgamma = dgamma;
   a.partial = n->partial;
   a.blocks = n->blocks;
-  TFL_CUDA(launch_rms_backward(a, st), "norm backward");
+  TFL_CUDA(launch_rms_backward(a, n->num_sms, st), "norm backward");
   return TFL_OK;
 }
 

@@ -39,7 +39,7 @@ struct RmsGradArgs {
 };
 constexpr int kRmsMaxRegisterRow = 32768;  // widest row the forward holds in registers (the backward: half)
 cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s);
-cudaError_t launch_rms_backward(const RmsGradArgs& a, cudaStream_t s);
+cudaError_t launch_rms_backward(const RmsGradArgs& a, int num_sms, cudaStream_t s);
 
 // Gated feed-forward (glu.cu).
 enum GluMode : int {

@@ -14,7 +14,7 @@
 // rounds once; max|y| = r max|s gamma| comes from the same pass as the sum of squares.
 //
 // Widths that 8 does not divide, unaligned buffers and rows too long for registers take the
-// element-wise kernels at the end: two passes over a row, the second from L1 / L2.
+// element-wise kernels at the end.
 #include "ops.h"
 #include "ptx.cuh"
 #include "xpose.cuh"
@@ -37,28 +37,67 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// ---- 8 consecutive values <-> fp32
-__device__ __forceinline__ void load8(const float* p, float* v) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// ---- 8 consecutive values as loaded, and as fp32
+template <class T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ void load_raw(const T* p, Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
 }
-__device__ __forceinline__ void load8(const __half* p, float* v) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+template <class T>
+__device__ __forceinline__ void zero_raw(Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void widen(const Raw8<float>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.w[i].x), v[4 * i + 1] = __uint_as_float(r.w[i].y);
+    v[4 * i + 2] = __uint_as_float(r.w[i].z), v[4 * i + 3] = __uint_as_float(r.w[i].w);
+  }
+}
+__device__ __forceinline__ void widen(const Raw8<__half>& r, float* v) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
     v[2 * i] = f.x, v[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* v) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ void widen(const Raw8<__nv_bfloat16>& r, float* v) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  Raw8<T> r;
+  load_raw(p, r);
+  widen(r, v);
+}
+// The same as four packed pairs.
+template <class T>
+__device__ __forceinline__ void widen2(const Raw8<T>& r, uint64_t* v) {
+  float f[8];
+  widen(r, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void load_gamma(const float* p, float* v) {  // read by every row: from L1
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void gamma2(const float* p, uint64_t* v) {
+  float f[8];
+  load_gamma(p, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2_pack(f[2 * i], f[2 * i + 1]);
 }
 __device__ __forceinline__ void store8(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -163,7 +202,7 @@ __global__ void __launch_bounds__(1024) rms_forward_kernel(const RmsArgs a) {
     const int c = t + j * tpr;
     if (live && c < nvec) {
       float g[8];
-      load8(a.gamma + c * 8, g);
+      load_gamma(a.gamma + c * 8, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         s[j][i] *= g[i];
@@ -189,91 +228,184 @@ __global__ void __launch_bounds__(1024) rms_forward_kernel(const RmsArgs a) {
   }
 }
 
-// Backward.  A block keeps its row groups over all their rows (grid-stride), so each thread
-// sums dgamma of its own columns in registers; the groups of a block are joined in shared
-// memory and every block writes one row of partial sums, which rms_dgamma_kernel adds in
-// block order: the result depends on the sizes and the SM count only, not on timing.
-template <class X, class R, int NV>
-__global__ void __launch_bounds__(512) rms_backward_kernel(const RmsGradArgs a) {
-  __shared__ float red[64];
+// Both sums of a row, for a group that loops over its rows on its own: groups wider than a warp
+// meet at a named barrier of their own, once a row (the buffers alternate).  Inside a warp the two
+// sums are folded into one first: half of the lanes go on with each.
+__device__ __forceinline__ void row_sums(float& a, float& b, int tpr, int group, int parity, float2 (*red)[32]) {
+  const int lane = threadIdx.x & 31;
+  const int lanes = tpr < 32 ? tpr : 32;
+  if (lanes > 1) {
+    const int h = lanes >> 1;
+    const bool upper = (lane & h) != 0;
+    float v = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, h);
+#pragma unroll
+    for (int o = 8; o; o >>= 1)
+      if (o < h) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const float w = __shfl_xor_sync(0xffffffffu, v, h);
+    a = upper ? w : v;
+    b = upper ? v : w;
+  }
+  if (tpr <= 32) return;
+  const int warp = threadIdx.x >> 5, nw = tpr >> 5;
+  if (lane == 0) red[parity][warp] = make_float2(a, b);
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+  const float2 p = red[parity][group * nw + (lane & (nw - 1))];
+  a = p.x;
+  b = p.y;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    if (o < nw) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+  }
+}
+
+// Backward.  A row group keeps its columns over all its rows, so each thread holds gamma and sums
+// dgamma of its own columns in registers; the groups of a block are joined in shared memory and
+// every block writes one row of partial sums, which rms_dgamma_kernel adds in block order: the
+// result depends on the sizes and the SM count only, not on timing.
+//
+// Three streams in and one or two out bound it, so loads have to stay in flight while a row is
+// reduced and written: the next row is loaded, as stored, before the current one is worked on
+// (20011 x 4096 fp16 229 -> 150 us), and the arithmetic runs on packed fp32 pairs.  A ring of rows
+// in shared memory filled by cp.async holds more bytes in flight but was slower: 161 us, and 39
+// against 28 us at 8192 x 1024.
+template <class X, class R, int NV, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const RmsGradArgs a) {
+  constexpr bool AHEAD = NV == 1 || (NV == 2 && sizeof(R) == 2);  // room for the next row
+  constexpr bool KEEP = NV == 1;                                  // room for gamma
+  __shared__ float2 red[2][32];
   extern __shared__ float part[];  // [groups][D] when the block has more than one group
   grid_launch_dependents();
   grid_wait_prior();
-  const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
-  const int nvec = a.D >> 3;
-  float dg[NV][8];
+  const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr;
+  const int nvec = a.D >> 3, rows = (int)a.rows;
+  const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
+  bool in[NV];  // vectors of this thread that exist
+  uint64_t dg[NV][4], gk[KEEP ? NV : 1][4];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    in[j] = t + j * tpr < nvec;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dg[j][i] = 0.f;
-  for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += (int64_t)gridDim.x * groups) {
-    const int64_t row = row0 + group;
-    const bool live = row < a.rows;
-    const size_t base = (size_t)row * a.D;
-    float s[NV][8], dy[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = t + j * tpr;
-      if (live && c < nvec) {
-        load8(static_cast<const R*>(a.sum) + base + c * 8, s[j]);
-        load8(static_cast<const X*>(a.dy) + base + c * 8, dy[j]);
+    for (int i = 0; i < 4; ++i) dg[j][i] = 0;  // two zeros
+    if constexpr (KEEP) {
+      if (in[j]) {
+        gamma2(a.gamma + (t + j * tpr) * 8, gk[j]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[j][i] = dy[j][i] = 0.f;
-      }
-    }
-    float v[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = t + j * tpr;
-      if (c < nvec) {
-        float g[8];
-        load8(a.gamma + c * 8, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[0] = fmaf(s[j][i], s[j][i], v[0]);
-          v[1] = fmaf(dy[j][i] * g[i], s[j][i], v[1]);
-        }
-      }
-    }
-    group_reduce<2>(v, tpr, false, red);
-    const float r = rsqrtf(v[0] * a.inv_d + a.eps);
-    const float k = r * r * r * (v[1] * a.inv_d);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = t + j * tpr;
-      if (live && c < nvec) {
-        float g[8], o[8];
-        load8(a.gamma + c * 8, g);
-        if (a.dres) {
-          load8(static_cast<const R*>(a.dres) + base + c * 8, o);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dg[j][i] = fmaf(dy[j][i] * r, s[j][i], dg[j][i]);
-          o[i] += fmaf(r * g[i], dy[j][i], -s[j][i] * k);
-        }
-        if (a.dsum) store8(static_cast<R*>(a.dsum) + base + c * 8, o);
-        if (a.dx) store8(static_cast<X*>(a.dx) + base + c * 8, o);
+        for (int i = 0; i < 4; ++i) gk[j][i] = 0;
       }
     }
   }
+  // this thread's first vector of the row to load next and of the row to write next
+  const size_t step = (size_t)stride * a.D, begin = (size_t)first * a.D + t * 8;
+  const R* sp = static_cast<const R*>(a.sum) + begin;
+  const X* yp = static_cast<const X*>(a.dy) + begin;
+  const R* ep = a.dres ? static_cast<const R*>(a.dres) + begin : nullptr;
+  const R* ep_late = ep;
+  R* dsum = a.dsum ? static_cast<R*>(a.dsum) + begin : nullptr;
+  X* dx = a.dx ? static_cast<X*>(a.dx) + begin : nullptr;
+  const int jump = tpr * 8;  // from one vector of a thread to its next
+  Raw8<R> s1[NV], e1[NV], e[NV];
+  Raw8<X> y1[NV];
+  auto fetch = [&](bool live) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (live && in[j]) {
+        load_raw(sp + j * jump, s1[j]);
+        load_raw(yp + j * jump, y1[j]);
+        if (AHEAD && ep) load_raw(ep + j * jump, e1[j]);
+      } else {
+        zero_raw(s1[j]);
+        zero_raw(y1[j]);
+      }
+    }
+    sp += step;
+    yp += step;
+    if (AHEAD && ep) ep += step;
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) zero_raw(e1[j]);
+  int parity = 0;
+  if (AHEAD) fetch(first < rows);
+  // groups that share a warp go through the same number of rows (its shuffles need all lanes)
+  const int lead = tpr < 32 ? first / (32 / tpr) * (32 / tpr) : first;  // of the warp's groups
+  int64_t next = first;
+  for (int64_t at = lead; at < rows; at += stride) {
+    const bool live = next < rows;
+    next += stride;
+    if (!AHEAD) fetch(live);
+    uint64_t s[NV][4], y[NV][4];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      widen2(s1[j], s[j]);
+      widen2(y1[j], y[j]);
+      e[j] = e1[j];
+    }
+    if (AHEAD) fetch(next < rows);
+    uint64_t ss = 0, as = 0;  // two zeros each
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint64_t g[4] = {0, 0, 0, 0};
+      if (!KEEP && in[j]) gamma2(a.gamma + (t + j * tpr) * 8, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ss = f2_fma(s[j][i], s[j][i], ss);
+        as = f2_fma(f2_mul(y[j][i], KEEP ? gk[KEEP ? j : 0][i] : g[i]), s[j][i], as);
+      }
+    }
+    float v0, v1, hi;
+    f2_unpack(ss, v0, hi);
+    v0 += hi;
+    f2_unpack(as, v1, hi);
+    v1 += hi;
+    row_sums(v0, v1, tpr, group, parity, red);
+    parity ^= 1;
+    const float r = rsqrtf(v0 * a.inv_d + a.eps);
+    const uint64_t r2 = f2_splat(r), k2 = f2_splat(-(r * r * r * (v1 * a.inv_d)));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (live && in[j]) {
+        uint64_t g[4], o[4];
+        if constexpr (!KEEP) gamma2(a.gamma + (t + j * tpr) * 8, g);
+        if (!AHEAD && ep_late) load_raw(ep_late + j * jump, e[j]);
+        widen2(e[j], o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t yr = f2_mul(y[j][i], r2);
+          dg[j][i] = f2_fma(yr, s[j][i], dg[j][i]);
+          o[i] = f2_fma(yr, KEEP ? gk[KEEP ? j : 0][i] : g[i], f2_fma(s[j][i], k2, o[i]));
+        }
+        float of[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(o[i], of[2 * i], of[2 * i + 1]);
+        if (dsum) store8(dsum + j * jump, of);
+        if (dx) store8(dx + j * jump, of);
+      }
+    }
+    if (dsum) dsum += step;
+    if (dx) dx += step;
+    if (!AHEAD && ep_late) ep_late += step;
+  }
+  float dgf[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(dg[j][i], dgf[j][2 * i], dgf[j][2 * i + 1]);
   float* out = a.partial + (size_t)blockIdx.x * a.D;
   if (groups == 1) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = t + j * tpr;
-      if (c < nvec) store8(out + c * 8, dg[j]);
+      if (c < nvec) store8(out + c * 8, dgf[j]);
     }
     return;
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = t + j * tpr;
-    if (c < nvec) store8(part + (size_t)group * a.D + c * 8, dg[j]);
+    if (c < nvec) store8(part + (size_t)group * a.D + c * 8, dgf[j]);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
@@ -283,25 +415,35 @@ __global__ void __launch_bounds__(512) rms_backward_kernel(const RmsGradArgs a) 
   }
 }
 
-// dgamma[c] = sum over the blocks' partial rows: 32 columns a block, 32 threads a column.
+// dgamma[c] = sum over the blocks' partial rows: 8 columns a block (enough blocks for the whole
+// GPU at the common widths), 128 threads a column with all their loads at once.
 __global__ void __launch_bounds__(1024) rms_dgamma_kernel(const float* partial, int n, int D, float* dgamma) {
-  __shared__ float red[32][33];
+  __shared__ float red[128][9];
   grid_launch_dependents();
   grid_wait_prior();
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
   float v = 0.f;
-  if (c < D)
-    for (int i = threadIdx.y; i < n; i += 32) v += partial[(size_t)i * D + c];
-  red[threadIdx.y][threadIdx.x] = v;
+  if (c < D) {
+#pragma unroll 5
+    for (int i = y; i < n; i += 128) v += partial[(size_t)i * D + c];
+  }
+  red[y][x] = v;
   __syncthreads();
-  v = red[threadIdx.x][threadIdx.y];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;  // warp w < 8 adds up column w
+  if (w >= 8) return;
+  v = (red[lane][w] + red[lane + 32][w]) + (red[lane + 64][w] + red[lane + 96][w]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && col < D) dgamma[col] = v;
+  if (lane == 0 && blockIdx.x * 8 + w < D) dgamma[blockIdx.x * 8 + w] = v;
 }
 
-// ---- element-wise form: any width and element-aligned buffers, one block a row
+// ---- element-wise forms: any width and element-aligned buffers, one block a row
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(__half v) { return __half2float(v); }
+__device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void assign(float& d, float v) { d = v; }
+__device__ __forceinline__ void assign(__half& d, float v) { d = __float2half_rn(v); }
+__device__ __forceinline__ void assign(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 __device__ __forceinline__ float load1(const void* p, int type, size_t i) {
   if (type == TFL_F32) return static_cast<const float*>(p)[i];
   if (type == TFL_F16) return __half2float(static_cast<const __half*>(p)[i]);
@@ -318,6 +460,90 @@ __device__ __forceinline__ void store1(void* p, int type, size_t i, float v) {
     static_cast<uint8_t*>(p)[i] = (uint8_t)e4m3x2(v, 0.f);
 }
 
+// Rows of up to T NE values: T threads with NE each in registers, all loads at once (1531 x 1001 fp32
+// 5.2 us; the two passes below take 8.5 us).
+template <class X, class R, int T, int NE>
+__global__ void __launch_bounds__(T) rms_forward_values_kernel(const RmsArgs a) {
+  __shared__ float red[64];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const size_t base = (size_t)blockIdx.x * a.D + threadIdx.x;
+  const X* x = static_cast<const X*>(a.x) + base;
+  const R* res = a.res ? static_cast<const R*>(a.res) + base : nullptr;
+  float s[NE], v[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NE; ++j) s[j] = (int)threadIdx.x + j * T < a.D ? value(x[j * T]) : 0.f;
+  if (res) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if ((int)threadIdx.x + j * T < a.D) s[j] += value(res[j * T]);
+  }
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    const int c = threadIdx.x + j * T;
+    v[0] = fmaf(s[j], s[j], v[0]);
+    if (c < a.D) {
+      if (a.res_out) assign(static_cast<R*>(a.res_out)[base + j * T], s[j]);
+      s[j] *= __ldg(a.gamma + c);
+      v[1] = max_nan(v[1], fabsf(s[j]));
+    }
+  }
+  group_reduce<2>(v, T, true, red);
+  float r = rsqrtf(v[0] * a.inv_d + a.eps);
+  if (a.y_type == TFL_E4M3) {
+    const float amax = max_nan(v[1] * r, kMinAmax);
+    if (threadIdx.x == 0) a.y_scale[blockIdx.x] = amax / kE4m3Max;
+    r *= kE4m3Max / amax;
+  }
+#pragma unroll
+  for (int j = 0; j < NE; ++j)
+    if ((int)threadIdx.x + j * T < a.D) store1(a.y, a.y_type, base + j * T, s[j] * r);
+}
+
+template <class X, class R, int T, int NE>
+__global__ void __launch_bounds__(T) rms_backward_values_kernel(const RmsGradArgs a) {
+  __shared__ float red[64];
+  grid_launch_dependents();
+  grid_wait_prior();
+  float dg[NE];
+#pragma unroll
+  for (int j = 0; j < NE; ++j) dg[j] = 0.f;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const size_t base = (size_t)row * a.D + threadIdx.x;
+    float s[NE], y[NE], e[NE], v[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const bool in = (int)threadIdx.x + j * T < a.D;
+      s[j] = in ? value(static_cast<const R*>(a.sum)[base + j * T]) : 0.f;
+      y[j] = in ? value(static_cast<const X*>(a.dy)[base + j * T]) : 0.f;
+      e[j] = in && a.dres ? value(static_cast<const R*>(a.dres)[base + j * T]) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const int c = threadIdx.x + j * T;
+      v[0] = fmaf(s[j], s[j], v[0]);
+      if (c < a.D) v[1] = fmaf(y[j] * __ldg(a.gamma + c), s[j], v[1]);
+    }
+    group_reduce<2>(v, T, false, red);
+    const float r = rsqrtf(v[0] * a.inv_d + a.eps);
+    const float k = r * r * r * (v[1] * a.inv_d);
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const int c = threadIdx.x + j * T;
+      if (c < a.D) {
+        dg[j] = fmaf(y[j] * r, s[j], dg[j]);
+        const float o = e[j] + fmaf(r * __ldg(a.gamma + c), y[j], -s[j] * k);
+        if (a.dsum) assign(static_cast<R*>(a.dsum)[base + j * T], o);
+        if (a.dx) assign(static_cast<X*>(a.dx)[base + j * T], o);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NE; ++j)
+    if ((int)threadIdx.x + j * T < a.D) a.partial[(size_t)blockIdx.x * a.D + threadIdx.x + j * T] = dg[j];
+}
+
+// Wider rows: two passes, the second from L1 / L2.
 __global__ void __launch_bounds__(256) rms_forward_any_kernel(const RmsArgs a) {
   __shared__ float red[64];
   grid_launch_dependents();
@@ -384,83 +610,106 @@ int pow2_at_least(int v) {
 }
 
 template <class X, class R, class Y>
-cudaError_t forward_vec(RmsArgs a, cudaStream_t s) {
+cudaError_t forward(RmsArgs a, cudaStream_t s) {
   const int nvec = a.D / 8;
   const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
   a.tpr = pow2_at_least((nvec + nv - 1) / nv);
   const int threads = a.tpr > 256 ? a.tpr : 256;
   const int64_t per = threads / a.tpr;
-  const dim3 grid((unsigned)((a.rows + per - 1) / per));
+  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
   if (nv == 1) return launch_dependent(rms_forward_kernel<X, R, Y, 1>, grid, threads, 0, s, a);
   if (nv == 2) return launch_dependent(rms_forward_kernel<X, R, Y, 2>, grid, threads, 0, s, a);
   return launch_dependent(rms_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
 }
 
-template <class X, class R>
-cudaError_t forward_y(const RmsArgs& a, cudaStream_t s) {
-  if (a.y_type == TFL_E4M3) return forward_vec<X, R, E4m3>(a, s);
-  if constexpr (sizeof(X) == 4) {
-    if (a.y_type == TFL_F16) return forward_vec<X, R, __half>(a, s);
-    if (a.y_type == TFL_BF16) return forward_vec<X, R, __nv_bfloat16>(a, s);
-  }
-  return forward_vec<X, R, X>(a, s);
+cudaError_t add_partials(const RmsGradArgs& a, int n, cudaStream_t s) {
+  return launch_dependent(rms_dgamma_kernel, (a.D + 7) / 8, 1024, 0, s, (const float*)a.partial, n, a.D, a.dgamma);
+}
+
+template <class X, class R, int NV, int THREADS, int BLOCKS>
+cudaError_t backward_with(RmsGradArgs a, int num_sms, cudaStream_t s) {
+  a.tpr = pow2_at_least((a.D / 8 + NV - 1) / NV);
+  const int groups = THREADS / a.tpr;
+  const int64_t need = (a.rows + groups - 1) / groups;
+  int grid = num_sms * BLOCKS < a.blocks ? num_sms * BLOCKS : a.blocks;  // what the GPU holds at once
+  if (need < grid) grid = (int)need;
+  const size_t smem = groups > 1 ? (size_t)groups * a.D * sizeof(float) : 0;  // at most 8 KB
+  const cudaError_t e = launch_dependent(rms_backward_kernel<X, R, NV, THREADS, BLOCKS>, grid, THREADS, smem, s, a);
+  return e == cudaSuccess ? add_partials(a, grid, s) : e;
 }
 
 template <class X, class R>
-cudaError_t backward_vec(RmsGradArgs a, cudaStream_t s) {
-  const int nvec = a.D / 8;
-  const int nv = nvec <= 32 ? 1 : nvec <= 1024 ? 2 : 4;
-  a.tpr = pow2_at_least((nvec + nv - 1) / nv);
-  const int threads = a.tpr > 256 ? a.tpr : 256, groups = threads / a.tpr;
-  const int64_t need = (a.rows + groups - 1) / groups;
-  const int grid = (int)(need < a.blocks ? need : a.blocks);
-  const size_t smem = groups > 1 ? (size_t)groups * a.D * sizeof(float) : 0;  // at most 16 KB
-  cudaError_t e;
-  if (nv == 1)
-    e = launch_dependent(rms_backward_kernel<X, R, 1>, grid, threads, smem, s, a);
-  else if (nv == 2)
-    e = launch_dependent(rms_backward_kernel<X, R, 2>, grid, threads, smem, s, a);
-  else
-    e = launch_dependent(rms_backward_kernel<X, R, 4>, grid, threads, smem, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(rms_dgamma_kernel, (a.D + 31) / 32, dim3(32, 32), 0, s, (const float*)a.partial, grid, a.D,
-                          a.dgamma);
+cudaError_t backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
+  constexpr int WIDE = sizeof(R) == 4;  // fp32 rows take more registers, and carry more bytes a thread
+  if (a.D <= 2048) return backward_with<X, R, 1, 256, WIDE ? 2 : 3>(a, num_sms, s);
+  if (a.D <= 4096) return WIDE ? backward_with<X, R, 1, 512, 1>(a, num_sms, s) : backward_with<X, R, 2, 256, 2>(a, num_sms, s);
+  if (a.D <= 8192) return backward_with<X, R, 2, 512, 1>(a, num_sms, s);
+  return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
 }
+
+constexpr int kRmsMaxValues = 8192;  // widest row the element-wise kernels hold in registers
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// f(X(), R()) for the C++ types of a call's x and residual.
+template <class F>
+cudaError_t with_types(int x_type, int res_type, F f) {
+  if (x_type == TFL_F32) return f(float(), float());
+  if (x_type == TFL_F16) return res_type == TFL_F32 ? f(__half(), float()) : f(__half(), __half());
+  return res_type == TFL_F32 ? f(__nv_bfloat16(), float()) : f(__nv_bfloat16(), __nv_bfloat16());
+}
 
 }  // namespace
 
 cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s) {
   const bool vec = a.D % 8 == 0 && a.D <= kRmsMaxRegisterRow && aligned(a.x, 16) && aligned(a.res, 16) &&
                    aligned(a.gamma, 16) && aligned(a.res_out, 16) && aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
+  if (!vec && a.D <= kRmsMaxValues) {
+    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+      using X = decltype(x);
+      using R = decltype(r);
+      const unsigned n = (unsigned)a.rows;
+      if (a.D <= 1024) return launch_dependent(rms_forward_values_kernel<X, R, 256, 4>, n, 256, 0, s, a);
+      if (a.D <= 4096) return launch_dependent(rms_forward_values_kernel<X, R, 256, 16>, n, 256, 0, s, a);
+      return launch_dependent(rms_forward_values_kernel<X, R, 1024, 8>, n, 1024, 0, s, a);
+    });
+  }
   if (!vec) {
     const int64_t most = (int64_t)num_sms * 8;
     return launch_dependent(rms_forward_any_kernel, (unsigned)(a.rows < most ? a.rows : most), 256, 0, s, a);
   }
-  if (a.x_type == TFL_F32) return forward_y<float, float>(a, s);
-  if (a.x_type == TFL_F16)
-    return a.res_type == TFL_F32 ? forward_y<__half, float>(a, s) : forward_y<__half, __half>(a, s);
-  return a.res_type == TFL_F32 ? forward_y<__nv_bfloat16, float>(a, s)
-                               : forward_y<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+    using X = decltype(x);
+    using R = decltype(r);
+    if (a.y_type == TFL_E4M3) return forward<X, R, E4m3>(a, s);
+    if constexpr (sizeof(X) == 4) {
+      if (a.y_type == TFL_F16) return forward<X, R, __half>(a, s);
+      if (a.y_type == TFL_BF16) return forward<X, R, __nv_bfloat16>(a, s);
+    }
+    return forward<X, R, X>(a, s);
+  });
 }
 
-cudaError_t launch_rms_backward(const RmsGradArgs& a, cudaStream_t s) {
-  const bool vec = a.D % 8 == 0 && a.D <= kRmsMaxRegisterRow / 2 && aligned(a.sum, 16) && aligned(a.gamma, 16) &&
-                   aligned(a.dy, 16) && aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
+cudaError_t launch_rms_backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
+  const bool vec = a.D % 8 == 0 && a.D <= kRmsMaxRegisterRow / 2 && aligned(a.sum, 16) && aligned(a.gamma, 16) && aligned(a.dy, 16) &&
+                   aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
   if (!vec) {
     const int grid = (int)(a.rows < a.blocks ? a.rows : a.blocks);
-    cudaError_t e = launch_dependent(rms_backward_any_kernel, grid, 256, 0, s, a);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(rms_dgamma_kernel, (a.D + 31) / 32, dim3(32, 32), 0, s, (const float*)a.partial, grid,
-                            a.D, a.dgamma);
+    const cudaError_t e =
+        a.D > kRmsMaxValues
+            ? launch_dependent(rms_backward_any_kernel, grid, 256, 0, s, a)
+            : with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+                using X = decltype(x);
+                using R = decltype(r);
+                if (a.D <= 1024) return launch_dependent(rms_backward_values_kernel<X, R, 256, 4>, grid, 256, 0, s, a);
+                if (a.D <= 4096) return launch_dependent(rms_backward_values_kernel<X, R, 512, 8>, grid, 512, 0, s, a);
+                return launch_dependent(rms_backward_values_kernel<X, R, 1024, 8>, grid, 1024, 0, s, a);
+              });
+    return e == cudaSuccess ? add_partials(a, grid, s) : e;
   }
-  if (a.x_type == TFL_F32) return backward_vec<float, float>(a, s);
-  if (a.x_type == TFL_F16)
-    return a.res_type == TFL_F32 ? backward_vec<__half, float>(a, s)
-                                 : backward_vec<__half, __half>(a, s);
-  return a.res_type == TFL_F32 ? backward_vec<__nv_bfloat16, float>(a, s)
-                               : backward_vec<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+    return backward<decltype(x), decltype(r)>(a, num_sms, s);
+  });
 }
 
 }  // namespace tfl

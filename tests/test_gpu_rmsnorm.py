@@ -129,10 +129,29 @@ def test_forward_of_every_type(xt, rt, yt):
 # one value, less than a warp, ragged vectors, one warp and more a row, the widest row kept in
 # registers and the first that is not, widths no vector divides
 @pytest.mark.parametrize("rows,d", [(1, 1), (3, 7), (9, 64), (300, 72), (33, 256), (17, 512), (12, 1000), (1000, 1024),
-                                    (3, 1032), (5, 4096), (3, 8200), (2, 32768), (2, 32776), (4, 1001), (2, 50001)])
+                                    (3, 1032), (5, 4096), (3, 8200), (2, 32768), (2, 32776), (4, 1001), (3, 1025), (70, 4095), (2, 4097), (30, 8191), (3, 8193), (2, 50001)])
 @pytest.mark.parametrize("xt,rt,yt", [("bf16", "f32", "e4m3"), ("f16", "f16", "f16"), ("f32", "f32", "f32")])
 def test_forward_of_every_width(rows, d, xt, rt, yt):
     _check_forward(rows, d, xt, rt, yt, _forward(rows, d, xt, rt, yt, seed=rows + d))
+
+
+# enough rows for the kernel that loops over them: groups of one thread to the whole block, a
+# ragged last round
+@pytest.mark.parametrize("rows,d", [(351000, 8), (45001, 72), (22000, 256), (11003, 400), (5603, 1000), (1501, 4096)])
+@pytest.mark.parametrize("xt,rt,yt", [("bf16", "f32", "e4m3"), ("f16", "f16", "f16"), ("f32", "f32", "f32"),
+                                      ("bf16", "bf16", "e4m3")])
+def test_forward_of_many_rows(rows, d, xt, rt, yt):
+    _check_forward(rows, d, xt, rt, yt, _forward(rows, d, xt, rt, yt, seed=d))
+
+
+@pytest.mark.parametrize("xt,rt,yt", TYPES)
+def test_forward_of_many_rows_of_every_type(xt, rt, yt):
+    _check_forward(11003, 512, xt, rt, yt, _forward(11003, 512, xt, rt, yt, seed=1))
+
+
+@pytest.mark.parametrize("with_res,store", [(False, True), (True, False)])
+def test_forward_of_many_rows_without_residual_or_its_store(with_res, store):
+    _check_forward(6001, 1024, "bf16", "f32", "bf16", _forward(6001, 1024, "bf16", "f32", "bf16", with_res, store))
 
 
 @pytest.mark.parametrize("with_res,store", [(False, True), (True, False), (False, False)])
@@ -147,40 +166,40 @@ def test_forward_of_unaligned_buffers(offset):
     _check_forward(7, 512, "f16", "f16", "f16", _forward(7, 512, "f16", "f16", "f16", offset=offset))
 
 
-@pytest.mark.parametrize("d", [512, 515])
-def test_forward_in_place_equals_out_of_place(d):
+@pytest.mark.parametrize("rows,d", [(40, 512), (40, 515), (11003, 512)])
+def test_forward_in_place_equals_out_of_place(rows, d):
     import torch
     pkg = _pkg()
-    x, res, gamma, out, y, _ = _forward(40, d, "bf16", "bf16", "bf16", seed=3)
+    x, res, gamma, out, y, _ = _forward(rows, d, "bf16", "bf16", "bf16", seed=3)
     h = pkg.tfl_rmsnorm_create(d, _code("bf16"), _code("bf16"), _code("bf16"), EPS)
     try:
         x2, r2 = x.clone(), res.clone()
-        pkg.tfl_rmsnorm_forward(h, 40, x2.data_ptr(), r2.data_ptr(), gamma.data_ptr(), r2.data_ptr(), x2.data_ptr(),
+        pkg.tfl_rmsnorm_forward(h, rows, x2.data_ptr(), r2.data_ptr(), gamma.data_ptr(), r2.data_ptr(), x2.data_ptr(),
                                 None, _stream())
         assert torch.equal(r2, out) and torch.equal(x2, y)
         x3, y3 = x.clone(), torch.empty_like(y)
-        pkg.tfl_rmsnorm_forward(h, 40, x3.data_ptr(), res.data_ptr(), gamma.data_ptr(), x3.data_ptr(), y3.data_ptr(),
+        pkg.tfl_rmsnorm_forward(h, rows, x3.data_ptr(), res.data_ptr(), gamma.data_ptr(), x3.data_ptr(), y3.data_ptr(),
                                 None, _stream())
         assert torch.equal(x3, out) and torch.equal(y3, y)
     finally:
         pkg.tfl_rmsnorm_destroy(h)
 
 
-@pytest.mark.parametrize("d", [256, 255])
-def test_rows_of_zeros_nan_and_infinity_stay_their_own(d):
+@pytest.mark.parametrize("rows,d", [(6, 256), (6, 255), (22000, 256)])
+def test_rows_of_zeros_nan_and_infinity_stay_their_own(rows, d):
     import torch
     pkg = _pkg()
     gen = torch.Generator(device="cuda").manual_seed(1)
-    x = _randn(gen, (6, d), "bf16")
+    x = _randn(gen, (rows, d), "bf16")
     x[1] = 0
     x[2, 5] = float("nan")
     x[3, 7] = float("inf")
     gamma = torch.ones(d, device="cuda")
     for yt in ("bf16", "e4m3"):
-        y = torch.zeros((6, d), device="cuda").to(_type(yt))
-        scale = torch.zeros(6, device="cuda")
+        y = torch.zeros((rows, d), device="cuda").to(_type(yt))
+        scale = torch.zeros(rows, device="cuda")
         h = pkg.tfl_rmsnorm_create(d, _code("bf16"), _code("bf16"), _code(yt), EPS)
-        pkg.tfl_rmsnorm_forward(h, 6, x.data_ptr(), None, gamma.data_ptr(), None, y.data_ptr(),
+        pkg.tfl_rmsnorm_forward(h, rows, x.data_ptr(), None, gamma.data_ptr(), None, y.data_ptr(),
                                 scale.data_ptr() if yt == "e4m3" else None, _stream())
         torch.cuda.synchronize()
         pkg.tfl_rmsnorm_destroy(h)
@@ -188,7 +207,7 @@ def test_rows_of_zeros_nan_and_infinity_stay_their_own(d):
         assert (f[1] == 0).all()
         assert f[2].isnan().all()
         assert f[3, 7].isnan()
-        assert f[[0, 1, 4, 5]].isfinite().all()
+        assert f[[0, 1, *range(4, rows)]].isfinite().all()
         if yt == "e4m3":
             assert scale[1].item() == np.float32(2.0 ** -100) / np.float32(448) and scale[2].isnan()
 
@@ -234,7 +253,8 @@ def _check_backward(rows, d, xt, rt, got):
 
 
 @pytest.mark.parametrize("rows,d", [(1, 1), (3, 7), (9, 64), (4001, 72), (33, 256), (700, 1000), (2500, 1024), (3, 1032),
-                                    (5, 4096), (3, 8200), (700, 16384), (2, 16392), (5, 32768), (40, 1001), (2, 50001)])
+                                    (5, 4096), (700, 4096), (3, 8200), (700, 8192), (700, 16384), (2, 16392), (5, 32768), (40, 1001), (900, 1025), (3, 4095), (700, 4097), (300, 8191),
+                                    (2, 50001)])
 @pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16")])
 def test_backward_of_every_width(rows, d, xt, rt):
     _check_backward(rows, d, xt, rt, _backward(rows, d, xt, rt, seed=rows + d))
