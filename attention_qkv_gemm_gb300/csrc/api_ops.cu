@@ -212,15 +212,17 @@ struct tfl_glu {
   int64_t max_grad_tokens = 0;
   int device = 0, num_sms = 0, pairs = 0;
   int* status = nullptr;                          // status word (256 bytes), then dg and du
-  uint16_t *dg = nullptr, *du = nullptr;          // [max_grad_tokens, F]
+  uint16_t *dg = nullptr, *du = nullptr;          // [max_grad_tokens, F] in rows of `pitch`
+  int pitch = 0;                                  // F to the next 128 bytes: a copied box row is then one line
 };
 
 namespace {
 
 // A row-major [rows, cols] matrix in boxes of 128 bytes of columns by box_rows, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, uint32_t box_rows) {
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, uint32_t box_rows,
+              int64_t pitch = 0) {
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)(cols * elem)};
+  cuuint64_t strides[1] = {(cuuint64_t)((pitch ? pitch : cols) * elem)};
   cuuint32_t box[2] = {(cuuint32_t)(128 / elem), box_rows};
   cuuint32_t es[2] = {1, 1};
   return get_encode()(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
@@ -284,7 +286,8 @@ int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_t
   g->device = dev;
   g->num_sms = sms;
   g->pairs = pairs;
-  const size_t each = ((size_t)max_grad_tokens * d_ff * 2 + 255) / 256 * 256;
+  g->pitch = (d_ff + 63) / 64 * 64;
+  const size_t each = ((size_t)max_grad_tokens * g->pitch * 2 + 255) / 256 * 256;
   if (cudaMalloc(&g->status, 256 + 2 * each) != cudaSuccess) {
     cudaGetLastError();
     delete g;
@@ -352,6 +355,7 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   a.x_scale = x_scale;
   a.g_scale = wg_scale;
   a.u_scale = wu_scale;
+  a.ldo = g->F;
   a.out = static_cast<uint16_t*>(h);
   TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, static_cast<cudaStream_t>(stream)), "feed-forward");
   return TFL_OK;
@@ -396,9 +400,11 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bno) &&
             make_map(&m1.b1, wu, Fi, Di, 2, p1.bno);
   m1.a1 = m1.a0;
-  ok = ok && make_map(&m2.a0, g->dg, tokens, Fi, 2, p2.a_rows) && make_map(&m2.a1, g->du, tokens, Fi, 2, p2.a_rows) &&
+  ok = ok && make_map(&m2.a0, g->dg, tokens, Fi, 2, p2.a_rows, g->pitch) &&
+       make_map(&m2.a1, g->du, tokens, Fi, 2, p2.a_rows, g->pitch) &&
        make_map(&m2.b0, wg, Fi, Di, 2, kMnBox) && make_map(&m2.b1, wu, Fi, Di, 2, kMnBox);
-  ok = ok && make_map(&m3.a0, g->dg, tokens, Fi, 2, kMnBox) && make_map(&m3.a1, g->du, tokens, Fi, 2, kMnBox) &&
+  ok = ok && make_map(&m3.a0, g->dg, tokens, Fi, 2, kMnBox, g->pitch) &&
+       make_map(&m3.a1, g->du, tokens, Fi, 2, kMnBox, g->pitch) &&
        make_map(&m3.b0, x, tokens, Di, 2, kMnBox);
   m3.b1 = m3.b0;
   if (!ok) return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
@@ -408,6 +414,7 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.N = Fi;
   a.num_k = kd;
   a.dh = static_cast<const uint16_t*>(dh);
+  a.ldo = g->pitch;
   a.out = g->dg;
   a.out2 = g->du;
   TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, st), "feed-forward slopes");
@@ -416,12 +423,14 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.N = Di;
   a.k_half = kf;
   a.num_k = 2 * kf;
+  a.ldo = Di;
   a.out = static_cast<uint16_t*>(dx);
   TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, st), "feed-forward dx");
   a = glu_args(g);
   a.M = Fi;
   a.N = Di;
   a.num_k = kt;
+  a.ldo = Di;
   a.out = static_cast<uint16_t*>(dwg);
   a.out2 = static_cast<uint16_t*>(dwu);
   TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, st), "feed-forward weight gradients");

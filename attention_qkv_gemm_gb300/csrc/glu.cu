@@ -384,9 +384,9 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       for (int c = half; c < chunks; c += 2) {
         const int n0 = tl.n * bno + c * W;                   // first output column
         const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
-        const size_t off = (size_t)m0 * args.N + n0;
         uint4 o[W / 8], o2[W / 8];
-        if constexpr (MODE == GLU_SLOPES) load_cols<W>(st, lane, o2, args.dh + off, args.N, rows, cols);
+        if constexpr (MODE == GLU_SLOPES)
+          load_cols<W>(st, lane, o2, args.dh + (size_t)m0 * args.N + n0, args.N, rows, cols);
 #pragma unroll
         for (int b = 0; b < W / LD; ++b) {
           const int col = c * W + b * LD;
@@ -426,9 +426,9 @@ __global__ void __launch_bounds__(kGluThreads, 1)
           }
           pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
         }
-        uint16_t* out = (MODE == GLU_DW && tl.z ? args.out2 : args.out) + off;
-        store_cols<W>(st, lane, o, out, args.N, rows, cols);
-        if constexpr (MODE == GLU_SLOPES) store_cols<W>(st, lane, o2, args.out2 + off, args.N, rows, cols);
+        const size_t to = (size_t)m0 * args.ldo + n0;
+        store_cols<W>(st, lane, o, (MODE == GLU_DW && tl.z ? args.out2 : args.out) + to, args.ldo, rows, cols);
+        if constexpr (MODE == GLU_SLOPES) store_cols<W>(st, lane, o2, args.out2 + to, args.ldo, rows, cols);
       }
       if (++acc == 2) {
         acc = 0;

@@ -56,6 +56,7 @@ struct GluArgs {
   int act = 0;
   int bf16_operands = 0;         // 16-bit operands: bf16, else fp16
   int bf16_out = 0;              // 16-bit outputs (and dh): bf16, else fp16
+  int ldo = 0;                   // row pitch of out and out2
   const uint16_t* dh = nullptr;  // SLOPES: [M, N]
   uint16_t* out = nullptr;
   uint16_t* out2 = nullptr;

@@ -433,7 +433,7 @@ typedef struct tfl_glu tfl_glu;
 /* d_model and d_ff: multiples of 8 (16 for e4m3 operands) up to 2^24.
  * max_grad_tokens: the most tokens tfl_glu_backward will be given (0: no
  * backward; e4m3 operands have none); the handle holds 4 max_grad_tokens d_ff
- * bytes of scratch for it.  Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
+ * bytes of scratch for it (d_ff to the next multiple of 64).  Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
 int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_type, int32_t act,
                    int64_t max_grad_tokens, tfl_glu** out);
 
