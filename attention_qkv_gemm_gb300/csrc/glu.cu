@@ -35,9 +35,12 @@ constexpr int kMnChunk = 64 * 128; // MN-major operands: 64 k rows of 64 values
 
 constexpr int kMaxBN = 256;        // accumulator columns of a tile, at most
 constexpr int kMaxStages = 12;
-constexpr int kXposeBytes = kGluEpiWarps * 32 * 128;  // one 32 x 128 B transpose stage a warp
-constexpr int kRingBytes = 232448 - 1024 - kXposeBytes - 256;
-constexpr size_t kGluSmem = 1024 + kRingBytes + kXposeBytes + 256;
+// Shared memory: ring, one 32-row transpose stage an epilogue warp (columns stored at a time: 64 in
+// wide tiles, 32 in narrow ones), barriers.
+constexpr int kBarrierBytes = 256;
+constexpr int xpose_bytes(bool wide) { return kGluEpiWarps * 32 * (wide ? 128 : 64); }
+constexpr int kGluSmem = 232448;
+constexpr int ring_bytes(bool wide) { return kGluSmem - 1024 - xpose_bytes(wide) - kBarrierBytes; }
 
 // The activation of a packed pair of fp32 values (FMA-pipe work runs two lanes an instruction;
 // the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
@@ -196,8 +199,8 @@ __global__ void __launch_bounds__(kGluThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   grid_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* xpose = smem + kRingBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + kXposeBytes);
+  uint8_t* xpose = smem + ring_bytes(WIDE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + xpose_bytes(WIDE));
   uint64_t* empty = full + kMaxStages;
   uint64_t* accf = empty + kMaxStages;
   uint64_t* acce = accf + 2;
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
   constexpr int kWideStage = (kGluRows + kMaxBN / CG) * kKBytes;
   const int bno = WIDE ? (TWO ? kMaxBN / 2 : kMaxBN) : args.bno;  // output columns of a tile
   const int bn = TWO ? 2 * bno : bno;                             // accumulator columns
-  const int stages = WIDE ? kRingBytes / kWideStage : args.stages;
+  const int stages = WIDE ? ring_bytes(true) / kWideStage : args.stages;
   const int stage_bytes = WIDE ? kWideStage : args.stage_bytes;
   const int a_bytes = WIDE ? kGluRows * kKBytes : args.a_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     constexpr int W = WIDE ? 64 : 32;  // columns stored at a time; the two warps of a lane quarter take turns
     constexpr int LD = 32;             // columns computed at a time
     const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* st = xpose + (warp - 2) * 4096;
+    uint8_t* st = xpose + (warp - 2) * (32 * 2 * W);
     int acc = 0;
     uint32_t acc_phase = 0;
     const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], 0) : 0, CG == 2 ? map_rank(&acce[1], 0) : 0};
@@ -361,12 +364,26 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       const Tile tl = tile_at(t, num_m, num_n);
       const int m0 = (tl.m * CG + rank) * kGluRows + q * 32, m = m0 + lane;
       const uint32_t rows = __ballot_sync(0xffffffffu, m < args.M);
+      const int n_tile = tl.n * bno;  // first output column of the tile
+      // e4m3: the row's scale and this lane's share of the first chunk's column scales, on their
+      // way while the products finish; columns past the last read the last one's (not stored)
+      float sx = 1.0f, sg[W / 32], su[W / 32];
+      auto fetch_scales = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < W / 32; ++i) {
+          const int n = min(n_tile + c * W + i * 32 + lane, args.N - 1);
+          sg[i] = __ldg(args.g_scale + n);
+          su[i] = __ldg(args.u_scale + n);
+        }
+      };
+      if constexpr (F8) {
+        sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
+        fetch_scales(half);
+      }
       const bool ok = wait_bounded(&accf[acc], acc_phase, wc);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxBN);
-      float sx = 1.0f;
-      if constexpr (F8) sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
       const int chunks = (bno + W - 1) / W;
       const int last = chunks - 1 - ((chunks - 1 - half) & 1);  // this warp's last chunk (< 0: it has none)
       auto hand_back = [&]() {
@@ -382,11 +399,21 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       if (half > last) hand_back();
 #pragma unroll 1
       for (int c = half; c < chunks; c += 2) {
-        const int n0 = tl.n * bno + c * W;                   // first output column
+        const int n0 = n_tile + c * W;                       // first output column
         const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
         uint4 o[W / 8], o2[W / 8];
         if constexpr (MODE == GLU_SLOPES)
           load_cols<W>(st, lane, o2, args.dh + (size_t)m0 * args.N + n0, args.N, rows, cols);
+        if constexpr (F8) {  // the chunk's scales to every lane, through the stage
+          float* sc = reinterpret_cast<float*>(st);
+#pragma unroll
+          for (int i = 0; i < W / 32; ++i) {
+            sc[i * 32 + lane] = sg[i];
+            sc[W + i * 32 + lane] = su[i];
+          }
+          __syncwarp();
+          if (c + 2 < chunks) fetch_scales(c + 2);
+        }
 #pragma unroll
         for (int b = 0; b < W / LD; ++b) {
           const int col = c * W + b * LD;
@@ -397,15 +424,15 @@ __global__ void __launch_bounds__(kGluThreads, 1)
           // once the accumulator is in registers it is handed back, before arithmetic and stores
           if (b == W / LD - 1 && c == last) hand_back();
           if constexpr (F8) {
-            // columns past the last read the last four scales again (they are not stored)
+            const float* sc = reinterpret_cast<const float*>(st) + b * LD;
 #pragma unroll
             for (int i = 0; i < LD / 4; ++i) {
-              const int n = min(n0 + b * LD + 4 * i, args.N - 4);
-              const float4 a = __ldg(reinterpret_cast<const float4*>(args.g_scale + n));
-              const float4 e = __ldg(reinterpret_cast<const float4*>(args.u_scale + n));
+              const float4 a = *reinterpret_cast<const float4*>(sc + 4 * i);
+              const float4 e = *reinterpret_cast<const float4*>(sc + W + 4 * i);
               g[4 * i] *= sx * a.x, g[4 * i + 1] *= sx * a.y, g[4 * i + 2] *= sx * a.z, g[4 * i + 3] *= sx * a.w;
               u[4 * i] *= sx * e.x, u[4 * i + 1] *= sx * e.y, u[4 * i + 2] *= sx * e.z, u[4 * i + 3] *= sx * e.w;
             }
+            if (b == W / LD - 1) __syncwarp();  // the stage is free for the rows
           }
           if constexpr (MODE == GLU_FORWARD) {
             // the activation is chosen once for all values: a branch at each would keep the
@@ -469,7 +496,7 @@ cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStrea
   const bool b_mn = MODE == GLU_DX || MODE == GLU_DW;
   a.a_bytes = p.a_rows * kKBytes;
   a.stage_bytes = a.a_bytes + (b_mn ? (bn / CG + 63) / 64 * kMnChunk : bn / CG * kKBytes);
-  a.stages = kRingBytes / a.stage_bytes;
+  a.stages = ring_bytes(WIDE) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * CG);
@@ -490,9 +517,9 @@ cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStrea
 template <int CG, int MODE, bool F8>
 cudaError_t prepare_one() {
   cudaError_t e = cudaFuncSetAttribute(glu_kernel<CG, MODE, F8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)kGluSmem);
+                                       kGluSmem);
   if (CG == 2 && e == cudaSuccess)
-    e = cudaFuncSetAttribute(glu_kernel<2, MODE, F8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGluSmem);
+    e = cudaFuncSetAttribute(glu_kernel<2, MODE, F8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGluSmem);
   return e;
 }
 
