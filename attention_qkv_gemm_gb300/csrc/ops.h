@@ -12,6 +12,7 @@ struct RmsArgs {
   int64_t rows = 0;
   int D = 0;
   int tpr = 0;                   // threads that hold one row (a power of two), set by the launcher
+  int64_t ahead = 0;             // rows between a row and the one prefetched beside it, likewise
   float inv_d = 0.f, eps = 0.f;
   int x_type = 0, res_type = 0, y_type = 0;
   const void* x = nullptr;       // [rows, D]

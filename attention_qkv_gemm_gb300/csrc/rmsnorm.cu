@@ -117,6 +117,12 @@ __device__ __forceinline__ void store8(E4m3* p, const float* v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
 }
 
+// Brings `bytes` from p on into L2, one 128-byte line a thread and turn (the last line only if a
+// multiple of 128 bytes from p lies in it).
+__device__ __forceinline__ void lines_to_l2(const void* p, int bytes, int t, int threads) {
+  for (int o = t * 128; o < bytes; o += threads * 128) prefetch_l2(static_cast<const uint8_t*>(p) + o);
+}
+
 // Sum (or maximum) over the `tpr` threads of this thread's row group; `red` holds one float a
 // warp and value.  Groups of up to a warp stay inside it.
 template <int N>
@@ -182,6 +188,13 @@ __global__ void __launch_bounds__(1024) rms_forward_kernel(const RmsArgs a) {
         for (int i = 0; i < 8; ++i) s[j][i] += r[i];
       }
     }
+  }
+  // While this row is reduced, the rows of the block that will take this one's place start on
+  // their way to L2 (100000 x 1024 bf16 to e4m3: 130 -> 106 us).
+  const int64_t later = row + a.ahead;
+  if (later < a.rows) {
+    lines_to_l2(static_cast<const X*>(a.x) + (size_t)later * a.D, a.D * (int)sizeof(X), t, tpr);
+    if (a.res) lines_to_l2(static_cast<const R*>(a.res) + (size_t)later * a.D, a.D * (int)sizeof(R), t, tpr);
   }
   float v[2] = {0.f, 0.f};
 #pragma unroll
@@ -478,6 +491,11 @@ __global__ void __launch_bounds__(T) rms_forward_values_kernel(const RmsArgs a) 
     for (int j = 0; j < NE; ++j)
       if ((int)threadIdx.x + j * T < a.D) s[j] += value(res[j * T]);
   }
+  const int64_t later = blockIdx.x + a.ahead;  // as in rms_forward_kernel
+  if (later < a.rows) {
+    lines_to_l2(static_cast<const X*>(a.x) + (size_t)later * a.D, a.D * (int)sizeof(X), threadIdx.x, T);
+    if (a.res) lines_to_l2(static_cast<const R*>(a.res) + (size_t)later * a.D, a.D * (int)sizeof(R), threadIdx.x, T);
+  }
 #pragma unroll
   for (int j = 0; j < NE; ++j) {
     const int c = threadIdx.x + j * T;
@@ -610,13 +628,14 @@ int pow2_at_least(int v) {
 }
 
 template <class X, class R, class Y>
-cudaError_t forward(RmsArgs a, cudaStream_t s) {
+cudaError_t forward(RmsArgs a, int num_sms, cudaStream_t s) {
   const int nvec = a.D / 8;
   const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
   a.tpr = pow2_at_least((nvec + nv - 1) / nv);
   const int threads = a.tpr > 256 ? a.tpr : 256;
   const int64_t per = threads / a.tpr;
   const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+  a.ahead = per * num_sms * (1024 / threads);  // 64 registers a thread: 1024 threads an SM
   if (nv == 1) return launch_dependent(rms_forward_kernel<X, R, Y, 1>, grid, threads, 0, s, a);
   if (nv == 2) return launch_dependent(rms_forward_kernel<X, R, Y, 2>, grid, threads, 0, s, a);
   return launch_dependent(rms_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
@@ -669,9 +688,11 @@ cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s) {
       using X = decltype(x);
       using R = decltype(r);
       const unsigned n = (unsigned)a.rows;
-      if (a.D <= 1024) return launch_dependent(rms_forward_values_kernel<X, R, 256, 4>, n, 256, 0, s, a);
-      if (a.D <= 4096) return launch_dependent(rms_forward_values_kernel<X, R, 256, 16>, n, 256, 0, s, a);
-      return launch_dependent(rms_forward_values_kernel<X, R, 1024, 8>, n, 1024, 0, s, a);
+      RmsArgs b = a;
+      b.ahead = a.D <= 4096 ? (int64_t)num_sms * 8 : a.rows;  // none for the widest: 9000 x 6001 139 us without, 180 with
+      if (a.D <= 1024) return launch_dependent(rms_forward_values_kernel<X, R, 256, 4>, n, 256, 0, s, b);
+      if (a.D <= 4096) return launch_dependent(rms_forward_values_kernel<X, R, 256, 16>, n, 256, 0, s, b);
+      return launch_dependent(rms_forward_values_kernel<X, R, 1024, 8>, n, 1024, 0, s, b);
     });
   }
   if (!vec) {
@@ -681,12 +702,12 @@ cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s) {
   return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
     using X = decltype(x);
     using R = decltype(r);
-    if (a.y_type == TFL_E4M3) return forward<X, R, E4m3>(a, s);
+    if (a.y_type == TFL_E4M3) return forward<X, R, E4m3>(a, num_sms, s);
     if constexpr (sizeof(X) == 4) {
-      if (a.y_type == TFL_F16) return forward<X, R, __half>(a, s);
-      if (a.y_type == TFL_BF16) return forward<X, R, __nv_bfloat16>(a, s);
+      if (a.y_type == TFL_F16) return forward<X, R, __half>(a, num_sms, s);
+      if (a.y_type == TFL_BF16) return forward<X, R, __nv_bfloat16>(a, num_sms, s);
     }
-    return forward<X, R, X>(a, s);
+    return forward<X, R, X>(a, num_sms, s);
   });
 }
 
