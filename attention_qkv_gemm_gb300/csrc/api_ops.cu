@@ -3,6 +3,8 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <map>
+#include <mutex>
 #include <new>
 
 #include "host.h"
@@ -210,7 +212,8 @@ void tfl_rmsnorm_destroy(tfl_rmsnorm* n) {
 struct tfl_glu {
   int D = 0, F = 0, in_type = 0, out_type = 0, act = 0;
   int64_t max_grad_tokens = 0;
-  int device = 0, num_sms = 0, pairs = 0;
+  int device = 0;
+  GluUnits units;
   int* status = nullptr;                          // status word (256 bytes), then dg and du
   uint16_t *dg = nullptr, *du = nullptr;          // [max_grad_tokens, F] in rows of `pitch`
   int pitch = 0;                                  // F to the next 128 bytes: a copied box row is then one line
@@ -229,6 +232,22 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int 
                       const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Kernel attributes and what runs at once on a device: the same for every handle, asked once.
+int glu_units(int dev, int sms, GluUnits* u) {
+  static std::mutex lock;
+  static std::map<int, GluUnits> known;
+  std::lock_guard<std::mutex> hold(lock);
+  const auto it = known.find(dev);
+  if (it != known.end()) {
+    *u = it->second;
+    return TFL_OK;
+  }
+  u->sms = sms;
+  TFL_CUDA(prepare_glu_kernels(u), "feed-forward kernel attributes");
+  known[dev] = *u;
+  return TFL_OK;
 }
 
 constexpr int kMnBox = 64;  // MN-major operands come in boxes of 64 k rows
@@ -272,9 +291,9 @@ int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_t
   int dev = 0, sms = 0;
   if (int rc = usable_device(&dev, &sms)) return rc;
   if (!get_encode()) return fail(TFL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  int pairs = 0;
-  TFL_CUDA(prepare_glu_kernels(&pairs), "feed-forward kernel attributes");
-  if (pairs < 1) return fail(TFL_ERR_UNSUPPORTED, "the device runs no CTA pairs");
+  GluUnits units;
+  if (int rc = glu_units(dev, sms, &units)) return rc;
+  if (units.pairs < 1) return fail(TFL_ERR_UNSUPPORTED, "the device runs no CTA pairs");
   tfl_glu* g = new (std::nothrow) tfl_glu();
   if (!g) return fail(TFL_ERR_OOM, "handle allocation failed");
   g->D = d_model;
@@ -284,8 +303,7 @@ int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_t
   g->act = act;
   g->max_grad_tokens = max_grad_tokens;
   g->device = dev;
-  g->num_sms = sms;
-  g->pairs = pairs;
+  g->units = units;
   g->pitch = (d_ff + 63) / 64 * 64;
   const size_t each = ((size_t)max_grad_tokens * g->pitch * 2 + 255) / 256 * 256;
   if (cudaMalloc(&g->status, 256 + 2 * each) != cudaSuccess) {
@@ -338,11 +356,11 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
     a.g_scale = wg_scale;
     a.u_scale = wu_scale;
     a.out = static_cast<uint16_t*>(h);
-    TFL_CUDA(launch_glu_few(g->in_type, a, g->num_sms, static_cast<cudaStream_t>(stream)), "feed-forward");
+    TFL_CUDA(launch_glu_few(g->in_type, a, g->units.sms, static_cast<cudaStream_t>(stream)), "feed-forward");
     return TFL_OK;
   }
   const int ke = f8 ? 128 : 64, num_k = (g->D + ke - 1) / ke;
-  const GluPlan p = glu_plan(GLU_FORWARD, f8, tokens, g->F, num_k, g->num_sms, g->pairs);
+  const GluPlan p = glu_plan(GLU_FORWARD, f8, tokens, g->F, num_k, g->units);
   GluMaps mp;
   if (!make_map(&mp.a0, x, tokens, g->D, (int)es, p.a_rows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bno) ||
       !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bno))
@@ -393,9 +411,9 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
 
   const int Di = g->D, Fi = g->F, Ti = (int)tokens;
   const int kd = (Di + 63) / 64, kf = (Fi + 63) / 64, kt = (Ti + 63) / 64;
-  const GluPlan p1 = glu_plan(GLU_SLOPES, false, tokens, Fi, kd, g->num_sms, g->pairs);
-  const GluPlan p2 = glu_plan(GLU_DX, false, tokens, Di, 2 * kf, g->num_sms, g->pairs);
-  const GluPlan p3 = glu_plan(GLU_DW, false, Fi, Di, kt, g->num_sms, g->pairs);
+  const GluPlan p1 = glu_plan(GLU_SLOPES, false, tokens, Fi, kd, g->units);
+  const GluPlan p2 = glu_plan(GLU_DX, false, tokens, Di, 2 * kf, g->units);
+  const GluPlan p3 = glu_plan(GLU_DW, false, Fi, Di, kt, g->units);
   GluMaps m1, m2, m3;
   bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bno) &&
             make_map(&m1.b1, wu, Fi, Di, 2, p1.bno);

@@ -187,12 +187,18 @@ __device__ __forceinline__ Tile tile_at(int t, int num_m, int num_n) {
   return r;
 }
 
-// WIDE: tiles of kMaxBN accumulator columns and 128 loaded rows of A, all sizes constants;
-// otherwise the plan's widths.
-template <int CG, int MODE, bool F8, bool WIDE>
+// kWide: tiles of kMaxBN accumulator columns and 128 loaded rows of A, all sizes constants.
+// kNarrow: the plan's widths.
+// kSplit: the same, with the k-blocks of a tile shared out to a cluster of lone CTAs (few tiles:
+// the whole GPU works on them); each CTA finishes some of the tile's 32-column pieces, and the
+// others send it their sums through its shared memory, added in CTA order.  One tile a CTA.
+enum GluForm : int { kWide = 0, kNarrow = 1, kSplit = 2 };
+template <int CG, int MODE, bool F8, int FORM>
 __global__ void __launch_bounds__(kGluThreads, 1)
     glu_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GluArgs args) {
+  constexpr bool WIDE = FORM == kWide, SPLIT = FORM == kSplit;
+  static_assert(!SPLIT || CG == 1, "lone CTAs share a tile's k-blocks");
   constexpr bool TWO = MODE == GLU_FORWARD || MODE == GLU_SLOPES;  // two products side by side
   constexpr bool A_MN = MODE == GLU_DW, B_MN = MODE == GLU_DX || MODE == GLU_DW;
   constexpr int KE = F8 ? 128 : 64;                                // k elements a stage
@@ -244,8 +250,9 @@ __global__ void __launch_bounds__(kGluThreads, 1)
 
   const int num_m = (args.M + kGluRows * CG - 1) / (kGluRows * CG), num_n = (args.N + bno - 1) / bno;
   const int total = num_m * num_n * (MODE == GLU_DW ? 2 : 1);
-  const int unit = blockIdx.x / CG, units = gridDim.x / CG;
-  const int num_k = args.num_k;
+  const int split = SPLIT ? args.split : 1, part = SPLIT ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / (CG * split), units = gridDim.x / (CG * split);
+  const int kb0 = args.num_k * part / split, kb1 = args.num_k * (part + 1) / split;  // this CTA's k-blocks
 
   uint32_t issued_mask = 0, issued_par = 0;  // stages with loads in flight (abort path)
   bool mma_issued = false;
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       for (int t = unit; t < total && ok; t += units) {
         const Tile tl = tile_at(t, num_m, num_n);
         const int m0 = (tl.m * CG + rank) * kGluRows;
-        for (int kb = 0; kb < num_k; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
@@ -306,6 +313,11 @@ __global__ void __launch_bounds__(kGluThreads, 1)
         }
       }
     }
+    if constexpr (SPLIT) {  // the two meetings of the epilogue below
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = (1u << 4) | (args.bf16_operands ? (1u << 7) | (1u << 10) : 0u) |
@@ -323,7 +335,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
         if (!wait_bounded(&acce[acc], acc_phase ^ 1u, wc)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * kMaxBN);
-        for (int kb = 0; kb < num_k; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(&full[stage], phase, wc)) {
             ok = false;
             break;
@@ -331,7 +343,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
           tc_fence_after();
           const uint32_t at = (uint32_t)(stage * (stage_bytes >> 4));
           const uint64_t ad = ad0 + at, bd = bd0 + at;
-          umma_cg<CG, F8>(d, ad, bd, idesc, kb != 0);
+          umma_cg<CG, F8>(d, ad, bd, idesc, kb != kb0);
 #pragma unroll
           for (int k = 1; k < 4; ++k)
             umma_cg<CG, F8>(d, ad + (uint32_t)(k * (A_MN ? 2048 : 32) >> 4), bd + (uint32_t)(k * (B_MN ? 2048 : 32) >> 4),
@@ -350,6 +362,11 @@ __global__ void __launch_bounds__(kGluThreads, 1)
           acc_phase ^= 1u;
         }
       }
+    }
+    if constexpr (SPLIT) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
     }
   } else {
     // ------------------------------------------------------------ epilogue (8 warps)
@@ -378,10 +395,11 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       };
       if constexpr (F8) {
         sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
-        fetch_scales(half);
+        fetch_scales(part + split * half);
       }
       const bool ok = wait_bounded(&accf[acc], acc_phase, wc);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      // (a split tile's CTAs meet all the same: its outputs are invalid then, as the status says)
+      if (!__all_sync(0xffffffffu, ok) && !SPLIT) break;
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxBN);
       const int chunks = (bno + W - 1) / W;
@@ -396,9 +414,39 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             mbar_arrive(&acce[acc]);
         }
       };
-      if (half > last) hand_back();
+      if (!SPLIT && half > last) hand_back();
+      // kSplit: piece c is finished by CTA c % split.  Its sums from another CTA lie in the ring of
+      // that CTA, idle by now: [other CTAs][pieces][8, or 2 x 8, parts of a row][128 rows][4 floats], so
+      // that a warp's stores and loads are of whole lines.
+      constexpr int kPart = kGluRows * 16, kPiece = (TWO ? 16 : 8) * kPart;
+      const int pieces = SPLIT ? (chunks + split - 1) / split : 0;
+      if constexpr (SPLIT) {
+        cluster_sync();  // every CTA of the tile has its sums, and an idle ring
+        tc_fence_after();
+        for (int c = 0, i = 0; c < chunks; ++c) {
+          const int owner = c % split;
+          if (owner == part || (i++ & 1) != half) continue;
+          float g[W], u[W];
+          tmem_ld32(tb + c * W, g);
+          if constexpr (TWO) tmem_ld32(tb + bno + c * W, u);
+          tmem_wait_ld();
+          const int slot = part < owner ? part : part - 1;
+          const uint32_t to =
+              map_rank(smem, owner) + (uint32_t)((slot * pieces + c / split) * kPiece + (q * 32 + lane) * 16);
+          if (m < args.M) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              store_cluster(to + k * kPart, g[4 * k], g[4 * k + 1], g[4 * k + 2], g[4 * k + 3]);
+              if constexpr (TWO)
+                store_cluster(to + (8 + k) * kPart, u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+            }
+          }
+        }
+        __syncwarp();
+        cluster_sync();  // the sums have arrived
+      }
 #pragma unroll 1
-      for (int c = half; c < chunks; c += 2) {
+      for (int c = part + split * half; c < chunks; c += 2 * split) {
         const int n0 = n_tile + c * W;                       // first output column
         const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
         uint4 o[W / 8], o2[W / 8];
@@ -412,7 +460,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             sc[W + i * 32 + lane] = su[i];
           }
           __syncwarp();
-          if (c + 2 < chunks) fetch_scales(c + 2);
+          if (c + 2 * split < chunks) fetch_scales(c + 2 * split);
         }
 #pragma unroll
         for (int b = 0; b < W / LD; ++b) {
@@ -422,7 +470,21 @@ __global__ void __launch_bounds__(kGluThreads, 1)
           if constexpr (TWO) tmem_ld32(tb + bno + col, u);
           tmem_wait_ld();
           // once the accumulator is in registers it is handed back, before arithmetic and stores
-          if (b == W / LD - 1 && c == last) hand_back();
+          if (!SPLIT && b == W / LD - 1 && c == last) hand_back();
+          if constexpr (SPLIT) {
+            for (int k = 0; k < split - 1; ++k) {
+              const uint8_t* from = smem + (k * pieces + c / split) * kPiece + (q * 32 + lane) * 16;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 a = *reinterpret_cast<const float4*>(from + i * kPart);
+                g[4 * i] += a.x, g[4 * i + 1] += a.y, g[4 * i + 2] += a.z, g[4 * i + 3] += a.w;
+                if constexpr (TWO) {
+                  const float4 e = *reinterpret_cast<const float4*>(from + (8 + i) * kPart);
+                  u[4 * i] += e.x, u[4 * i + 1] += e.y, u[4 * i + 2] += e.z, u[4 * i + 3] += e.w;
+                }
+              }
+            }
+          }
           if constexpr (F8) {
             const float* sc = reinterpret_cast<const float*>(st) + b * LD;
 #pragma unroll
@@ -482,24 +544,26 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     }
     __syncthreads();
   }
-  if constexpr (CG == 2) cluster_sync();  // nothing of the peer reaches this CTA any more
+  if constexpr (CG == 2) cluster_sync();  // nothing of the peer reaches this CTA any more (a split tile's CTAs met after the last)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_cg<CG>(tmem_base, 2 * kMaxBN);
   }
 }
 
-template <int CG, int MODE, bool F8, bool WIDE>
+template <int CG, int MODE, bool F8, int FORM>
 cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStream_t s) {
   a.bno = p.bno;
+  a.split = p.split;
   const int bn = (MODE == GLU_FORWARD || MODE == GLU_SLOPES) ? 2 * p.bno : p.bno;
   const bool b_mn = MODE == GLU_DX || MODE == GLU_DW;
   a.a_bytes = p.a_rows * kKBytes;
   a.stage_bytes = a.a_bytes + (b_mn ? (bn / CG + 63) / 64 * kMnChunk : bn / CG * kKBytes);
-  a.stages = ring_bytes(WIDE) / a.stage_bytes;
+  a.stages = ring_bytes(FORM == kWide) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
+  const int cluster = CG * p.split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * CG);
+  cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * cluster);
   cfg.blockDim = dim3(kGluThreads);
   cfg.dynamicSmemBytes = kGluSmem;
   cfg.stream = s;
@@ -507,49 +571,53 @@ cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStrea
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = CG;
+  at[1].val.clusterDim.x = cluster;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = CG == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, glu_kernel<CG, MODE, F8, WIDE>, mp.a0, mp.a1, mp.b0, mp.b1, a);
+  cfg.numAttrs = cluster == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, glu_kernel<CG, MODE, F8, FORM>, mp.a0, mp.a1, mp.b0, mp.b1, a);
 }
 
-template <int CG, int MODE, bool F8>
+template <int CG, int MODE, bool F8, int FORM>
 cudaError_t prepare_one() {
-  cudaError_t e = cudaFuncSetAttribute(glu_kernel<CG, MODE, F8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kGluSmem);
-  if (CG == 2 && e == cudaSuccess)
-    e = cudaFuncSetAttribute(glu_kernel<2, MODE, F8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGluSmem);
-  return e;
+  return cudaFuncSetAttribute(glu_kernel<CG, MODE, F8, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGluSmem);
 }
 
-}  // namespace
-
-// Every (CTA group, mode, operand form); pairs also in the WIDE form.
-#define TFL_GLU_VARIANTS(X)                                                                         \
-  X(1, GLU_FORWARD, false) X(1, GLU_FORWARD, true) X(1, GLU_SLOPES, false) X(1, GLU_DX, false)      \
-  X(1, GLU_DW, false) X(2, GLU_FORWARD, false) X(2, GLU_FORWARD, true) X(2, GLU_SLOPES, false)      \
-  X(2, GLU_DX, false) X(2, GLU_DW, false)
-
-cudaError_t prepare_glu_kernels(int* pairs) {
-  cudaError_t e = cudaSuccess;
-#define TFL_PREP(CG, MODE, F8) \
-  if (e == cudaSuccess) e = prepare_one<CG, MODE, F8>();
-  TFL_GLU_VARIANTS(TFL_PREP)
-#undef TFL_PREP
-  if (e != cudaSuccess) return e;
-  // CTA pairs the GPU holds at once (a pair stays within a GPU processing cluster): one each
+// Clusters of `size` CTAs that the GPU holds at once, one CTA an SM (a cluster stays within a GPU
+// processing cluster, so fewer than SMs / size may fit).
+template <int CG, int FORM>
+cudaError_t clusters_at_once(int size, int* n) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2);
+  cfg.gridDim = dim3(size);
   cfg.blockDim = dim3(kGluThreads);
   cfg.dynamicSmemBytes = kGluSmem;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 2;
+  at.val.clusterDim.x = size;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, glu_kernel<2, GLU_FORWARD, false, true>, &cfg);
+  return cudaOccupancyMaxActiveClusters(n, glu_kernel<CG, GLU_FORWARD, false, FORM>, &cfg);
+}
+
+}  // namespace
+
+// Every (mode, operand form) in every (CTAs of a tile, form).
+#define TFL_GLU_MODES(X, CG, FORM)                                                                  \
+  X(CG, GLU_FORWARD, false, FORM) X(CG, GLU_FORWARD, true, FORM) X(CG, GLU_SLOPES, false, FORM)     \
+  X(CG, GLU_DX, false, FORM) X(CG, GLU_DW, false, FORM)
+#define TFL_GLU_VARIANTS(X) \
+  TFL_GLU_MODES(X, 2, kWide) TFL_GLU_MODES(X, 2, kNarrow) TFL_GLU_MODES(X, 1, kNarrow) TFL_GLU_MODES(X, 1, kSplit)
+
+cudaError_t prepare_glu_kernels(GluUnits* u) {
+  cudaError_t e = cudaSuccess;
+#define TFL_PREP(CG, MODE, F8, FORM) \
+  if (e == cudaSuccess) e = prepare_one<CG, MODE, F8, FORM>();
+  TFL_GLU_VARIANTS(TFL_PREP)
+#undef TFL_PREP
+  if (e == cudaSuccess) e = clusters_at_once<2, kWide>(2, &u->pairs);
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = clusters_at_once<1, kSplit>(2 << i, &u->splits[i]);
+  return e;
 }
 
 // CTA pairs take tiles of 256 rows: each CTA stages half of B, so a k-block of a 256 x 256 tile
@@ -559,27 +627,53 @@ cudaError_t prepare_glu_kernels(int* pairs) {
 // Fewer than 128 rows of A: only those (to the next 8) are loaded and given room in the ring; the
 // MMA still reads 128, the others being whatever lies behind, and their results are not stored.
 //
-// The tile's width goes by rounds: a launch takes ceil(tiles / units) of them, each about as
-// long as a k-block's products (a 256-column accumulator: 555 cycles measured) or its operand
-// stream from L2 (62 bytes a cycle and SM measured), whichever is longer, and narrower tiles
-// can trade a mostly empty last round for a little more of either.
-GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, int num_sms, int pairs) {
+// The cut goes by an estimate of the cycles a launch takes, from what was measured:
+//   a k-block costs its products (a 256-column accumulator: 555), its operand stream from L2 (62
+//   bytes a cycle and SM) or issuing its four MMAs and commit (500), whichever is longest;
+//   a round of tiles costs its k-blocks or its share of what has to come from memory (3566 bytes a
+//   cycle, the copy bandwidth, which fewer than about 130 SMs do not draw), whichever is longer,
+//   and a fifth of the other;
+//   the last tile's epilogue is not hidden: 1300 for each turn of its two warps of a lane quarter;
+//   sharing a tile's k-blocks out to a cluster costs two meetings (2500) and the exchange of the
+//   sums (10 bytes a cycle and CTA); the pieces have to fit in the ring.
+// So wide tiles where there are rounds of them, narrower ones where that fills a last round or
+// spreads the weights of a few rows over all SMs, and shared k-blocks where the tiles are few and
+// the rows long (60 tokens x 2048 x 8192 backward: 110 -> 57 us, most of it dx).
+GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, const GluUnits& u) {
   const bool two = mode == GLU_FORWARD || mode == GLU_SLOPES;
+  const int64_t twice = mode == GLU_DW ? 2 : 1;
+  const double memory = (double)(M * twice + (two ? 2 : 1) * N) * num_k * kKBytes / 3566.0;
   GluPlan best;
   double best_cost = 0;
-  for (int cg = M > kGluRows ? 2 : 1; cg >= 1; --cg) {
-    const int64_t units = cg == 2 ? pairs : num_sms, num_m = (M + kGluRows * cg - 1) / (kGluRows * cg);
+  for (int form = 0; form < 5; ++form) {  // pairs; lone CTAs; clusters of 2, 4, 8 lone CTAs
+    const int cg = form == 0 ? 2 : 1, split = form < 2 ? 1 : 1 << (form - 1);
+    if ((cg == 2 && M <= kGluRows) || (split > 1 && num_k < 2 * split)) continue;
+    const int64_t units = form == 0 ? u.pairs : form == 1 ? u.sms : u.splits[form - 2];
+    if (units < 1) continue;
+    const int64_t num_m = (M + kGluRows * cg - 1) / (kGluRows * cg);
     const int64_t rows = M < kGluRows ? M : kGluRows;  // rows of A outside the matrix cost no reads
     // tcgen05.mma takes N in steps of 16, a pair's in steps of 32
     for (int bn = kMaxBN; bn >= 32; bn -= 16 * cg) {
-      const int bno = two ? bn / 2 : bn;
-      const int64_t tiles = num_m * ((N + bno - 1) / bno) * (mode == GLU_DW ? 2 : 1);
-      const int64_t rounds = (tiles + units - 1) / units;
-      const double products = 555.0 * bn / kMaxBN / (f8 ? 2 : 1);
+      const int bno = two ? bn / 2 : bn, chunks = (bno + 31) / 32;
+      const int64_t tiles = num_m * ((N + bno - 1) / bno) * twice;
+      const int64_t rounds = (tiles + units - 1) / units, last = tiles - (rounds - 1) * units;
+      const int pieces = (chunks + split - 1) / split;
+      if (split > 1 && (rounds > 1 || (split - 1) * pieces * kGluRows * (two ? 256 : 128) > ring_bytes(false))) continue;
+      double block = 555.0 * bn / kMaxBN / (f8 ? 2 : 1);
       const double stream = (double)(rows + bn / cg) * kKBytes / 62.0;
-      const double cost = rounds * (num_k * (products > stream ? products : stream) + 1500.0);
+      if (block < stream) block = stream;
+      if (block < 500.0) block = 500.0;
+      const double products = (double)((num_k + split - 1) / split) * block;
+      auto round = [&](int64_t n) {  // n tiles at once
+        const double active = (double)n * cg * split;
+        const double read = memory * n / tiles * (active < 130.0 ? 130.0 / active : 1.0);
+        return products > read ? products + 0.2 * read : read + 0.2 * products;
+      };
+      double cost = (rounds - 1) * (round(units) + 500.0) + round(last) + 500.0 + 1300.0 * ((pieces + 1) / 2);
+      if (split > 1) cost += 2500.0 + (double)rows * bn * 4 * (split - 1) / split / 10.0;
       if (!best.cg || cost < best_cost * 0.97) {
         best.cg = cg;
+        best.split = split;
         best.a_rows = M < kGluRows && mode != GLU_DW ? (int)((M + 7) / 8 * 8) : kGluRows;
         best.bno = bno;
         best.units = (int)units;
@@ -593,9 +687,9 @@ GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, int num
 
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s) {
   const bool wide = p.bno == (mode == GLU_FORWARD || mode == GLU_SLOPES ? kMaxBN / 2 : kMaxBN);
-#define TFL_LAUNCH(CG, MODE, F8)                               \
-  if (p.cg == CG && mode == MODE && f8 == F8)                  \
-    return CG == 2 && wide ? launch_one<CG, MODE, F8, CG == 2>(mp, a, p, s) : launch_one<CG, MODE, F8, false>(mp, a, p, s);
+  const int form = p.split > 1 ? kSplit : p.cg == 2 && wide ? kWide : kNarrow;
+#define TFL_LAUNCH(CG, MODE, F8, FORM) \
+  if (p.cg == CG && form == FORM && mode == MODE && f8 == F8) return launch_one<CG, MODE, F8, FORM>(mp, a, p, s);
   TFL_GLU_VARIANTS(TFL_LAUNCH)
 #undef TFL_LAUNCH
   return cudaErrorInvalidValue;

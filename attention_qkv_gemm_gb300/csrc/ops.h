@@ -53,7 +53,7 @@ struct GluArgs {
   int M = 0, N = 0;              // rows and columns of the output
   int num_k = 0;                 // k-blocks of a tile
   int k_half = 0;                // DX: k-blocks of the first product
-  int bno = 0, stages = 0, stage_bytes = 0, a_bytes = 0;  // set by the launcher from the plan
+  int bno = 0, split = 1, stages = 0, stage_bytes = 0, a_bytes = 0;  // set by the launcher from the plan
   int act = 0;
   int bf16_operands = 0;         // 16-bit operands: bf16, else fp16
   int bf16_out = 0;              // 16-bit outputs (and dh): bf16, else fp16
@@ -69,15 +69,20 @@ constexpr int kGluRows = 128;  // rows of A a CTA takes
 struct GluMaps {
   CUtensorMap a0, a1, b0, b1;
 };
-// How a call is cut: CTAs that share a tile, output columns of a tile, tiles that run at once,
+// How a call is cut: CTAs of a pair (2) or lone ones (1), lone CTAs that share a tile's k-blocks,
+// output columns of a tile, tiles that run at once,
 // rows of A a CTA loads for a tile, tiles in all.
 struct GluPlan {
-  int cg = 0, bno = 0, units = 0, a_rows = 0;
+  int cg = 0, split = 1, bno = 0, units = 0, a_rows = 0;
   int64_t tiles = 0;
 };
-GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, int num_sms, int pairs);
-// Kernel attributes; *pairs: CTA pairs that the current device runs at once.
-cudaError_t prepare_glu_kernels(int* pairs);
+// What runs at once on a device: lone CTAs, CTA pairs, clusters of 2, 4 and 8 lone CTAs.
+struct GluUnits {
+  int sms = 0, pairs = 0, splits[3] = {};
+};
+GluPlan glu_plan(int mode, bool f8, int64_t M, int64_t N, int64_t num_k, const GluUnits& u);
+// Kernel attributes, and all of *u but sms for the current device.
+cudaError_t prepare_glu_kernels(GluUnits* u);
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s);
 
 // The forward for at most kGluFewTokens tokens (glu_few.cu).

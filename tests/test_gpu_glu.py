@@ -104,7 +104,9 @@ def _forward(tokens, d, f, t, act, seed=0):
 # tiles than the GPU holds at a time
 SIZES = [(1, 8, 8), (1, 1024, 520), (3, 72, 16), (8, 264, 40), (9, 1000, 136), (16, 512, 24), (17, 64, 256),
          (33, 136, 1000), (64, 2056, 128), (65, 64, 136), (127, 72, 136), (128, 64, 128), (129, 200, 264),
-         (300, 1160, 712), (513, 64, 1000), (4100, 72, 1032)]
+         (300, 1160, 712), (513, 64, 1000), (4100, 72, 1032),
+         # few tiles of long rows: several CTAs share a tile's sum
+         (20, 4104, 72), (100, 2056, 520), (128, 1096, 4096), (300, 4096, 264)]
 
 
 @pytest.mark.parametrize("tokens,d,f", SIZES)
@@ -131,7 +133,7 @@ def _rows8(t):
 
 
 @pytest.mark.parametrize("tokens,d,f", [(1, 16, 16), (1, 2064, 528), (7, 144, 32), (16, 1024, 48), (33, 144, 272),
-                                        (100, 4112, 144), (200, 1024, 512), (4100, 144, 1040)])
+                                        (100, 4112, 144), (30, 8192, 544), (200, 1024, 512), (4100, 144, 1040)])
 @pytest.mark.parametrize("t,act", [("bf16", "silu"), ("f16", "gelu")])
 def test_forward_of_e4m3_operands(tokens, d, f, t, act):
     import torch
@@ -175,7 +177,8 @@ def _backward(tokens, d, f, t, act, seed=0, room=5):
 
 @pytest.mark.parametrize("tokens,d,f", [(1, 8, 8), (1, 264, 72), (3, 72, 16), (65, 64, 136), (128, 256, 64),
                                         (129, 200, 264), (300, 1160, 712), (1000, 72, 328), (70, 1000, 2568),
-                                        (5000, 2056, 72)])
+                                        (5000, 2056, 72), (20, 520, 2056), (5, 2056, 1032), (200, 264, 4104),
+                                        (6000, 136, 200)])
 @pytest.mark.parametrize("t,act", [("bf16", "silu"), ("f16", "gelu")])
 def test_backward(tokens, d, f, t, act):
     got = _backward(tokens, d, f, t, act, seed=tokens + f)
