@@ -3,7 +3,6 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
-#include <map>
 #include <mutex>
 #include <new>
 
@@ -45,6 +44,16 @@ int usable_device(int* dev, int* num_sms) {
     return fail(TFL_ERR_UNSUPPORTED, "device is sm_" + std::to_string(major) + std::to_string(minor) +
                                          "; this library is built for sm_103a (GB300)");
   return TFL_OK;
+}
+
+// Frees a handle's memory with its device current, after what still runs there.
+void release(int device, void* p) {
+  int dev = device;
+  cudaGetDevice(&dev);
+  if (dev != device) cudaSetDevice(device);
+  cudaDeviceSynchronize();
+  if (p) cudaFree(p);
+  if (dev != device) cudaSetDevice(dev);
 }
 
 int same_device(int device) {
@@ -200,8 +209,7 @@ int tfl_rmsnorm_backward(tfl_rmsnorm* n, int64_t rows, const void* sum, const fl
 
 void tfl_rmsnorm_destroy(tfl_rmsnorm* n) {
   if (!n) return;
-  cudaDeviceSynchronize();
-  if (n->partial) cudaFree(n->partial);
+  release(n->device, n->partial);
   delete n;
 }
 
@@ -236,17 +244,17 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int 
 
 // Kernel attributes and what runs at once on a device: the same for every handle, asked once.
 int glu_units(int dev, int sms, GluUnits* u) {
+  constexpr int kDevices = 64;
   static std::mutex lock;
-  static std::map<int, GluUnits> known;
+  static GluUnits known[kDevices];
   std::lock_guard<std::mutex> hold(lock);
-  const auto it = known.find(dev);
-  if (it != known.end()) {
-    *u = it->second;
+  if (dev < kDevices && known[dev].sms) {
+    *u = known[dev];
     return TFL_OK;
   }
-  u->sms = sms;
   TFL_CUDA(prepare_glu_kernels(u), "feed-forward kernel attributes");
-  known[dev] = *u;
+  u->sms = sms;
+  if (dev < kDevices) known[dev] = *u;
   return TFL_OK;
 }
 
@@ -469,8 +477,7 @@ int tfl_glu_status(tfl_glu* g, tfl_stream stream) {
 
 void tfl_glu_destroy(tfl_glu* g) {
   if (!g) return;
-  cudaDeviceSynchronize();
-  if (g->status) cudaFree(g->status);
+  release(g->device, g->status);
   delete g;
 }
 

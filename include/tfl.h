@@ -456,8 +456,9 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
  * nothing is kept between the two calls) and dh [tokens, d_ff]:
  *   dg = dh u act'(g),  du = dh act(g),  g = x Wg^T,  u = x Wu^T
  *   dx = dg Wg + du Wu  [tokens, d_model],  dwg = dg^T x,  dwu = du^T x  [d_ff, d_model]
- * All of the operands' 16-bit type; dg and du are rounded to it once, sums are
- * fp32, each gradient is rounded once.  Outputs are written in full (dwg, dwu:
+ * All of the operands' 16-bit type; dg and du are rounded to it once (in fp16
+ * they overflow past 65504: scale the loss), sums are fp32, each gradient is
+ * rounded once.  Outputs are written in full (dwg, dwu:
  * zeros for 0 tokens) and must not overlap anything.  No atomics: the same
  * inputs give the same bits.  Calls on one handle share its scratch and must not
  * overlap on the GPU (graphs that hold such calls included).
