@@ -10,6 +10,10 @@
 // common widths need no block barrier).  Sums are fp32: a thread's own elements in order, then
 // a butterfly, so a row's result does not depend on the other rows.
 //
+// Measured: 100000 x 1024 bf16 to e4m3 106 us (the copy bandwidth), 8192 x 1024 fp16 with an fp32
+// residual 18.3 us (0.81 of it), one row 2.7 us in a graph; backward 20011 x 4096 fp16 110 us (0.88),
+// 8192 x 1024 bf16 / fp32 25.7 us (0.77, 4 us of it the second launch for dgamma).
+//
 // The e4m3 form divides a row by its scale = max|y| / 448 (448 is e4m3's largest value) and
 // rounds once; max|y| = r max|s gamma| comes from the same pass as the sum of squares.
 //
@@ -281,8 +285,9 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int tpr, int group,
 //
 // Three streams in and one or two out bound it, so loads have to stay in flight while a row is
 // reduced and written: the next row is loaded, as stored, before the current one is worked on
-// (20011 x 4096 fp16 229 -> 150 us), and the arithmetic runs on packed fp32 pairs.  A ring of rows
-// in shared memory filled by cp.async holds more bytes in flight but was slower: 161 us, and 39
+// (20011 x 4096 fp16 229 -> 150 us).  Instructions come next: packed fp32 pairs, the two sums folded
+// into one butterfly, pointers carried along (150 -> 110 us).  A ring of rows in shared memory filled
+// by cp.async holds more bytes in flight but was slower: 161 us where this form took 150, and 39
 // against 28 us at 8192 x 1024.
 template <class X, class R, int NV, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const RmsGradArgs a) {
