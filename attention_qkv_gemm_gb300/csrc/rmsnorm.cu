@@ -433,26 +433,37 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const Rms
   }
 }
 
-// dgamma[c] = sum over the blocks' partial rows: 8 columns a block (enough blocks for the whole
-// GPU at the common widths), 128 threads a column with all their loads at once.
-__global__ void __launch_bounds__(1024) rms_dgamma_kernel(const float* partial, int n, int D, float* dgamma) {
-  __shared__ float red[128][9];
+// dgamma[c] = sum over the blocks' partial rows: C columns a block, Y threads a column with all their
+// loads at once, joined in a fixed order.  8 x 128 for the partial rows of a whole GPU (enough blocks
+// for it at the common widths), 32 x 8 for those of a few blocks.
+template <int C, int Y>
+__global__ void __launch_bounds__(C * Y) rms_dgamma_kernel(const float* partial, int n, int D, float* dgamma) {
+  __shared__ float red[Y][C + 1];
   grid_launch_dependents();
   grid_wait_prior();
-  const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
+  const int x = threadIdx.x % C, y = threadIdx.x / C, c = blockIdx.x * C + x;
   float v = 0.f;
   if (c < D) {
-#pragma unroll 5
-    for (int i = y; i < n; i += 128) v += partial[(size_t)i * D + c];
+#pragma unroll 8
+    for (int i = y; i < n; i += Y) v += partial[(size_t)i * D + c];
   }
   red[y][x] = v;
   __syncthreads();
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;  // warp w < 8 adds up column w
-  if (w >= 8) return;
-  v = (red[lane][w] + red[lane + 32][w]) + (red[lane + 64][w] + red[lane + 96][w]);
+  if constexpr (Y >= 32) {  // warp w < C adds up column w
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (w >= C) return;
+    v = 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0 && blockIdx.x * 8 + w < D) dgamma[blockIdx.x * 8 + w] = v;
+    for (int i = 0; i < Y / 32; ++i) v += red[lane + 32 * i][w];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * C + w < D) dgamma[blockIdx.x * C + w] = v;
+  } else if (y == 0 && c < D) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < Y; ++i) v += red[i][x];
+    dgamma[c] = v;
+  }
 }
 
 // ---- element-wise forms: any width and element-aligned buffers, one block a row
@@ -531,16 +542,31 @@ __global__ void __launch_bounds__(T) rms_backward_values_kernel(const RmsGradArg
   float dg[NE];
 #pragma unroll
   for (int j = 0; j < NE; ++j) dg[j] = 0.f;
+  constexpr bool AHEAD = NE <= 4;  // room for the next row, loaded as stored before this one is worked on
+  R s1[NE], e1[NE];
+  X y1[NE];
+  auto fetch = [&](int64_t row) {
+    const size_t base = (size_t)row * a.D + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const bool in = row < a.rows && (int)threadIdx.x + j * T < a.D;
+      s1[j] = in ? static_cast<const R*>(a.sum)[base + j * T] : R(0.f);
+      y1[j] = in ? static_cast<const X*>(a.dy)[base + j * T] : X(0.f);
+      e1[j] = in && a.dres ? static_cast<const R*>(a.dres)[base + j * T] : R(0.f);
+    }
+  };
+  if (AHEAD) fetch(blockIdx.x);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const size_t base = (size_t)row * a.D + threadIdx.x;
     float s[NE], y[NE], e[NE], v[2] = {0.f, 0.f};
+    if (!AHEAD) fetch(row);
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      const bool in = (int)threadIdx.x + j * T < a.D;
-      s[j] = in ? value(static_cast<const R*>(a.sum)[base + j * T]) : 0.f;
-      y[j] = in ? value(static_cast<const X*>(a.dy)[base + j * T]) : 0.f;
-      e[j] = in && a.dres ? value(static_cast<const R*>(a.dres)[base + j * T]) : 0.f;
+      s[j] = value(s1[j]);
+      y[j] = value(y1[j]);
+      e[j] = value(e1[j]);
     }
+    if (AHEAD) fetch(row + gridDim.x);
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
       const int c = threadIdx.x + j * T;
@@ -646,17 +672,27 @@ cudaError_t forward(RmsArgs a, int num_sms, cudaStream_t s) {
   return launch_dependent(rms_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
 }
 
+// Blocks of a backward over groups of rows: what the GPU holds at once, and one alone for so few that
+// a second launch would cost more than their turns; a lone block writes dgamma itself.
+int backward_blocks(RmsGradArgs& a, int64_t groups_of_rows, int at_once) {
+  int64_t n = at_once < a.blocks ? at_once : a.blocks;
+  if (groups_of_rows < n) n = groups_of_rows <= 3 ? 1 : groups_of_rows;
+  if (n == 1) a.partial = a.dgamma;
+  return (int)n;
+}
+
 cudaError_t add_partials(const RmsGradArgs& a, int n, cudaStream_t s) {
-  return launch_dependent(rms_dgamma_kernel, (a.D + 7) / 8, 1024, 0, s, (const float*)a.partial, n, a.D, a.dgamma);
+  if (n == 1) return cudaSuccess;
+  const float* p = a.partial;
+  if (n <= 64) return launch_dependent(rms_dgamma_kernel<32, 8>, (a.D + 31) / 32, 256, 0, s, p, n, a.D, a.dgamma);
+  return launch_dependent(rms_dgamma_kernel<8, 128>, (a.D + 7) / 8, 1024, 0, s, p, n, a.D, a.dgamma);
 }
 
 template <class X, class R, int NV, int THREADS, int BLOCKS>
 cudaError_t backward_with(RmsGradArgs a, int num_sms, cudaStream_t s) {
   a.tpr = pow2_at_least((a.D / 8 + NV - 1) / NV);
   const int groups = THREADS / a.tpr;
-  const int64_t need = (a.rows + groups - 1) / groups;
-  int grid = num_sms * BLOCKS < a.blocks ? num_sms * BLOCKS : a.blocks;  // what the GPU holds at once
-  if (need < grid) grid = (int)need;
+  const int grid = backward_blocks(a, (a.rows + groups - 1) / groups, num_sms * BLOCKS);
   const size_t smem = groups > 1 ? (size_t)groups * a.D * sizeof(float) : 0;  // at most 8 KB
   const cudaError_t e = launch_dependent(rms_backward_kernel<X, R, NV, THREADS, BLOCKS>, grid, THREADS, smem, s, a);
   return e == cudaSuccess ? add_partials(a, grid, s) : e;
@@ -716,11 +752,12 @@ cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s) {
   });
 }
 
-cudaError_t launch_rms_backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_rms_backward(const RmsGradArgs& args, int num_sms, cudaStream_t s) {
+  RmsGradArgs a = args;
   const bool vec = a.D % 8 == 0 && a.D <= kRmsMaxRegisterRow / 2 && aligned(a.sum, 16) && aligned(a.gamma, 16) && aligned(a.dy, 16) &&
                    aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
   if (!vec) {
-    const int grid = (int)(a.rows < a.blocks ? a.rows : a.blocks);
+    const int grid = backward_blocks(a, a.rows, num_sms * 4);
     const cudaError_t e =
         a.D > kRmsMaxValues
             ? launch_dependent(rms_backward_any_kernel, grid, 256, 0, s, a)
@@ -728,7 +765,8 @@ cudaError_t launch_rms_backward(const RmsGradArgs& a, int num_sms, cudaStream_t 
                 using X = decltype(x);
                 using R = decltype(r);
                 if (a.D <= 1024) return launch_dependent(rms_backward_values_kernel<X, R, 256, 4>, grid, 256, 0, s, a);
-                if (a.D <= 4096) return launch_dependent(rms_backward_values_kernel<X, R, 512, 8>, grid, 512, 0, s, a);
+                if (a.D <= 2048) return launch_dependent(rms_backward_values_kernel<X, R, 512, 4>, grid, 512, 0, s, a);
+                if (a.D <= 4096) return launch_dependent(rms_backward_values_kernel<X, R, 1024, 4>, grid, 1024, 0, s, a);
                 return launch_dependent(rms_backward_values_kernel<X, R, 1024, 8>, grid, 1024, 0, s, a);
               });
     return e == cudaSuccess ? add_partials(a, grid, s) : e;
