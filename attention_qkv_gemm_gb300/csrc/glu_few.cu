@@ -84,8 +84,14 @@ __global__ void __launch_bounds__(256) glu_few_kernel(const GluFewArgs a) {
       }
     }
   };
-  grid_wait_prior();
   int base = warp * (kUnroll * 64);
+  // The weights of the first steps set out for L2 while the kernels before this one still run (what
+  // they write is only read after the wait): one line a lane, two of each of the warp's 16 rows.
+  {
+    const int row = f0 + (lane & 7), off = base + (lane >> 4) * 128;
+    if (off < row_bytes) prefetch_l2((lane & 8 ? a.wu : a.wg) + (size_t)row * row_bytes + off);
+  }
+  grid_wait_prior();
   for (; base + kUnroll * 64 <= row_bytes; base += warps * (kUnroll * 64)) steps(base, std::true_type());
   if (base < row_bytes) steps(base, std::false_type());
 #pragma unroll
