@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(1024) rms_forward_kernel(const RmsArgs a) {
 // Both sums of a row, for a group that loops over its rows on its own: groups wider than a warp
 // meet at a named barrier of their own, once a row (the buffers alternate).  Inside a warp the two
 // sums are folded into one first: half of the lanes go on with each.
+template <int WARPS = 16>  // of the widest group
 __device__ __forceinline__ void row_sums(float& a, float& b, int tpr, int group, int parity, float2 (*red)[32]) {
   const int lane = threadIdx.x & 31;
   const int lanes = tpr < 32 ? tpr : 32;
@@ -270,7 +271,7 @@ __device__ __forceinline__ void row_sums(float& a, float& b, int tpr, int group,
   a = p.x;
   b = p.y;
 #pragma unroll
-  for (int o = 8; o; o >>= 1) {
+  for (int o = WARPS / 2; o; o >>= 1) {
     if (o < nw) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
       b += __shfl_xor_sync(0xffffffffu, b, o);
@@ -534,62 +535,96 @@ __global__ void __launch_bounds__(T) rms_forward_values_kernel(const RmsArgs a) 
     if ((int)threadIdx.x + j * T < a.D) store1(a.y, a.y_type, base + j * T, s[j] * r);
 }
 
-template <class X, class R, int T, int NE>
-__global__ void __launch_bounds__(T) rms_backward_values_kernel(const RmsGradArgs a) {
-  __shared__ float red[64];
+// Groups of G threads take rows of up to G NE values, all groups of a block together T threads.  The
+// next row is on its way while one is worked on, without its residual gradient where registers are
+// short (NE = 8), and gamma then comes from L1.  Loads of single values bound it: 9807 x 103 fp16 takes
+// 7.3 us (24.5 with a whole block a row), 3000 x 3333 bf16 30 us (floor 12), 1115 x 8190 fp32 44 us (22).
+template <class X, class R, int T, int G, int NE>
+__global__ void __launch_bounds__(T, 1024 / T) rms_backward_values_kernel(const RmsGradArgs a) {
+  constexpr bool ROOM = NE <= 4, ROOM_E = NE <= 6;
+  constexpr int GROUPS = T / G;
+  __shared__ float2 red[2][32];
+  __shared__ float part[GROUPS > 1 ? T * NE : 1];
   grid_launch_dependents();
   grid_wait_prior();
-  float dg[NE];
+  const int t = threadIdx.x % G, group = threadIdx.x / G, D = a.D;
+  const int64_t stride = (int64_t)gridDim.x * GROUPS;
+  float dg[NE], gk[ROOM ? NE : 1];
 #pragma unroll
-  for (int j = 0; j < NE; ++j) dg[j] = 0.f;
-  constexpr bool AHEAD = NE <= 4;  // room for the next row, loaded as stored before this one is worked on
+  for (int j = 0; j < NE; ++j) {
+    dg[j] = 0.f;
+    if constexpr (ROOM) gk[j] = t + j * G < D ? __ldg(a.gamma + t + j * G) : 0.f;
+  }
+  auto gamma = [&](int j) { return ROOM ? gk[ROOM ? j : 0] : __ldg(a.gamma + t + j * G); };
   R s1[NE], e1[NE];
   X y1[NE];
+  auto fetch_res = [&](int64_t row) {
+    const R* p = static_cast<const R*>(a.dres) + (size_t)row * D + t;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) e1[j] = a.dres && row < a.rows && t + j * G < D ? p[j * G] : R(0.f);
+  };
   auto fetch = [&](int64_t row) {
-    const size_t base = (size_t)row * a.D + threadIdx.x;
+    const R* p = static_cast<const R*>(a.sum) + (size_t)row * D + t;
+    const X* q = static_cast<const X*>(a.dy) + (size_t)row * D + t;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      const bool in = row < a.rows && (int)threadIdx.x + j * T < a.D;
-      s1[j] = in ? static_cast<const R*>(a.sum)[base + j * T] : R(0.f);
-      y1[j] = in ? static_cast<const X*>(a.dy)[base + j * T] : X(0.f);
-      e1[j] = in && a.dres ? static_cast<const R*>(a.dres)[base + j * T] : R(0.f);
+      const bool in = row < a.rows && t + j * G < D;
+      s1[j] = in ? p[j * G] : R(0.f);
+      y1[j] = in ? q[j * G] : X(0.f);
     }
+    if (ROOM_E) fetch_res(row);
   };
-  if (AHEAD) fetch(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const size_t base = (size_t)row * a.D + threadIdx.x;
-    float s[NE], y[NE], e[NE], v[2] = {0.f, 0.f};
-    if (!AHEAD) fetch(row);
+  int parity = 0;
+  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+  fetch(row);
+  for (; row < a.rows; row += stride) {
+    float s[NE], y[NE], e[NE];
+    if (!ROOM_E) fetch_res(row);
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
       s[j] = value(s1[j]);
       y[j] = value(y1[j]);
-      e[j] = value(e1[j]);
+      if (ROOM_E) e[j] = value(e1[j]);
     }
-    if (AHEAD) fetch(row + gridDim.x);
+    fetch(row + stride);
+    float v0 = 0.f, v1 = 0.f;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      const int c = threadIdx.x + j * T;
-      v[0] = fmaf(s[j], s[j], v[0]);
-      if (c < a.D) v[1] = fmaf(y[j] * __ldg(a.gamma + c), s[j], v[1]);
+      v0 = fmaf(s[j], s[j], v0);
+      if (t + j * G < D) v1 = fmaf(y[j] * gamma(j), s[j], v1);
     }
-    group_reduce<2>(v, T, false, red);
-    const float r = rsqrtf(v[0] * a.inv_d + a.eps);
-    const float k = r * r * r * (v[1] * a.inv_d);
+    row_sums<32>(v0, v1, G, group, parity, red);
+    parity ^= 1;
+    const float r = rsqrtf(v0 * a.inv_d + a.eps);
+    const float k = r * r * r * (v1 * a.inv_d);
+    const size_t base = (size_t)row * D + t;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      const int c = threadIdx.x + j * T;
-      if (c < a.D) {
+      if (t + j * G < D) {
+        if (!ROOM_E) e[j] = value(e1[j]);
         dg[j] = fmaf(y[j] * r, s[j], dg[j]);
-        const float o = e[j] + fmaf(r * __ldg(a.gamma + c), y[j], -s[j] * k);
-        if (a.dsum) assign(static_cast<R*>(a.dsum)[base + j * T], o);
-        if (a.dx) assign(static_cast<X*>(a.dx)[base + j * T], o);
+        const float o = e[j] + fmaf(r * gamma(j), y[j], -s[j] * k);
+        if (a.dsum) assign(static_cast<R*>(a.dsum)[base + j * G], o);
+        if (a.dx) assign(static_cast<X*>(a.dx)[base + j * G], o);
       }
     }
   }
+  float* out = a.partial + (size_t)blockIdx.x * D;
+  if constexpr (GROUPS == 1) {
 #pragma unroll
-  for (int j = 0; j < NE; ++j)
-    if ((int)threadIdx.x + j * T < a.D) a.partial[(size_t)blockIdx.x * a.D + threadIdx.x + j * T] = dg[j];
+    for (int j = 0; j < NE; ++j)
+      if (t + j * G < D) out[t + j * G] = dg[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NE; ++j) part[(group * NE + j) * G + t] = dg[j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += T) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) v += part[g * NE * G + c];
+      out[c] = v;
+    }
+  }
 }
 
 // Wider rows: two passes, the second from L1 / L2.
@@ -698,6 +733,13 @@ cudaError_t backward_with(RmsGradArgs a, int num_sms, cudaStream_t s) {
   return e == cudaSuccess ? add_partials(a, grid, s) : e;
 }
 
+template <class X, class R, int T, int G, int NE>
+cudaError_t backward_values(RmsGradArgs a, int num_sms, cudaStream_t s) {
+  const int grid = backward_blocks(a, (a.rows + T / G - 1) / (T / G), num_sms * (1024 / T));
+  const cudaError_t e = launch_dependent(rms_backward_values_kernel<X, R, T, G, NE>, grid, T, 0, s, a);
+  return e == cudaSuccess ? add_partials(a, grid, s) : e;
+}
+
 template <class X, class R>
 cudaError_t backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
   constexpr int WIDE = sizeof(R) == 4;  // fp32 rows take more registers, and carry more bytes a thread
@@ -757,19 +799,24 @@ cudaError_t launch_rms_backward(const RmsGradArgs& args, int num_sms, cudaStream
   const bool vec = a.D % 8 == 0 && a.D <= kRmsMaxRegisterRow / 2 && aligned(a.sum, 16) && aligned(a.gamma, 16) && aligned(a.dy, 16) &&
                    aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
   if (!vec) {
-    const int grid = backward_blocks(a, a.rows, num_sms * 4);
-    const cudaError_t e =
-        a.D > kRmsMaxValues
-            ? launch_dependent(rms_backward_any_kernel, grid, 256, 0, s, a)
-            : with_types(a.x_type, a.res_type, [&](auto x, auto r) {
-                using X = decltype(x);
-                using R = decltype(r);
-                if (a.D <= 1024) return launch_dependent(rms_backward_values_kernel<X, R, 256, 4>, grid, 256, 0, s, a);
-                if (a.D <= 2048) return launch_dependent(rms_backward_values_kernel<X, R, 512, 4>, grid, 512, 0, s, a);
-                if (a.D <= 4096) return launch_dependent(rms_backward_values_kernel<X, R, 1024, 4>, grid, 1024, 0, s, a);
-                return launch_dependent(rms_backward_values_kernel<X, R, 1024, 8>, grid, 1024, 0, s, a);
-              });
-    return e == cudaSuccess ? add_partials(a, grid, s) : e;
+    if (a.D > kRmsMaxValues) {
+      const int grid = backward_blocks(a, a.rows, num_sms * 4);
+      const cudaError_t e = launch_dependent(rms_backward_any_kernel, grid, 256, 0, s, a);
+      return e == cudaSuccess ? add_partials(a, grid, s) : e;
+    }
+    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+      using X = decltype(x);
+      using R = decltype(r);
+      if (a.D <= 128) return backward_values<X, R, 256, 32, 4>(a, num_sms, s);
+      if (a.D <= 256) return backward_values<X, R, 256, 64, 4>(a, num_sms, s);
+      if (a.D <= 512) return backward_values<X, R, 256, 128, 4>(a, num_sms, s);
+      if (a.D <= 1024) return backward_values<X, R, 256, 256, 4>(a, num_sms, s);
+      if (a.D <= 2048) return backward_values<X, R, 512, 512, 4>(a, num_sms, s);
+      if (a.D <= 4096) return backward_values<X, R, 1024, 1024, 4>(a, num_sms, s);
+      if (a.D <= 5120) return backward_values<X, R, 1024, 1024, 5>(a, num_sms, s);
+      if (a.D <= 6144) return backward_values<X, R, 1024, 1024, 6>(a, num_sms, s);
+      return backward_values<X, R, 1024, 1024, 8>(a, num_sms, s);
+    });
   }
   return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
     return backward<decltype(x), decltype(r)>(a, num_sms, s);
