@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const Rms
   constexpr bool AHEAD = NV == 1 || (NV == 2 && sizeof(R) == 2);  // room for the next row
   constexpr bool KEEP = NV == 1;                                  // room for gamma
   __shared__ float2 red[2][32];
-  extern __shared__ float part[];  // [groups][D] when the block has more than one group
+  extern __shared__ float part[];  // [groups][D + 4] when the block has more than one group
   grid_launch_dependents();
   grid_wait_prior();
   const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr;
@@ -421,20 +421,31 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const Rms
     }
     return;
   }
+  const int pitch = a.D + 4;  // columns of 8 rows in a row lie in different banks
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = t + j * tpr;
-    if (c < nvec) store8(part + (size_t)group * a.D + c * 8, dgf[j]);
+    if (c < nvec) store8(part + group * pitch + c * 8, dgf[j]);
   }
   __syncthreads();
+  if (groups > 32) {  // short rows: a warp a column (in turn, 768 rows would be a long chain of additions)
+    for (int c = threadIdx.x >> 5; c < a.D; c += THREADS / 32) {
+      float v = 0.f;
+      for (int g = threadIdx.x & 31; g < groups; g += 32) v += part[g * pitch + c];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if ((threadIdx.x & 31) == 0) out[c] = v;
+    }
+    return;
+  }
   for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
     float v = 0.f;
-    for (int g = 0; g < groups; ++g) v += part[(size_t)g * a.D + c];
+    for (int g = 0; g < groups; ++g) v += part[g * pitch + c];
     out[c] = v;
   }
 }
 
-// dgamma[c] = sum over the blocks' partial rows: C columns a block, Y threads a column with all their
+// dgamma[c] = sum over the blocks' partial rows: C columns a block, Y threads a column with two
 // loads at once, joined in a fixed order.  8 x 128 for the partial rows of a whole GPU (enough blocks
 // for it at the common widths), 32 x 8 for those of a few blocks.
 template <int C, int Y>
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(C * Y) rms_dgamma_kernel(const float* partial,
   const int x = threadIdx.x % C, y = threadIdx.x / C, c = blockIdx.x * C + x;
   float v = 0.f;
   if (c < D) {
-#pragma unroll 8
+#pragma unroll 2
     for (int i = y; i < n; i += Y) v += partial[(size_t)i * D + c];
   }
   red[y][x] = v;
@@ -728,7 +739,7 @@ cudaError_t backward_with(RmsGradArgs a, int num_sms, cudaStream_t s) {
   a.tpr = pow2_at_least((a.D / 8 + NV - 1) / NV);
   const int groups = THREADS / a.tpr;
   const int grid = backward_blocks(a, (a.rows + groups - 1) / groups, num_sms * BLOCKS);
-  const size_t smem = groups > 1 ? (size_t)groups * a.D * sizeof(float) : 0;  // at most 8 KB
+  const size_t smem = groups > 1 ? (size_t)groups * (a.D + 4) * sizeof(float) : 0;  // at most 36 KB
   const cudaError_t e = launch_dependent(rms_backward_kernel<X, R, NV, THREADS, BLOCKS>, grid, THREADS, smem, s, a);
   return e == cudaSuccess ? add_partials(a, grid, s) : e;
 }
@@ -743,6 +754,10 @@ cudaError_t backward_values(RmsGradArgs a, int num_sms, cudaStream_t s) {
 template <class X, class R>
 cudaError_t backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
   constexpr int WIDE = sizeof(R) == 4;  // fp32 rows take more registers, and carry more bytes a thread
+  // one wide block an SM where the rows give each of them work (fewer partial rows to add: 8192 x 1024
+  // fp16 18.0 -> 16.1 us), narrower ones to spread fewer rows over all SMs (500 x 2048: 6.5, wide 6.9)
+  if (a.D <= 2048 && a.rows * pow2_at_least(a.D / 8) >= (int64_t)num_sms * 768)
+    return backward_with<X, R, 1, WIDE ? 512 : 768, 1>(a, num_sms, s);
   if (a.D <= 2048) return backward_with<X, R, 1, 256, WIDE ? 2 : 3>(a, num_sms, s);
   if (a.D <= 4096) return WIDE ? backward_with<X, R, 1, 512, 1>(a, num_sms, s) : backward_with<X, R, 2, 256, 2>(a, num_sms, s);
   if (a.D <= 8192) return backward_with<X, R, 2, 512, 1>(a, num_sms, s);

@@ -267,6 +267,13 @@ def test_backward_of_the_other_types(xt, rt):
         _check_backward(50, d, xt, rt, _backward(50, d, xt, rt, with_dres=False, both=False, seed=d))
 
 
+@pytest.mark.parametrize("d", [8, 16, 64, 256, 264])
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16")])
+def test_backward_of_many_short_rows(d, xt, rt):
+    for rows in (300, 160001 // d * 8):
+        _check_backward(rows, d, xt, rt, _backward(rows, d, xt, rt, seed=rows + d))
+
+
 @pytest.mark.parametrize("d", [31, 127, 129, 255, 257, 510, 513, 1023, 2047, 2049, 4094, 5119, 5121, 6143, 6145, 8191])
 @pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
 def test_backward_of_the_widths_where_the_row_groups_change(d, xt, rt):
