@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
   bool mma_issued = false;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       const int mn_chunks = (bn / CG + 63) / 64;  // MN-major B: 64-column boxes of this CTA
       int stage = 0;
       uint32_t phase = 0;
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       cluster_sync();
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc = (1u << 4) | (args.bf16_operands ? (1u << 7) | (1u << 10) : 0u) |
                              ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16) | ((uint32_t)(bn >> 3) << 17) |
                              ((uint32_t)((kGluRows * CG) >> 4) << 24);
@@ -572,11 +572,11 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     // Abort path: let the copies and MMAs in flight land before the shared and tensor memory
     // are released (bounded as well).  A pair's copies complete on the leader's barriers.
     const WaitCtl dc{args.status, never_flag, 100000000LL};
-    if (warp == 0 && lane == 0 && rank == 0) {
+    if (warp == 0 && rank == 0 && elect_one()) {
       for (int s = 0; s < stages; ++s)
         if (issued_mask & (1u << s)) wait_bounded(&full[s], (issued_par >> s) & 1u, dc);
     }
-    if (warp == 1 && lane == 0 && mma_issued) {
+    if (warp == 1 && elect_one() && mma_issued) {
       umma_commit_cg<CG>(drain, 3 << (2 * pair));
       wait_bounded(drain, 0, dc);
     }
