@@ -666,16 +666,20 @@ cudaError_t prepare_glu_kernels(GluUnits* u) {
 // Fewer than 128 rows of A: only those (to the next 8) are loaded and given room in the ring; the
 // MMA still reads 128, the others being whatever lies behind, and their results are not stored.
 //
-// The cut goes by an estimate of the cycles a launch takes, from what was measured:
-//   a k-block costs its products (a 256-column accumulator: 555; e4m3's have twice the k), its
-//   operand stream from L2 (62 bytes a cycle and SM, 46 where rows do not begin on a 128-byte line
-//   and a box row takes two) or issuing its four MMAs and commit (500), whichever is longest;
-//   a round of tiles costs its k-blocks or its share of what has to come from memory (3566 bytes a
-//   cycle, the copy bandwidth, which fewer than about 130 SMs do not draw), whichever is longer,
-//   and a fifth of the other;
-//   the last tile's epilogue is not hidden: 1300 for each turn of its two warps of a lane quarter;
-//   sharing a tile's k-blocks out to a cluster costs two meetings (2500) and the exchange of the
-//   sums (10 bytes a cycle and CTA); the pieces have to fit in the ring.
+// The cut goes by an estimate of the cycles a launch takes.  Its constants were fitted to the times of
+// all cuts of 192 sizes (12 to 3000 tokens, weights of 520 x 5696 to 4096 x 10240, all modes): the cut
+// that it takes is 1 % slower than the fastest on average, 11 % at worst.
+//   A k-block costs its products (a 256-column accumulator: 555, narrower ones 8 % more a column; e4m3's
+//   have twice the k), its operand stream from L2 (74 bytes a cycle and SM, 44 where rows do not begin
+//   on a 128-byte line and a box row takes two) or issuing its four MMAs and commit (240, a pair 350),
+//   whichever is longest.
+//   A round of tiles costs its k-blocks or its share of what has to come from memory (3800 bytes a
+//   cycle, which fewer than about 112 SMs do not draw), whichever is longer, and 0.44 of the other; at
+//   least its epilogues, 450 for each turn of the two warps of a lane quarter.
+//   The last tile's epilogue is not hidden: 1200 a turn.
+//   Pairs start later and end later (1950).  Sharing a tile's k-blocks out to a cluster costs two
+//   meetings (1100) and the exchange of the sums (11 bytes a cycle and CTA); the pieces have to fit in
+//   the ring.
 // Two pairs share B where the rows are not of whole lines (4000 x 2056 x 8200 bf16: 200 -> 185 us);
 // elsewhere that brings nothing (4000 x 2048 x 8192 backward: 523 us, 538 with it).
 // So wide tiles where there are rounds of them, narrower ones where that fills a last round or
@@ -684,7 +688,7 @@ cudaError_t prepare_glu_kernels(GluUnits* u) {
 GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const GluUnits& u) {
   const bool two = mode == GLU_FORWARD || mode == GLU_SLOPES;
   const int64_t twice = mode == GLU_DW ? 2 : 1;
-  const double memory = (double)(M * twice + (two ? 2 : 1) * N) * num_k * kKBytes / 3566.0;
+  const double memory = (double)(M * twice + (two ? 2 : 1) * N) * num_k * kKBytes / 3800.0;
   GluPlan best;
   double best_cost = 0;
   for (int form = 0; form < 6; ++form) {  // pairs; two pairs; lone CTAs; clusters of 2, 4, 8 lone CTAs
@@ -701,19 +705,23 @@ GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k
       const int64_t rounds = (tiles + units - 1) / units, last = tiles - (rounds - 1) * units;
       const int pieces = (chunks + split - 1) / split;
       if (split > 1 && (rounds > 1 || (split - 1) * pieces * kGluRows * (two ? 256 : 128) > ring_bytes(false))) continue;
-      double block = 555.0 * bn / kMaxBN;
-      const double stream = (double)(rows + bn / cg / (1 + quad)) * kKBytes / (whole_lines ? 62.0 : 46.0);
+      double block = (bn == kMaxBN ? 555.0 : 600.0) * bn / kMaxBN;
+      const double stream = (double)(rows + bn / cg / (1 + quad)) * kKBytes / (whole_lines ? 74.0 : 44.0);
       if (block < stream) block = stream;
-      if (block < 500.0) block = 500.0;
+      const double issue = cg == 2 ? 350.0 : 240.0;
+      if (block < issue) block = issue;
       const double products = (double)((num_k + split - 1) / split) * block;
       auto round = [&](int64_t n) {  // n tiles at once
         const double active = (double)n * cg * split * (1 + quad);
-        const double read = memory * n / tiles * (active < 130.0 ? 130.0 / active : 1.0);
-        return products > read ? products + 0.2 * read : read + 0.2 * products;
+        const double read = memory * n / tiles * (active < 112.0 ? 112.0 / active : 1.0);
+        return products > read ? products + 0.44 * read : read + 0.44 * products;
       };
-      double cost = (rounds - 1) * (round(units) + 500.0) + round(last) + 500.0 + 1300.0 * ((pieces + 1) / 2);
-      if (split > 1) cost += 2500.0 + (double)rows * bn * 4 * (split - 1) / split / 10.0;
-      if (!best.cg || cost < best_cost * 0.97) {
+      const int turns = (pieces + 1) / 2;
+      const double full = round(units) > 450.0 * turns ? round(units) : 450.0 * turns;
+      double cost = (rounds - 1) * (full + 600.0) + round(last) + 600.0 + 1200.0 * turns;
+      if (cg == 2) cost += 1950.0;
+      if (split > 1) cost += 1100.0 + (double)rows * bn * 4 * (split - 1) / split / 11.0;
+      if (!best.cg || cost < best_cost * 0.98) {
         best.cg = cg;
         best.split = split;
         best.quad = quad;
