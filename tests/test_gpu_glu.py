@@ -126,6 +126,16 @@ def test_forward_of_the_other_pairs(t, act):
         _close(_np(h), r, bound, "h")
 
 
+@pytest.mark.parametrize("d,f", [(1032, 40), (1160, 72), (1400, 1200), (2048, 5120), (2056, 48), (2600, 64), (4056, 56),
+                                 (4096, 1032), (8192, 16), (8200, 16)])
+@pytest.mark.parametrize("tokens", [1, 8])
+def test_forward_of_a_few_tokens_and_long_rows(tokens, d, f):
+    """Rows read in one round of a block's warps, in several, and in several with little in the last."""
+    x, wg, wu, h = _forward(tokens, d, f, "bf16", "silu")
+    r, bound = _forward_bound(_np(x), _np(wg), _np(wu), "silu", "bf16")
+    _close(_np(h), r, bound, "h")
+
+
 def _rows8(t):
     import torch
     scale = t.abs().amax(dim=1).clamp_min(2.0 ** -100) / 448
