@@ -12,7 +12,7 @@
 //
 // Measured: 100000 x 1024 bf16 to e4m3 106 us (the copy bandwidth), 8192 x 1024 fp16 with an fp32
 // residual 18.3 us (0.81 of it), one row 2.7 us in a graph; backward 20011 x 4096 fp16 110 us (0.88),
-// 8192 x 1024 bf16 / fp32 25.7 us (0.77, 4 us of it the second launch for dgamma).
+// 8192 x 1024 bf16 / fp32 24.9 us (0.80, 3.5 us of it the second launch for dgamma).
 //
 // The e4m3 form divides a row by its scale = max|y| / 448 (448 is e4m3's largest value) and
 // rounds once; max|y| = r max|s gamma| comes from the same pass as the sum of squares.
