@@ -718,17 +718,20 @@ cudaError_t forward(RmsArgs a, int num_sms, cudaStream_t s) {
   return launch_dependent(rms_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
 }
 
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 // Blocks of a backward over groups of rows: what the GPU holds at once, and one alone for so few that
-// a second launch would cost more than their turns; a lone block writes dgamma itself.
+// a second launch would cost more than their turns; a lone block writes dgamma itself, where that takes
+// the 16-byte stores of the partial rows.
 int backward_blocks(RmsGradArgs& a, int64_t groups_of_rows, int at_once) {
   int64_t n = at_once < a.blocks ? at_once : a.blocks;
   if (groups_of_rows < n) n = groups_of_rows <= 3 ? 1 : groups_of_rows;
-  if (n == 1) a.partial = a.dgamma;
+  if (n == 1 && aligned(a.dgamma, 16)) a.partial = a.dgamma;
   return (int)n;
 }
 
 cudaError_t add_partials(const RmsGradArgs& a, int n, cudaStream_t s) {
-  if (n == 1) return cudaSuccess;
+  if (a.partial == a.dgamma) return cudaSuccess;
   const float* p = a.partial;
   if (n <= 64) return launch_dependent(rms_dgamma_kernel<32, 8>, (a.D + 31) / 32, 256, 0, s, p, n, a.D, a.dgamma);
   return launch_dependent(rms_dgamma_kernel<8, 128>, (a.D + 7) / 8, 1024, 0, s, p, n, a.D, a.dgamma);
@@ -765,8 +768,6 @@ cudaError_t backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
 }
 
 constexpr int kRmsMaxValues = 8192;  // widest row the element-wise kernels hold in registers
-
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // f(X(), R()) for the C++ types of a call's x and residual.
 template <class F>

@@ -325,6 +325,22 @@ def test_backward_gives_the_same_bits_every_time_and_in_place():
         pkg.tfl_rmsnorm_destroy(h)
 
 
+@pytest.mark.parametrize("rows", [1, 3, 700])
+@pytest.mark.parametrize("d", [64, 512, 513, 2048, 8200])
+def test_backward_into_a_dgamma_that_is_only_aligned_to_its_elements(rows, d):
+    import torch
+    pkg = _pkg()
+    s, dy, dres, gamma, dx, dsum, dgamma = got = _backward(rows, d, "bf16", "f32", seed=rows)
+    _check_backward(rows, d, "bf16", "f32", got)
+    room = torch.full((d + 2,), 7.0, device="cuda")
+    h = pkg.tfl_rmsnorm_create(d, 2, 0, 2, EPS)
+    pkg.tfl_rmsnorm_backward(h, rows, s.data_ptr(), gamma.data_ptr(), dy.data_ptr(), dres.data_ptr(), dx.data_ptr(),
+                             dsum.data_ptr(), room[1:].data_ptr(), _stream())
+    torch.cuda.synchronize()
+    pkg.tfl_rmsnorm_destroy(h)
+    assert torch.equal(room[1:-1], dgamma) and room[0] == 7 and room[-1] == 7
+
+
 def test_no_rows():
     import torch
     pkg = _pkg()
