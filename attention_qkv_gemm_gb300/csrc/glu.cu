@@ -15,7 +15,7 @@
 //   GLU_DW        dWg = dg^T x and dWu = du^T x: sums over the tokens, both operands MN-major.
 //
 // Structure: warp 0 feeds a ring of k-blocks (128 bytes of k a row, 128-byte swizzle) by TMA,
-// warp 1 issues the MMAs, warps 2-9 are the epilogue (two per tensor-memory lane quarter), two
+// warp 1 issues the MMAs, the others are the epilogue (two or four per tensor-memory lane quarter), two
 // accumulators so that a tile's epilogue runs under the next tile's MMAs.
 //
 // What bounds it: with many tokens the tensor cores, and in long runs the power cap (8192 x 1024 x 4096
@@ -38,19 +38,16 @@ namespace tfl {
 
 namespace {
 
-constexpr int kGluEpiWarps = 8;
-constexpr int kGluThreads = 64 + 32 * kGluEpiWarps;
 constexpr int kKBytes = 128;       // bytes of k a row and stage
 constexpr int kMnChunk = 64 * 128; // MN-major operands: 64 k rows of 64 values
 
 constexpr int kMaxBN = 256;        // accumulator columns of a tile, at most
 constexpr int kMaxStages = 12;
-// Shared memory: ring, one 32-row transpose stage an epilogue warp (columns stored at a time: 64 in
-// wide tiles, 32 in narrow ones), barriers.
+// Shared memory: ring, one 32-row transpose stage an epilogue warp, barriers.
 constexpr int kBarrierBytes = 256;
-constexpr int xpose_bytes(bool wide) { return kGluEpiWarps * 32 * (wide ? 128 : 64); }
+__host__ __device__ constexpr int xpose_bytes(bool wide) { return wide ? 32768 : 16384; }
 constexpr int kGluSmem = 232448;
-constexpr int ring_bytes(bool wide) { return kGluSmem - 1024 - xpose_bytes(wide) - kBarrierBytes; }
+__host__ __device__ constexpr int ring_bytes(bool wide) { return kGluSmem - 1024 - xpose_bytes(wide) - kBarrierBytes; }
 
 // The activation of a packed pair of fp32 values (FMA-pipe work runs two lanes an instruction;
 // the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
@@ -206,8 +203,15 @@ __device__ __forceinline__ Tile tile_at(int t, int num_m, int num_n, int group_m
 // loads half of its part of B and multicasts it to its like of the other pair, so that a k-block
 // costs it 24 KB of L2 reads instead of 32 KB.
 enum GluForm : int { kWide = 0, kNarrow = 1, kSplit = 2, kQuad = 3 };
+// Epilogue warps: sixteen for the wide tiles, 32 columns each, which a short k needs (8192 x 1024 x 4096
+// e4m3 47.5 -> 45.4 us; kQuad 10130 x 448 x 9952 e4m3 120 -> 104; the eight before computed 32 columns at
+// a time and stored 64, these 16 and 32, and have the registers for it).  Eight for the narrow tiles,
+// most of which have one or two chunks, and for kQuad in 16 bits, whose rows straddle lines: stores of
+// 64 columns keep it 1 to 2 % faster there (backward 2979 x 1160 x 2856).
+__host__ __device__ constexpr int epi_warps(int form, bool f8) { return form == kWide || (form == kQuad && f8) ? 16 : 8; }
+__host__ __device__ constexpr int glu_threads(int form, bool f8) { return 64 + 32 * epi_warps(form, f8); }
 template <int CG, int MODE, bool F8, int FORM>
-__global__ void __launch_bounds__(kGluThreads, 1)
+__global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
     glu_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GluArgs args) {
   constexpr bool WIDE = FORM == kWide || FORM == kQuad, SPLIT = FORM == kSplit;
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&accf[a], 1);
-      mbar_init(&acce[a], CG * kGluEpiWarps);
+      mbar_init(&acce[a], CG * epi_warps(FORM, F8));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -407,9 +411,10 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       cluster_sync();
     }
   } else {
-    // ------------------------------------------------------------ epilogue (8 warps)
-    constexpr int W = WIDE ? 64 : 32;  // columns stored at a time; the two warps of a lane quarter take turns
-    constexpr int LD = 32;             // columns computed at a time
+    // ------------------------------------------------------------ epilogue
+    constexpr int H = epi_warps(FORM, F8) / 4;          // warps of a lane quarter, which take the chunks in turn
+    constexpr int W = FORM == kQuad && !F8 ? 64 : 32;   // columns stored at a time
+    constexpr int LD = H == 4 ? 16 : 32;                // columns computed at a time
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* st = xpose + (warp - 2) * (32 * 2 * W);
     int acc = 0;
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
       tc_fence_after();
       const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxBN);
       const int chunks = (bno + W - 1) / W;
-      const int last = chunks - 1 - ((chunks - 1 - half) & 1);  // this warp's last chunk (< 0: it has none)
+      const int last = chunks - 1 - ((chunks - 1 - half) & (H - 1));  // this warp's last chunk (< half: it has none)
       auto hand_back = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -463,7 +468,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
         tc_fence_after();
         for (int c = 0, i = 0; c < chunks; ++c) {
           const int owner = c % split;
-          if (owner == part || (i++ & 1) != half) continue;
+          if (owner == part || (i++ & (H - 1)) != half) continue;
           float g[W], u[W];
           tmem_ld32(tb + c * W, g);
           if constexpr (TWO) tmem_ld32(tb + bno + c * W, u);
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(kGluThreads, 1)
         cluster_sync();  // the sums have arrived
       }
 #pragma unroll 1
-      for (int c = part + split * half; c < chunks; c += 2 * split) {
+      for (int c = part + split * half; c < chunks; c += H * split) {
         const int n0 = n_tile + c * W;                       // first output column
         const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
         uint4 o[W / 8], o2[W / 8];
@@ -498,14 +503,19 @@ __global__ void __launch_bounds__(kGluThreads, 1)
             sc[W + i * 32 + lane] = su[i];
           }
           __syncwarp();
-          if (c + 2 * split < chunks) fetch_scales(c + 2 * split);
+          if (c + H * split < chunks) fetch_scales(c + H * split);
         }
 #pragma unroll
         for (int b = 0; b < W / LD; ++b) {
           const int col = c * W + b * LD;
           float g[LD], u[LD];
-          tmem_ld32(tb + col, g);
-          if constexpr (TWO) tmem_ld32(tb + bno + col, u);
+          if constexpr (LD == 16) {
+            tmem_ld16(tb + col, g);
+            if constexpr (TWO) tmem_ld16(tb + bno + col, u);
+          } else {
+            tmem_ld32(tb + col, g);
+            if constexpr (TWO) tmem_ld32(tb + bno + col, u);
+          }
           tmem_wait_ld();
           // once the accumulator is in registers it is handed back, before arithmetic and stores
           if (!SPLIT && b == W / LD - 1 && c == last) hand_back();
@@ -526,11 +536,14 @@ __global__ void __launch_bounds__(kGluThreads, 1)
           if constexpr (F8) {
             const float* sc = reinterpret_cast<const float*>(st) + b * LD;
 #pragma unroll
-            for (int i = 0; i < LD / 4; ++i) {
-              const float4 a = *reinterpret_cast<const float4*>(sc + 4 * i);
-              const float4 e = *reinterpret_cast<const float4*>(sc + W + 4 * i);
-              g[4 * i] *= sx * a.x, g[4 * i + 1] *= sx * a.y, g[4 * i + 2] *= sx * a.z, g[4 * i + 3] *= sx * a.w;
-              u[4 * i] *= sx * e.x, u[4 * i + 1] *= sx * e.y, u[4 * i + 2] *= sx * e.z, u[4 * i + 3] *= sx * e.w;
+            for (int i = 0; i < LD; i += 4) {
+              const float4 a = *reinterpret_cast<const float4*>(sc + i);
+              const float4 e = *reinterpret_cast<const float4*>(sc + W + i);
+              auto scale2 = [&](float* v, float s0, float s1) {
+                f2_unpack(f2_mul(f2_pack(v[0], v[1]), f2_mul(f2_splat(sx), f2_pack(s0, s1))), v[0], v[1]);
+              };
+              scale2(g + i, a.x, a.y), scale2(g + i + 2, a.z, a.w);
+              scale2(u + i, e.x, e.y), scale2(u + i + 2, e.z, e.w);
             }
             if (b == W / LD - 1) __syncwarp();  // the stage is free for the rows
           }
@@ -602,7 +615,7 @@ cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStrea
   const int cluster = CG * p.split * (FORM == kQuad ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * cluster);
-  cfg.blockDim = dim3(kGluThreads);
+  cfg.blockDim = dim3(glu_threads(FORM, F8));
   cfg.dynamicSmemBytes = kGluSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -627,7 +640,7 @@ template <int CG, int FORM>
 cudaError_t clusters_at_once(int size, int* n) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size);
-  cfg.blockDim = dim3(kGluThreads);
+  cfg.blockDim = dim3(glu_threads(FORM, false));
   cfg.dynamicSmemBytes = kGluSmem;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
