@@ -19,8 +19,8 @@
 // accumulators so that a tile's epilogue runs under the next tile's MMAs.
 //
 // What bounds it: with many tokens the tensor cores, and in long runs the power cap (8192 x 1024 x 4096
-// fp16 forward 74 us in a burst, 1.86 PFLOP/s, 0.99 of the measured burst rate, 94 us in a long run;
-// 16384 x 2048 x 8192 bf16 backward 1.76 ms and 2.07 ms); with few tokens the weights' bytes (40 x 4096 x
+// fp16 forward 74 us in a burst, 1.86 PFLOP/s, 0.99 of the measured burst rate, 93 us in a long run;
+// 16384 x 2048 x 8192 bf16 backward 1.76 ms and 2.03 ms); with few tokens the weights' bytes (40 x 4096 x
 // 10240 e4m3: 16.4 us for 85 MB, 5.2 TB/s).  A pair's 256 x 256 tile took the first two from 107 to 101 us
 // and from 2.26 to 2.06 ms against a lone CTA's 128 x 256, a thread that the compiler knows to be alone
 // for the issue of MMAs from 82 to 74 us and from 1.95 to 1.76 ms (bursts).  The epilogue's arithmetic is
