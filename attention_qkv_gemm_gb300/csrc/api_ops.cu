@@ -370,8 +370,8 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   const int ke = f8 ? 128 : 64, num_k = (g->D + ke - 1) / ke;
   const GluPlan p = glu_plan(GLU_FORWARD, g->D * es % 128 == 0, tokens, g->F, num_k, g->units);
   GluMaps mp;
-  if (!make_map(&mp.a0, x, tokens, g->D, (int)es, p.a_rows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.b_rows) ||
-      !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.b_rows))
+  if (!make_map(&mp.a0, x, tokens, g->D, (int)es, p.a_rows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bno) ||
+      !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bno))
     return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
   mp.a1 = mp.a0;
   GluArgs a = glu_args(g);
@@ -424,8 +424,8 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   const GluPlan p2 = glu_plan(GLU_DX, lines, tokens, Di, 2 * kf, g->units);
   const GluPlan p3 = glu_plan(GLU_DW, lines, Fi, Di, kt, g->units);
   GluMaps m1, m2, m3;
-  bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.b_rows) &&
-            make_map(&m1.b1, wu, Fi, Di, 2, p1.b_rows);
+  bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bno) &&
+            make_map(&m1.b1, wu, Fi, Di, 2, p1.bno);
   m1.a1 = m1.a0;
   ok = ok && make_map(&m2.a0, g->dg, tokens, Fi, 2, p2.a_rows, g->pitch) &&
        make_map(&m2.a1, g->du, tokens, Fi, 2, p2.a_rows, g->pitch) &&

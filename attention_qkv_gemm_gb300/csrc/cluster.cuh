@@ -55,17 +55,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// The same into that place of every CTA in `mask`; each pair's barrier at the place of `bar` (in the
-// even or odd CTAs, as `bar` is) is told of the bytes its CTAs get.
-__device__ __forceinline__ void tma_load_2d_pair_to(void* dst, const CUtensorMap* m, uint32_t bar, int c0, int c1,
-                                                    int mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "h"((uint16_t)mask)
-      : "memory");
-}
-
 template <int CG>
 __device__ __forceinline__ void tmem_alloc_cg(uint32_t* dst_smem, uint32_t ncols) {
   if constexpr (CG == 1) {
@@ -102,14 +91,14 @@ __device__ __forceinline__ void umma_cg(uint32_t d, uint64_t a, uint64_t b, uint
 #undef TFL_UMMA
 }
 
-// Arrive once on `bar` (with CG = 2: on the barrier at its place in the cluster's CTAs of `ctas`) when
-// this thread's tcgen05 operations so far have completed.
+// Arrive once on `bar` (with CG = 2: on the barrier at its place in both CTAs) when this thread's
+// tcgen05 operations so far have completed.
 template <int CG>
-__device__ __forceinline__ void umma_commit_cg(uint64_t* bar, int ctas) {
+__device__ __forceinline__ void umma_commit_cg(uint64_t* bar) {
   if constexpr (CG == 1) {
     umma_commit(bar);
   } else {
-    const uint16_t mask = (uint16_t)ctas;
+    const uint16_t mask = 3;
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),

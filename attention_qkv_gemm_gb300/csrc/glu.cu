@@ -199,23 +199,17 @@ __device__ __forceinline__ Tile tile_at(int t, int num_m, int num_n, int group_m
 // kSplit: the same, with the k-blocks of a tile shared out to a cluster of lone CTAs (few tiles:
 // the whole GPU works on them); each CTA finishes some of the tile's 32-column pieces, and the
 // others send it their sums through its shared memory, added in CTA order.  One tile a CTA.
-// kQuad: kWide for two CTA pairs with row blocks next to each other and the same columns: each CTA
-// loads half of its part of B and multicasts it to its like of the other pair, so that a k-block
-// costs it 24 KB of L2 reads instead of 32 KB.
-enum GluForm : int { kWide = 0, kNarrow = 1, kSplit = 2, kQuad = 3 };
+enum GluForm : int { kWide = 0, kNarrow = 1, kSplit = 2 };
 // Epilogue warps: sixteen for the wide tiles, 32 columns each, which a short k needs (8192 x 1024 x 4096
-// e4m3 47.5 -> 45.4 us; kQuad 10130 x 448 x 9952 e4m3 120 -> 104; the eight before computed 32 columns at
-// a time and stored 64, these 16 and 32, and have the registers for it).  Eight for the narrow tiles,
-// most of which have one or two chunks, and for kQuad in 16 bits, whose rows straddle lines: stores of
-// 64 columns keep it 1 to 2 % faster there (backward 2979 x 1160 x 2856).
-__host__ __device__ constexpr int epi_warps(int form, bool f8) { return form == kWide || (form == kQuad && f8) ? 16 : 8; }
-__host__ __device__ constexpr int glu_threads(int form, bool f8) { return 64 + 32 * epi_warps(form, f8); }
+// e4m3 47.5 -> 45.4 us; the eight before computed 32 columns at a time and stored 64, these 16 and 32,
+// and have the registers for it).  Eight for the narrow tiles, most of which have one or two chunks.
+__host__ __device__ constexpr int epi_warps(int form) { return form == kWide ? 16 : 8; }
+__host__ __device__ constexpr int glu_threads(int form) { return 64 + 32 * epi_warps(form); }
 template <int CG, int MODE, bool F8, int FORM>
-__global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
+__global__ void __launch_bounds__(glu_threads(FORM), 1)
     glu_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const GluArgs args) {
-  constexpr bool WIDE = FORM == kWide || FORM == kQuad, SPLIT = FORM == kSplit;
-  constexpr int PAIRS = FORM == kQuad ? 2 : 1;  // CTA pairs of a cluster
+  constexpr bool WIDE = FORM == kWide, SPLIT = FORM == kSplit;
   static_assert(!SPLIT || CG == 1, "lone CTAs share a tile's k-blocks");
   constexpr bool TWO = MODE == GLU_FORWARD || MODE == GLU_SLOPES;  // two products side by side
   constexpr bool A_MN = MODE == GLU_DW, B_MN = MODE == GLU_DX || MODE == GLU_DW;
@@ -240,16 +234,15 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
   const int stage_bytes = WIDE ? kWideStage : args.stage_bytes;
   const int a_bytes = WIDE ? kGluRows * kKBytes : args.a_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = CG == 2 ? (int)cluster_rank() & 1 : 0;            // of the pair
-  const int pair = PAIRS == 2 ? (int)cluster_rank() >> 1 : 0;        // of the cluster
+  const int rank = CG == 2 ? (int)cluster_rank() : 0;             // of the pair
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], PAIRS);
+      mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&accf[a], 1);
-      mbar_init(&acce[a], CG * epi_warps(FORM, F8));
+      mbar_init(&acce[a], CG * epi_warps(FORM));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -282,10 +275,10 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
   const WaitCtl wc{args.status, abort_flag, args.timeout_ns};
   grid_wait_prior();  // everything below reads or writes what earlier kernels use
 
-  const int num_m = (args.M + kGluRows * CG * PAIRS - 1) / (kGluRows * CG * PAIRS), num_n = (args.N + bno - 1) / bno;
+  const int num_m = (args.M + kGluRows * CG - 1) / (kGluRows * CG), num_n = (args.N + bno - 1) / bno;
   const int total = num_m * num_n * (MODE == GLU_DW ? 2 : 1);
   const int split = SPLIT ? args.split : 1, part = SPLIT ? (int)cluster_rank() : 0;
-  const int unit = blockIdx.x / (CG * PAIRS * split), units = gridDim.x / (CG * PAIRS * split);
+  const int unit = blockIdx.x / (CG * split), units = gridDim.x / (CG * split);
   const int kb0 = args.num_k * part / split, kb1 = args.num_k * (part + 1) / split;  // this CTA's k-blocks
 
   uint32_t issued_mask = 0, issued_par = 0;  // stages with loads in flight (abort path)
@@ -298,8 +291,8 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = tile_at(t, num_m, num_n, kGroupM / PAIRS);
-        const int m0 = ((tl.m * PAIRS + pair) * CG + rank) * kGluRows;
+        const Tile tl = tile_at(t, num_m, num_n, kGroupM);
+        const int m0 = (tl.m * CG + rank) * kGluRows;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
@@ -310,7 +303,7 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
           uint64_t* bar = &full[stage];
           // both CTAs' loads complete on the leader's barrier, which expects the pair's bytes
           if (rank == 0) mbar_arrive_expect_tx(bar, CG * stage_bytes);
-          const uint32_t pair_bar = CG == 2 ? map_rank(bar, pair * 2) : 0;
+          const uint32_t pair_bar = CG == 2 ? map_rank(bar, 0) : 0;
           auto load = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
             if constexpr (CG == 2)
               tma_load_2d_pair(dst, m, pair_bar, c0, c1);
@@ -320,10 +313,7 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
           if constexpr (TWO) {
             const int k = kb * KE, n0 = tl.n * bno;
             load(sa, &tmA0, k, m0);
-            if constexpr (PAIRS == 2) {
-              tma_load_2d_pair_to(sb + pair * (64 * kKBytes), rank == 0 ? &tmB0 : &tmB1, pair_bar, k, n0 + pair * 64,
-                                  0x5 << rank);
-            } else if constexpr (CG == 2) {  // CTA 0 brings the gate's rows, CTA 1 the other projection's
+            if constexpr (CG == 2) {  // CTA 0 brings the gate's rows, CTA 1 the other projection's
               load(sb, rank == 0 ? &tmB0 : &tmB1, k, n0);
             } else {
               load(sb, &tmB0, k, n0);
@@ -333,18 +323,12 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
             const bool second = kb >= args.k_half;
             const int k = (second ? kb - args.k_half : kb) * KE, n0 = tl.n * bno + rank * (bn / CG);
             load(sa, second ? &tmA1 : &tmA0, k, m0);
-            if constexpr (PAIRS == 2)
-              tma_load_2d_pair_to(sb + pair * kMnChunk, second ? &tmB1 : &tmB0, pair_bar, n0 + pair * 64, k, 0x5 << rank);
-            else
-              for (int c = 0; c < mn_chunks; ++c) load(sb + c * kMnChunk, second ? &tmB1 : &tmB0, n0 + c * 64, k);
+            for (int c = 0; c < mn_chunks; ++c) load(sb + c * kMnChunk, second ? &tmB1 : &tmB0, n0 + c * 64, k);
           } else {
             const int k = kb * KE, n0 = tl.n * bno + rank * (bn / CG);
 #pragma unroll
             for (int c = 0; c < kGluRows / 64; ++c) load(sa + c * kMnChunk, tl.z ? &tmA1 : &tmA0, m0 + c * 64, k);
-            if constexpr (PAIRS == 2)
-              tma_load_2d_pair_to(sb + pair * kMnChunk, &tmB0, pair_bar, n0 + pair * 64, k, 0x5 << rank);
-            else
-              for (int c = 0; c < mn_chunks; ++c) load(sb + c * kMnChunk, &tmB0, n0 + c * 64, k);
+            for (int c = 0; c < mn_chunks; ++c) load(sb + c * kMnChunk, &tmB0, n0 + c * 64, k);
           }
           issued_mask |= 1u << stage;
           issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
@@ -391,14 +375,14 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
             umma_cg<CG, F8>(d, ad + (uint32_t)(k * (A_MN ? 2048 : 32) >> 4), bd + (uint32_t)(k * (B_MN ? 2048 : 32) >> 4),
                             idesc, 1u);
           mma_issued = true;
-          umma_commit_cg<CG>(&empty[stage], (1 << (2 * PAIRS)) - 1);  // free for every CTA that fills it
+          umma_commit_cg<CG>(&empty[stage]);
           if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_cg<CG>(&accf[acc], 3 << (2 * pair));
+        umma_commit_cg<CG>(&accf[acc]);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
@@ -412,29 +396,26 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    constexpr int H = epi_warps(FORM, F8) / 4;          // warps of a lane quarter, which take the chunks in turn
-    constexpr int W = FORM == kQuad && !F8 ? 64 : 32;   // columns stored at a time
-    constexpr int LD = H == 4 ? 16 : 32;                // columns computed at a time
+    constexpr int H = epi_warps(FORM) / 4;  // warps of a lane quarter, which take the chunks in turn
+    constexpr int W = 32;                   // columns stored at a time
+    constexpr int LD = H == 4 ? 16 : 32;    // columns computed at a time
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* st = xpose + (warp - 2) * (32 * 2 * W);
     int acc = 0;
     uint32_t acc_phase = 0;
-    const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], pair * 2) : 0, CG == 2 ? map_rank(&acce[1], pair * 2) : 0};
+    const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], 0) : 0, CG == 2 ? map_rank(&acce[1], 0) : 0};
     for (int t = unit; t < total; t += units) {
-      const Tile tl = tile_at(t, num_m, num_n, kGroupM / PAIRS);
-      const int m0 = ((tl.m * PAIRS + pair) * CG + rank) * kGluRows + q * 32, m = m0 + lane;
+      const Tile tl = tile_at(t, num_m, num_n, kGroupM);
+      const int m0 = (tl.m * CG + rank) * kGluRows + q * 32, m = m0 + lane;
       const uint32_t rows = __ballot_sync(0xffffffffu, m < args.M);
       const int n_tile = tl.n * bno;  // first output column of the tile
       // e4m3: the row's scale and this lane's share of the first chunk's column scales, on their
       // way while the products finish; columns past the last read the last one's (not stored)
-      float sx = 1.0f, sg[W / 32], su[W / 32];
+      float sx = 1.0f, sg = 0.f, su = 0.f;
       auto fetch_scales = [&](int c) {
-#pragma unroll
-        for (int i = 0; i < W / 32; ++i) {
-          const int n = min(n_tile + c * W + i * 32 + lane, args.N - 1);
-          sg[i] = __ldg(args.g_scale + n);
-          su[i] = __ldg(args.u_scale + n);
-        }
+        const int n = min(n_tile + c * W + lane, args.N - 1);
+        sg = __ldg(args.g_scale + n);
+        su = __ldg(args.u_scale + n);
       };
       if constexpr (F8) {
         sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
@@ -497,11 +478,8 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
           load_cols<W>(st, lane, o2, args.dh + (size_t)m0 * args.N + n0, args.N, rows, cols);
         if constexpr (F8) {  // the chunk's scales to every lane, through the stage
           float* sc = reinterpret_cast<float*>(st);
-#pragma unroll
-          for (int i = 0; i < W / 32; ++i) {
-            sc[i * 32 + lane] = sg[i];
-            sc[W + i * 32 + lane] = su[i];
-          }
+          sc[lane] = sg;
+          sc[W + lane] = su;
           __syncwarp();
           if (c + H * split < chunks) fetch_scales(c + H * split);
         }
@@ -590,7 +568,7 @@ __global__ void __launch_bounds__(glu_threads(FORM, F8), 1)
         if (issued_mask & (1u << s)) wait_bounded(&full[s], (issued_par >> s) & 1u, dc);
     }
     if (warp == 1 && elect_one() && mma_issued) {
-      umma_commit_cg<CG>(drain, 3 << (2 * pair));
+      umma_commit_cg<CG>(drain);
       wait_bounded(drain, 0, dc);
     }
     __syncthreads();
@@ -610,12 +588,12 @@ cudaError_t launch_one(const GluMaps& mp, GluArgs a, const GluPlan& p, cudaStrea
   const bool b_mn = MODE == GLU_DX || MODE == GLU_DW;
   a.a_bytes = p.a_rows * kKBytes;
   a.stage_bytes = a.a_bytes + (b_mn ? (bn / CG + 63) / 64 * kMnChunk : bn / CG * kKBytes);
-  a.stages = ring_bytes(FORM == kWide || FORM == kQuad) / a.stage_bytes;
+  a.stages = ring_bytes(FORM == kWide) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
-  const int cluster = CG * p.split * (FORM == kQuad ? 2 : 1);
+  const int cluster = CG * p.split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * cluster);
-  cfg.blockDim = dim3(glu_threads(FORM, F8));
+  cfg.blockDim = dim3(glu_threads(FORM));
   cfg.dynamicSmemBytes = kGluSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -640,7 +618,7 @@ template <int CG, int FORM>
 cudaError_t clusters_at_once(int size, int* n) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size);
-  cfg.blockDim = dim3(glu_threads(FORM, false));
+  cfg.blockDim = dim3(glu_threads(FORM));
   cfg.dynamicSmemBytes = kGluSmem;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -658,7 +636,7 @@ cudaError_t clusters_at_once(int size, int* n) {
   X(CG, GLU_FORWARD, false, FORM) X(CG, GLU_FORWARD, true, FORM) X(CG, GLU_SLOPES, false, FORM)     \
   X(CG, GLU_DX, false, FORM) X(CG, GLU_DW, false, FORM)
 #define TFL_GLU_VARIANTS(X) \
-  TFL_GLU_MODES(X, 2, kWide) TFL_GLU_MODES(X, 2, kQuad) TFL_GLU_MODES(X, 2, kNarrow) TFL_GLU_MODES(X, 1, kNarrow) TFL_GLU_MODES(X, 1, kSplit)
+  TFL_GLU_MODES(X, 2, kWide) TFL_GLU_MODES(X, 2, kNarrow) TFL_GLU_MODES(X, 1, kNarrow) TFL_GLU_MODES(X, 1, kSplit)
 
 cudaError_t prepare_glu_kernels(GluUnits* u) {
   cudaError_t e = cudaSuccess;
@@ -667,7 +645,6 @@ cudaError_t prepare_glu_kernels(GluUnits* u) {
   TFL_GLU_VARIANTS(TFL_PREP)
 #undef TFL_PREP
   if (e == cudaSuccess) e = clusters_at_once<2, kWide>(2, &u->pairs);
-  if (e == cudaSuccess) e = clusters_at_once<2, kQuad>(4, &u->quads);
   for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = clusters_at_once<1, kSplit>(2 << i, &u->splits[i]);
   return e;
 }
@@ -693,8 +670,6 @@ cudaError_t prepare_glu_kernels(GluUnits* u) {
 //   Pairs start later and end later (1950).  Sharing a tile's k-blocks out to a cluster costs two
 //   meetings (1100) and the exchange of the sums (11 bytes a cycle and CTA); the pieces have to fit in
 //   the ring.
-// Two pairs share B where the rows are not of whole lines (4000 x 2056 x 8200 bf16: 200 -> 185 us);
-// elsewhere that brings nothing (4000 x 2048 x 8192 backward: 523 us, 538 with it).
 // So wide tiles where there are rounds of them, narrower ones where that fills a last round or
 // spreads the weights of a few rows over all SMs, and shared k-blocks where the tiles are few and
 // the rows long (60 tokens x 2048 x 8192 backward: 110 -> 57 us, most of it dx).
@@ -704,28 +679,28 @@ GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k
   const double memory = (double)(M * twice + (two ? 2 : 1) * N) * num_k * kKBytes / 3800.0;
   GluPlan best;
   double best_cost = 0;
-  for (int form = 0; form < 6; ++form) {  // pairs; two pairs; lone CTAs; clusters of 2, 4, 8 lone CTAs
-    const int quad = form == 1, cg = form < 2 ? 2 : 1, split = form < 3 ? 1 : 1 << (form - 2);
-    if ((cg == 2 && M <= kGluRows * (1 + quad)) || (split > 1 && num_k < 2 * split) || (quad && whole_lines)) continue;
-    const int64_t units = form == 0 ? u.pairs : quad ? u.quads : form == 2 ? u.sms : u.splits[form - 3];
+  for (int form = 0; form < 5; ++form) {  // pairs; lone CTAs; clusters of 2, 4, 8 lone CTAs
+    const int cg = form == 0 ? 2 : 1, split = form < 2 ? 1 : 1 << (form - 1);
+    if ((cg == 2 && M <= kGluRows) || (split > 1 && num_k < 2 * split)) continue;
+    const int64_t units = form == 0 ? u.pairs : form == 1 ? u.sms : u.splits[form - 2];
     if (units < 1) continue;
-    const int64_t tile_rows = kGluRows * cg * (1 + quad), num_m = (M + tile_rows - 1) / tile_rows;
+    const int64_t tile_rows = kGluRows * cg, num_m = (M + tile_rows - 1) / tile_rows;
     const int64_t rows = M < kGluRows ? M : kGluRows;  // rows of A outside the matrix cost no reads
     // tcgen05.mma takes N in steps of 16, a pair's in steps of 32
-    for (int bn = kMaxBN; bn >= (quad ? kMaxBN : 32); bn -= 16 * cg) {
+    for (int bn = kMaxBN; bn >= 32; bn -= 16 * cg) {
       const int bno = two ? bn / 2 : bn, chunks = (bno + 31) / 32;
       const int64_t tiles = num_m * ((N + bno - 1) / bno) * twice;
       const int64_t rounds = (tiles + units - 1) / units, last = tiles - (rounds - 1) * units;
       const int pieces = (chunks + split - 1) / split;
       if (split > 1 && (rounds > 1 || (split - 1) * pieces * kGluRows * (two ? 256 : 128) > ring_bytes(false))) continue;
       double block = (bn == kMaxBN ? 555.0 : 600.0) * bn / kMaxBN;
-      const double stream = (double)(rows + bn / cg / (1 + quad)) * kKBytes / (whole_lines ? 74.0 : 44.0);
+      const double stream = (double)(rows + bn / cg) * kKBytes / (whole_lines ? 74.0 : 44.0);
       if (block < stream) block = stream;
       const double issue = cg == 2 ? 350.0 : 240.0;
       if (block < issue) block = issue;
       const double products = (double)((num_k + split - 1) / split) * block;
       auto round = [&](int64_t n) {  // n tiles at once
-        const double active = (double)n * cg * split * (1 + quad);
+        const double active = (double)n * cg * split;
         const double read = memory * n / tiles * (active < 112.0 ? 112.0 / active : 1.0);
         return products > read ? products + 0.44 * read : read + 0.44 * products;
       };
@@ -737,8 +712,6 @@ GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k
       if (!best.cg || cost < best_cost * 0.98) {
         best.cg = cg;
         best.split = split;
-        best.quad = quad;
-        best.b_rows = quad ? 64 : bno;
         best.a_rows = M < kGluRows && mode != GLU_DW ? (int)((M + 7) / 8 * 8) : kGluRows;
         best.bno = bno;
         best.units = (int)units;
@@ -752,7 +725,7 @@ GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k
 
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s) {
   const bool wide = p.bno == (mode == GLU_FORWARD || mode == GLU_SLOPES ? kMaxBN / 2 : kMaxBN);
-  const int form = p.split > 1 ? kSplit : p.quad ? kQuad : p.cg == 2 && wide ? kWide : kNarrow;
+  const int form = p.split > 1 ? kSplit : p.cg == 2 && wide ? kWide : kNarrow;
 #define TFL_LAUNCH(CG, MODE, F8, FORM) \
   if (p.cg == CG && form == FORM && mode == MODE && f8 == F8) return launch_one<CG, MODE, F8, FORM>(mp, a, p, s);
   TFL_GLU_VARIANTS(TFL_LAUNCH)

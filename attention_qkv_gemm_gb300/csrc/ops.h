@@ -73,13 +73,12 @@ struct GluMaps {
 // output columns of a tile, tiles that run at once,
 // rows of A a CTA loads for a tile, tiles in all.
 struct GluPlan {
-  int cg = 0, split = 1, quad = 0, bno = 0, units = 0, a_rows = 0, b_rows = 0;
+  int cg = 0, split = 1, bno = 0, units = 0, a_rows = 0;
   int64_t tiles = 0;
 };
-// What runs at once on a device: lone CTAs, CTA pairs, clusters of two pairs, and of 2, 4 and 8 lone
-// CTAs.
+// What runs at once on a device: lone CTAs, CTA pairs, and clusters of 2, 4 and 8 lone CTAs.
 struct GluUnits {
-  int sms = 0, pairs = 0, quads = 0, splits[3] = {};
+  int sms = 0, pairs = 0, splits[3] = {};
 };
 // whole_lines: the rows of x and the weights begin on 128-byte lines.
 GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const GluUnits& u);
