@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(glu_threads(FORM), 1)
         su = __ldg(args.u_scale + n);
       };
       if constexpr (F8) {
-        sx = m < args.M ? __ldg(args.x_scale + m) : 0.f;
+        sx = m < args.M ? args.x_scale[m] : 0.f;  // written by the kernel before this one: a plain load
         fetch_scales(part + split * half);
       }
       const bool ok = wait_bounded(&accf[acc], acc_phase, wc);

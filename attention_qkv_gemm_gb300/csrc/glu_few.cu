@@ -58,7 +58,9 @@ __global__ void __launch_bounds__(256) glu_few_kernel(const GluFewArgs a) {
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-  const uint8_t* xr[NT];  // this lane's token of each tile (past the last: the last again, not stored)
+  // This lane's token of each tile (past the last: the last again, not stored).  x and its scales may
+  // still be written while this kernel starts: plain loads, behind the wait.
+  const uint8_t* xr[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) xr[n] = a.x + (size_t)min(n * 8 + r, a.tokens - 1) * row_bytes + c * 16;
   const uint8_t *wg = a.wg + row0, *wu = a.wu + row0;
@@ -72,7 +74,7 @@ __global__ void __launch_bounds__(256) glu_few_kernel(const GluFewArgs a) {
       g[j] = in ? load_once(wg + off) : zero;
       u[j] = in ? load_once(wu + off) : zero;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) x[j][n] = in ? __ldg(reinterpret_cast<const uint4*>(xr[n] + off)) : zero;
+      for (int n = 0; n < NT; ++n) x[j][n] = in ? *reinterpret_cast<const uint4*>(xr[n] + off) : zero;
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(256) glu_few_kernel(const GluFewArgs a) {
       u += red[w][n * 4 + 2 + odd][l];
     }
     if constexpr (TYPE == TFL_E4M3) {
-      const float sx = __ldg(a.x_scale + t);
+      const float sx = a.x_scale[t];
       g *= sx * __ldg(a.g_scale + f);
       u *= sx * __ldg(a.u_scale + f);
     }
