@@ -2,7 +2,9 @@
 //
 //   s = x + res,  r = 1 / sqrt(mean(s^2) + eps),  y = s r gamma
 // and, with a = dy gamma, the gradient of s and gamma:
-//   ds = dres + r a - s r^3 mean(a s),   dgamma = sum over rows of dy s r.
+//   ds = dres + r a - s r^3 mean(a s),   dgamma = sum over rows of dy s r
+// with t = s r as dres + r a - t (r (r mean(a s))) and the sum of dy t: t is at most sqrt(d) and
+// r mean(a s) of the size of a, where r^3 alone overflows from r = 7e12 on (rows of size 1e-13, eps 0).
 //
 // Every value is read once and written once: bandwidth bounds it, so a row lives in the
 // registers of TPR threads between its loads and its stores, TPR the smallest power of two
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const Rms
     row_sums(v0, v1, tpr, group, parity, red);
     parity ^= 1;
     const float r = rsqrtf(v0 * a.inv_d + a.eps);
-    const uint64_t r2 = f2_splat(r), k2 = f2_splat(-(r * r * r * (v1 * a.inv_d)));
+    const uint64_t r2 = f2_splat(r), k2 = f2_splat(-(r * (r * (v1 * a.inv_d))));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (live && in[j]) {
@@ -392,9 +394,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rms_backward_kernel(const Rms
         widen2(e[j], o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint64_t yr = f2_mul(y[j][i], r2);
-          dg[j][i] = f2_fma(yr, s[j][i], dg[j][i]);
-          o[i] = f2_fma(yr, KEEP ? gk[KEEP ? j : 0][i] : g[i], f2_fma(s[j][i], k2, o[i]));
+          const uint64_t t2 = f2_mul(s[j][i], r2);
+          dg[j][i] = f2_fma(y[j][i], t2, dg[j][i]);
+          o[i] = f2_fma(y[j][i], f2_mul(KEEP ? gk[KEEP ? j : 0][i] : g[i], r2), f2_fma(t2, k2, o[i]));
         }
         float of[8];
 #pragma unroll
@@ -607,14 +609,15 @@ __global__ void __launch_bounds__(T, 1024 / T) rms_backward_values_kernel(const 
     row_sums<32>(v0, v1, G, group, parity, red);
     parity ^= 1;
     const float r = rsqrtf(v0 * a.inv_d + a.eps);
-    const float k = r * r * r * (v1 * a.inv_d);
+    const float k = r * (r * (v1 * a.inv_d));
     const size_t base = (size_t)row * D + t;
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
       if (t + j * G < D) {
         if (!ROOM_E) e[j] = value(e1[j]);
-        dg[j] = fmaf(y[j] * r, s[j], dg[j]);
-        const float o = e[j] + fmaf(r * gamma(j), y[j], -s[j] * k);
+        const float sr = s[j] * r;
+        dg[j] = fmaf(y[j], sr, dg[j]);
+        const float o = fmaf(y[j], r * gamma(j), fmaf(-sr, k, e[j]));
         if (a.dsum) assign(static_cast<R*>(a.dsum)[base + j * G], o);
         if (a.dx) assign(static_cast<X*>(a.dx)[base + j * G], o);
       }
@@ -686,12 +689,12 @@ __global__ void __launch_bounds__(256) rms_backward_any_kernel(const RmsGradArgs
     }
     group_reduce<2>(v, 256, false, red);
     const float r = rsqrtf(v[0] * a.inv_d + a.eps);
-    const float k = r * r * r * (v[1] * a.inv_d);
+    const float k = r * (r * (v[1] * a.inv_d));
     for (int c = threadIdx.x; c < a.D; c += 256) {
       const float s = load1(a.sum, a.res_type, base + c), dy = load1(a.dy, a.x_type, base + c);
-      float o = a.dres ? load1(a.dres, a.res_type, base + c) : 0.f;
-      o += fmaf(r * a.gamma[c], dy, -s * k);
-      part[c] = fmaf(dy * r, s, part[c]);
+      const float sr = s * r;
+      const float o = fmaf(dy, r * a.gamma[c], fmaf(-sr, k, a.dres ? load1(a.dres, a.res_type, base + c) : 0.f));
+      part[c] = fmaf(dy, sr, part[c]);
       if (a.dsum) store1(a.dsum, a.res_type, base + c, o);
       if (a.dx) store1(a.dx, a.x_type, base + c, o);
     }
@@ -758,7 +761,7 @@ template <class X, class R>
 cudaError_t backward(const RmsGradArgs& a, int num_sms, cudaStream_t s) {
   constexpr int WIDE = sizeof(R) == 4;  // fp32 rows take more registers, and carry more bytes a thread
   // one wide block an SM where the rows give each of them work (fewer partial rows to add: 8192 x 1024
-  // fp16 18.0 -> 16.1 us), narrower ones to spread fewer rows over all SMs (500 x 2048: 6.5, wide 6.9)
+  // fp16 18.0 -> 16.1 us then, 16.6 now), narrower ones to spread fewer rows over all SMs (500 x 2048: 6.5, wide 6.9)
   if (a.D <= 2048 && a.rows * pow2_at_least(a.D / 8) >= (int64_t)num_sms * 768)
     return backward_with<X, R, 1, WIDE ? 512 : 768, 1>(a, num_sms, s);
   if (a.D <= 2048) return backward_with<X, R, 1, 256, WIDE ? 2 : 3>(a, num_sms, s);

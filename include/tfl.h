@@ -359,7 +359,9 @@ void tfl_attn_destroy(tfl_attn* a);
  * Root-mean-square norm with the residual's addition:
  *   s = x + res,   r = 1 / sqrt(mean(s^2) + eps),   y = s r gamma   (per row)
  * s, the sums and y are fp32 inside; res_out is s and y is y, each rounded once
- * to its type (y is taken from the unrounded s).
+ * to its type (y is taken from the unrounded s).  mean(s^2) + eps has to lie
+ * within fp32's normal range, 1.2e-38 to 3.4e38: with eps 0, rows of an rms
+ * between 1.1e-19 and 1.8e19 (a row of zeros has no norm then).
  *
  * e4m3 output: y_scale[row] = max(max|y|, 2^-100) / 448 and y holds
  * e4m3(y / y_scale[row]), so y_scale[row] times the stored value is the norm's
