@@ -17,7 +17,9 @@
 // 8192 x 1024 bf16 / fp32 24.9 us (0.80, 3.5 us of it the second launch for dgamma).
 //
 // The e4m3 form divides a row by its scale = max|y| / 448 (448 is e4m3's largest value) and
-// rounds once; max|y| = r max|s gamma| comes from the same pass as the sum of squares.
+// rounds once; max|y| = r max|s gamma| comes from the same pass as the sum of squares.  y is formed
+// before 448 / max|y| is applied: their product alone overflows for a row of zeros with a small eps
+// (r = 1e6 times 448 2^100).
 //
 // Widths that 8 does not divide, unaligned buffers and rows too long for registers take the
 // element-wise kernels at the end.
@@ -230,18 +232,19 @@ __global__ void __launch_bounds__(1024) rms_forward_kernel(const RmsArgs a) {
     }
   }
   group_reduce<Q ? 2 : 1>(v, tpr, Q, red);
-  float r = rsqrtf(v[0] * a.inv_d + a.eps);
+  const float r = rsqrtf(v[0] * a.inv_d + a.eps);
+  float to8 = 1.0f;
   if constexpr (Q) {
     const float amax = max_nan(v[1] * r, kMinAmax);
     if (live && t == 0) a.y_scale[row] = amax / kE4m3Max;
-    r *= kE4m3Max / amax;
+    to8 = kE4m3Max / amax;
   }
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = t + j * tpr;
     if (live && c < nvec) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[j][i] *= r;
+      for (int i = 0; i < 8; ++i) s[j][i] = Q ? s[j][i] * r * to8 : s[j][i] * r;
       store8(static_cast<Y*>(a.y) + base + c * 8, s[j]);
     }
   }
@@ -537,15 +540,16 @@ __global__ void __launch_bounds__(T) rms_forward_values_kernel(const RmsArgs a) 
     }
   }
   group_reduce<2>(v, T, true, red);
-  float r = rsqrtf(v[0] * a.inv_d + a.eps);
+  const float r = rsqrtf(v[0] * a.inv_d + a.eps);
+  float to8 = 1.0f;
   if (a.y_type == TFL_E4M3) {
     const float amax = max_nan(v[1] * r, kMinAmax);
     if (threadIdx.x == 0) a.y_scale[blockIdx.x] = amax / kE4m3Max;
-    r *= kE4m3Max / amax;
+    to8 = kE4m3Max / amax;
   }
 #pragma unroll
   for (int j = 0; j < NE; ++j)
-    if ((int)threadIdx.x + j * T < a.D) store1(a.y, a.y_type, base + j * T, s[j] * r);
+    if ((int)threadIdx.x + j * T < a.D) store1(a.y, a.y_type, base + j * T, s[j] * r * to8);
 }
 
 // Groups of G threads take rows of up to G NE values, all groups of a block together T threads.  The
@@ -656,17 +660,18 @@ __global__ void __launch_bounds__(256) rms_forward_any_kernel(const RmsArgs a) {
       v[1] = max_nan(v[1], fabsf(s * a.gamma[c]));
     }
     group_reduce<2>(v, 256, true, red);
-    float r = rsqrtf(v[0] * a.inv_d + a.eps);
+    const float r = rsqrtf(v[0] * a.inv_d + a.eps);
+    float to8 = 1.0f;
     if (a.y_type == TFL_E4M3) {
       const float amax = max_nan(v[1] * r, kMinAmax);
       if (threadIdx.x == 0) a.y_scale[row] = amax / kE4m3Max;
-      r *= kE4m3Max / amax;
+      to8 = kE4m3Max / amax;
     }
     for (int c = threadIdx.x; c < a.D; c += 256) {
       float s = load1(a.x, a.x_type, base + c);
       if (a.res) s += load1(a.res, a.res_type, base + c);
       if (a.res_out) store1(a.res_out, a.res_type, base + c, s);
-      store1(a.y, a.y_type, base + c, s * a.gamma[c] * r);
+      store1(a.y, a.y_type, base + c, s * a.gamma[c] * r * to8);
     }
   }
 }

@@ -40,3 +40,30 @@ def test_backward_of_tiny_rows(rows, d, xt, rt, eps, size):
     _close(_np(dx), ds, own + _u(xt) * np.abs(ds), "dx")
     _close(_np(dsum), ds, own + _u(rt) * np.abs(ds), "dsum")
     _close(_np(dgamma), dg, (rows / 304 + 64 + _n(d) + 12) * E * np.sum(np.abs(dy * s * r), axis=0) + 1e-30, "dgamma")
+
+
+# rows of zeros and rows whose y lies below the least maximum a scale is taken from (2^-100 = 7.9e-31),
+# beside ordinary ones: r up to 1e6 and 1e15, times 448 / 2^-100 = 5.7e32
+@pytest.mark.parametrize("eps,tiny", [(1e-12, 2.0 ** -126), (1e-14, 2.0 ** -126), (1e-30, 2.0 ** -130)])
+@pytest.mark.parametrize("rows,d", [(6, 8), (700, 1024), (6, 103), (6, 5001), (6, 8193), (6, 16384)])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_e4m3_of_rows_of_zeros_and_of_almost_nothing(rows, d, xt, eps, tiny):
+    import torch
+    pkg = _pkg()
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    x = torch.randn((rows, d), generator=gen, device="cuda")
+    x[1::6] = 0
+    x[2::6] = tiny * torch.randint(-3, 4, x[2::6].shape, generator=gen, device="cuda")
+    x, gamma = x.to(_type(xt)), torch.ones(d, device="cuda")
+    y, scale = torch.zeros((rows, d), device="cuda").to(_type("e4m3")), torch.zeros(rows, device="cuda")
+    h = pkg.tfl_rmsnorm_create(d, _code(xt), _code(xt), _code("e4m3"), eps)
+    pkg.tfl_rmsnorm_forward(h, rows, x.data_ptr(), None, gamma.data_ptr(), None, y.data_ptr(), scale.data_ptr(), _stream())
+    torch.cuda.synchronize()
+    pkg.tfl_rmsnorm_destroy(h)
+    _, ref = ops.rms_norm(_np(x), None, _np(gamma), float(np.float32(eps)))
+    rs = ops.row_scale(ref)
+    own = (_n(d) / 2 + 10) * E * np.abs(ref)
+    _close(_np(scale), rs, (_n(d) / 2 + 14) * E * rs, "scale")
+    assert (_np(y)[1::6] == 0).all() and (_np(y)[2::6] != 0).any()
+    # as in test_gpu_rmsnorm.py, in units of the scale (products with it leave no room for subnormals)
+    _close(_np(y), ref / rs[:, None], 2.0 ** -4 * np.abs(ref / rs[:, None]) + 2.0 ** -10 + 2 * own / rs[:, None], "y")
