@@ -53,7 +53,8 @@ __host__ __device__ constexpr int ring_bytes(bool wide) { return kGluSmem - 1024
 // the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
 // a = act(g) and, when wanted, slope = act'(g).
 //   SiLU  p = 1 / (1 + e^-g);  a = g p,  slope = p + p (g - a)
-//   GELU  exact erf form, erf from Abramowitz & Stegun 7.1.26 as in gelu2_as7126:
+//   GELU  exact erf form, erf from Abramowitz & Stegun 7.1.26 as in gelu_as7126 (its packed form takes
+//         max(g, 0) - |g| erfc / 2, which is no number at +infinity):
 //         a = g Phi(g),  slope = Phi(g) + g phi(g)
 template <int ACT, bool SLOPE>
 __device__ __forceinline__ void act2(uint64_t g, uint64_t& a, uint64_t& slope) {
@@ -64,8 +65,6 @@ __device__ __forceinline__ void act2(uint64_t g, uint64_t& a, uint64_t& slope) {
     const uint64_t p = f2_pack(rcp_approx(e0), rcp_approx(e1));
     a = f2_mul(g, p);
     if constexpr (SLOPE) slope = f2_fma(p, f2_sub(g, a), p);
-  } else if constexpr (!SLOPE) {
-    a = gelu2_as7126(g);
   } else {
     constexpr float p_s = 0.3275911f * 0.7071067811865476f;
     constexpr float h1 = 0.5f * 0.254829592f, h2 = 0.5f * -0.284496736f, h3 = 0.5f * 1.421413741f,
@@ -83,7 +82,7 @@ __device__ __forceinline__ void act2(uint64_t g, uint64_t& a, uint64_t& slope) {
     f2_unpack(f2_mul(f2_mul(t, poly), e), d0, d1);  // erfc(|g| / sqrt 2) / 2
     const uint64_t cdf = f2_pack(x0 >= 0.f ? 1.0f - d0 : d0, x1 >= 0.f ? 1.0f - d1 : d1);
     a = f2_mul(g, cdf);
-    slope = f2_fma(f2_mul(g, f2_splat(0.3989422804014327f)), e, cdf);
+    if constexpr (SLOPE) slope = f2_fma(f2_mul(g, f2_splat(0.3989422804014327f)), e, cdf);
   }
 }
 // N outputs of a row: g <- act(g) u.
