@@ -29,6 +29,7 @@ TFL_ERR_BAD_LENGTHS = -6
 # element types of the operators that stand on their own
 TFL_F32, TFL_F16, TFL_BF16, TFL_E4M3 = 0, 1, 2, 3
 TFL_ACT_SILU, TFL_ACT_GELU = 0, 1
+TFL_GLU_FORM_FEW, TFL_GLU_FORM_LONE, TFL_GLU_FORM_SHARED, TFL_GLU_FORM_PAIR, TFL_GLU_FORM_WIDE = range(5)
 
 KIND_NAMES = {1: "rownorm", 2: "gemm_qkv", 3: "attention", 4: "gemm_oproj", 5: "gemm_ffn1", 6: "gemm_ffn2",
               7: "postchain", 8: "stack"}
@@ -37,7 +38,7 @@ EXPORTS = ("tfl_default_options", "tfl_workspace_bytes", "tfl_create", "tfl_forw
            "tfl_forward_host", "tfl_forward_streamed",
            "tfl_attn_create", "tfl_attn_forward", "tfl_attn_backward", "tfl_attn_status", "tfl_attn_destroy",
            "tfl_status", "tfl_destroy", "tfl_last_error", "tfl_profile_forward", "tfl_launch_count",
-           "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu",
+           "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu", "tfl_selftest_glu_plan",
            "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy",
            "tfl_glu_create", "tfl_glu_forward", "tfl_glu_backward", "tfl_glu_status", "tfl_glu_destroy")
 
@@ -129,6 +130,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.tfl_launch_count.restype = ctypes.c_int
     lib.tfl_selftest_gelu.argtypes = [i32, ctypes.POINTER(ctypes.c_float), vp]
     lib.tfl_selftest_gelu.restype = ctypes.c_int
+    lib.tfl_selftest_glu_plan.argtypes = [i32, i32, i32, i32, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    lib.tfl_selftest_glu_plan.restype = ctypes.c_int
     lib.tfl_probe_wait_timeout.argtypes = [i64, vp]
     lib.tfl_probe_wait_timeout.restype = ctypes.c_int
     lib.tfl_rmsnorm_create.argtypes = [i32, i32, i32, i32, ctypes.c_float, ctypes.POINTER(vp)]
@@ -324,6 +327,15 @@ def tfl_selftest_gelu(n: int = 1 << 20, stream: int = 0) -> float:
     v = ctypes.c_float()
     _check(load().tfl_selftest_gelu(int(n), ctypes.byref(v), stream))
     return float(v.value)
+
+
+def tfl_selftest_glu_plan(d_model: int, d_ff: int, in_type: int, part: int, tokens: int, units=None):
+    """(form, output columns of a tile, tiles, tiles at once) of a feed-forward launch; part 0 is the forward,
+    1 to 3 the backward's; units: (CTAs, pairs, clusters of 2, 4 and 8) at once, or None for the current device."""
+    out = (ctypes.c_int32 * 4)()
+    u = None if units is None else (ctypes.c_int32 * 5)(*units)
+    _check(load().tfl_selftest_glu_plan(int(d_model), int(d_ff), int(in_type), int(part), int(tokens), u, out))
+    return tuple(out)
 
 
 def tfl_probe_wait_timeout(timeout_ns: int, stream: int = 0) -> int:

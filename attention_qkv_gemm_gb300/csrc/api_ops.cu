@@ -258,6 +258,15 @@ int glu_units(int dev, int sms, GluUnits* u) {
   return TFL_OK;
 }
 
+// How the forward and the three launches of the backward are cut.
+GluPlan glu_call_plan(int D, int F, bool f8, int mode, int64_t tokens, const GluUnits& u) {
+  const int ke = f8 ? 128 : 64;
+  const bool lines = D * (f8 ? 1 : 2) % 128 == 0;
+  if (mode == GLU_DX) return glu_plan(mode, lines, tokens, D, 2 * ((F + ke - 1) / ke), u);
+  if (mode == GLU_DW) return glu_plan(mode, lines, F, D, (tokens + ke - 1) / ke, u);
+  return glu_plan(mode, lines, tokens, F, (D + ke - 1) / ke, u);
+}
+
 constexpr int kMnBox = 64;  // MN-major operands come in boxes of 64 k rows
 
 int check_tokens(const tfl_glu* g, int64_t tokens) {
@@ -367,8 +376,7 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
     TFL_CUDA(launch_glu_few(g->in_type, a, g->units.sms, static_cast<cudaStream_t>(stream)), "feed-forward");
     return TFL_OK;
   }
-  const int ke = f8 ? 128 : 64, num_k = (g->D + ke - 1) / ke;
-  const GluPlan p = glu_plan(GLU_FORWARD, g->D * es % 128 == 0, tokens, g->F, num_k, g->units);
+  const GluPlan p = glu_call_plan(g->D, g->F, f8, GLU_FORWARD, tokens, g->units);
   GluMaps mp;
   if (!make_map(&mp.a0, x, tokens, g->D, (int)es, p.a_rows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bno) ||
       !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bno))
@@ -377,7 +385,7 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   GluArgs a = glu_args(g);
   a.M = (int)tokens;
   a.N = g->F;
-  a.num_k = num_k;
+  a.num_k = (g->D + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
   a.x_scale = x_scale;
   a.g_scale = wg_scale;
   a.u_scale = wu_scale;
@@ -419,10 +427,9 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
 
   const int Di = g->D, Fi = g->F, Ti = (int)tokens;
   const int kd = (Di + 63) / 64, kf = (Fi + 63) / 64, kt = (Ti + 63) / 64;
-  const bool lines = Di % 64 == 0;
-  const GluPlan p1 = glu_plan(GLU_SLOPES, lines, tokens, Fi, kd, g->units);
-  const GluPlan p2 = glu_plan(GLU_DX, lines, tokens, Di, 2 * kf, g->units);
-  const GluPlan p3 = glu_plan(GLU_DW, lines, Fi, Di, kt, g->units);
+  const GluPlan p1 = glu_call_plan(Di, Fi, false, GLU_SLOPES, tokens, g->units);
+  const GluPlan p2 = glu_call_plan(Di, Fi, false, GLU_DX, tokens, g->units);
+  const GluPlan p3 = glu_call_plan(Di, Fi, false, GLU_DW, tokens, g->units);
   GluMaps m1, m2, m3;
   bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bno) &&
             make_map(&m1.b1, wu, Fi, Di, 2, p1.bno);
@@ -461,6 +468,34 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.out = static_cast<uint16_t*>(dwg);
   a.out2 = static_cast<uint16_t*>(dwu);
   TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, st), "feed-forward weight gradients");
+  return TFL_OK;
+}
+
+int tfl_selftest_glu_plan(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t part, int64_t tokens,
+                          const int32_t* units, int32_t* out) {
+  g_err.clear();
+  const bool f8 = in_type == TFL_E4M3;
+  if (!out || d_model < 1 || d_ff < 1 || tokens < 1 || tokens > INT32_MAX - 512 || part < GLU_FORWARD || part > GLU_DW ||
+      !(f8 ? part == GLU_FORWARD : type_16bit(in_type)))
+    return fail(TFL_ERR_INVALID_ARG, "no such launch");
+  GluUnits u;
+  if (units) {
+    u.sms = units[0];
+    u.pairs = units[1];
+    for (int i = 0; i < 3; ++i) u.splits[i] = units[2 + i];
+    if (u.sms < 1 || u.pairs < 1) return fail(TFL_ERR_INVALID_ARG, "a device runs lone CTAs and pairs");
+  } else {
+    int dev = 0, sms = 0;
+    if (int rc = usable_device(&dev, &sms)) return rc;
+    if (int rc = glu_units(dev, sms, &u)) return rc;
+  }
+  for (int i = 0; i < 4; ++i) out[i] = 0;
+  if (part == GLU_FORWARD && glu_few_fits(tokens, (int64_t)d_model * (f8 ? 1 : 2))) return TFL_OK;
+  const GluPlan p = glu_call_plan(d_model, d_ff, f8, part, tokens, u);
+  out[0] = glu_form(p, part);
+  out[1] = p.bno;
+  out[2] = (int32_t)(p.tiles > INT32_MAX ? INT32_MAX : p.tiles);
+  out[3] = p.units;
   return TFL_OK;
 }
 

@@ -722,9 +722,15 @@ GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k
   return best;
 }
 
-cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s) {
+int glu_form(const GluPlan& p, int mode) {
   const bool wide = p.bno == (mode == GLU_FORWARD || mode == GLU_SLOPES ? kMaxBN / 2 : kMaxBN);
-  const int form = p.split > 1 ? kSplit : p.cg == 2 && wide ? kWide : kNarrow;
+  if (p.cg == 2) return wide ? TFL_GLU_FORM_WIDE : TFL_GLU_FORM_PAIR;
+  return p.split > 1 ? TFL_GLU_FORM_SHARED : TFL_GLU_FORM_LONE;
+}
+
+cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s) {
+  const int is = glu_form(p, mode);
+  const int form = is == TFL_GLU_FORM_SHARED ? kSplit : is == TFL_GLU_FORM_WIDE ? kWide : kNarrow;
 #define TFL_LAUNCH(CG, MODE, F8, FORM) \
   if (p.cg == CG && form == FORM && mode == MODE && f8 == F8) return launch_one<CG, MODE, F8, FORM>(mp, a, p, s);
   TFL_GLU_VARIANTS(TFL_LAUNCH)

@@ -82,6 +82,7 @@ struct GluUnits {
 };
 // whole_lines: the rows of x and the weights begin on 128-byte lines.
 GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const GluUnits& u);
+int glu_form(const GluPlan& p, int mode);  // TFL_GLU_FORM_* of the kernel it runs in
 // Kernel attributes, and all of *u but sms for the current device.
 cudaError_t prepare_glu_kernels(GluUnits* u);
 cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s);

@@ -243,6 +243,25 @@ int tfl_profile_forward(tfl_handle* h, const float* x, const int32_t* lengths,
  */
 int tfl_selftest_gelu(int32_t n, float* max_abs_diff, tfl_stream stream);
 
+/*
+ * Which kernel a launch of the gated feed-forward (below) takes, by the rule the
+ * calls themselves use, so that tests can show that they reach each one.  Host
+ * only.
+ *   part   0 the forward; 1, 2, 3 the backward's slopes, dx and weight gradients
+ *   units  what the device runs at once: CTAs with all of an SM's shared memory,
+ *          pairs of them, clusters of 2, 4 and 8; NULL: asked of the current device
+ *   out    a TFL_GLU_FORM_*, output columns of a tile, tiles, tiles at once (0s
+ *          after the form for the few-token kernel)
+ * Errors: INVALID_ARG, and without `units` UNSUPPORTED, CUDA.
+ */
+#define TFL_GLU_FORM_FEW    0   /* a few tokens, weights straight into MMA fragments */
+#define TFL_GLU_FORM_LONE   1   /* lone CTAs */
+#define TFL_GLU_FORM_SHARED 2   /* clusters of lone CTAs that share a tile's sum */
+#define TFL_GLU_FORM_PAIR   3   /* CTA pairs, tiles narrower than the accumulator */
+#define TFL_GLU_FORM_WIDE   4   /* CTA pairs, tiles as wide as it */
+int tfl_selftest_glu_plan(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t part, int64_t tokens,
+                          const int32_t* units, int32_t* out);
+
 /* Number of kernel launches one tfl_forward makes for this handle and causal flag. */
 int tfl_launch_count(const tfl_handle* h, int causal);
 

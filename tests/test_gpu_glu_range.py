@@ -1,5 +1,4 @@
-"""The gated feed-forward's values at the ends of their range: gates that overflow to infinity, and
-scales whose product leaves fp32's range."""
+"""The gated feed-forward at the ends of its range: gates that overflow to infinity."""
 import pytest
 
 pytestmark = pytest.mark.gpu
