@@ -100,3 +100,63 @@ def test_backward(tokens, d, f, t, act):
         _close(out, r, 1.01 * bound + U[t] * r.abs() + TINY[t], 1.2 * U[t], what)
     del eg, eu, edg, edu
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("tokens,d,f", sorted(set(glu_forms.FORWARD + glu_forms.BACKWARD)))
+def test_rows_do_not_affect_one_another(tokens, d, f):
+    """Rows with no numbers and infinities at the ends of tiles: the other rows keep their bits, forward and dx."""
+    import torch
+    from tests.test_gpu_glu import _inputs
+    pkg = _pkg()
+    x, wg, wu, dh = _inputs(tokens, d, f, "bf16", 4)
+    bad = sorted({1, min(127, tokens - 1), tokens // 2, tokens - 2})
+    code, a = _codes("bf16", "silu")
+    op = pkg.tfl_glu_create(d, f, code, code, a, tokens)
+    out = []
+    for dirty in (False, True):
+        if dirty:
+            x[bad, 3] = float("nan")
+            x[bad[0], 5] = float("inf")
+        h, dx, dwg, dwu = torch.empty_like(dh), torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+        P = lambda t: t.data_ptr()  # noqa: E731
+        pkg.tfl_glu_forward(op, tokens, P(x), None, P(wg), None, P(wu), None, P(h), _stream())
+        pkg.tfl_glu_backward(op, tokens, P(x), P(wg), P(wu), P(dh), P(dx), P(dwg), P(dwu), _stream())
+        out.append((h, dx))
+    assert pkg.tfl_glu_status(op, _stream()) == 0
+    pkg.tfl_glu_destroy(op)
+    keep = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    for clean, dirty in zip(*out):
+        assert torch.equal(clean[keep], dirty[keep]) and clean.isfinite().all() and dirty[bad].isnan().all()
+
+
+@pytest.mark.parametrize("tokens,d,f", glu_forms.BACKWARD)
+def test_same_bits_every_time_and_in_a_graph(tokens, d, f):
+    """Forward and backward one behind the other, twice, and captured and replayed on another stream."""
+    import torch
+    from tests.test_gpu_glu import _inputs
+    pkg = _pkg()
+    x, wg, wu, dh = _inputs(tokens, d, f, "f16", 5)
+    code, a = _codes("f16", "gelu")
+    op = pkg.tfl_glu_create(d, f, code, code, a, tokens)
+    out = torch.empty_like(dh), torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+    P = lambda t: t.data_ptr()  # noqa: E731
+
+    def step(st):
+        pkg.tfl_glu_forward(op, tokens, P(x), None, P(wg), None, P(wu), None, P(out[0]), st)
+        pkg.tfl_glu_backward(op, tokens, P(x), P(wg), P(wu), P(dh), P(out[1]), P(out[2]), P(out[3]), st)
+
+    step(_stream())
+    ref = [v.clone() for v in out]
+    st, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=st):
+        step(st.cuda_stream)
+    for again in (lambda: step(_stream()), graph.replay, graph.replay):
+        for v in out:
+            v.zero_()
+        again()
+        torch.cuda.synchronize()
+        assert all(torch.equal(v, r) for v, r in zip(out, ref))
+    assert pkg.tfl_glu_status(op, _stream()) == 0
+    pkg.tfl_glu_destroy(op)

@@ -15,7 +15,7 @@ def _stream():
 
 
 # the few-token kernel, lone CTAs, CTAs that share a sum, pairs of narrow and of wide tiles
-@pytest.mark.parametrize("tokens,d,f", [(3, 64, 64), (40, 64, 64), (40, 4096, 64), (3000, 64, 1024), (3000, 64, 8192)])
+@pytest.mark.parametrize("tokens,d,f", [(3, 64, 64), (40, 64, 64), (40, 4096, 64), (7824, 216, 304), (6763, 136, 584)])
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_infinite_gates(tokens, d, f, act):
     """Gates of +-3e38 x 2, which overflow fp32, beside u = 2: act(inf) = inf; act(-inf) = -inf times 0,

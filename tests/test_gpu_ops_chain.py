@@ -66,7 +66,7 @@ class Chain:
 
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("tokens,d,f", [(1, 1024, 1040), (1, 4096, 4096), (8, 2048, 2080), (16, 512, 2048), (40, 4096, 2048),
-                                        (200, 1024, 2048)])
+                                        (200, 1024, 2048), (1500, 512, 2064)])
 def test_turns_on_the_same_buffers_equal_turns_alone(tokens, d, f, e4m3):
     import torch
     c = Chain(tokens, d, f, e4m3)
