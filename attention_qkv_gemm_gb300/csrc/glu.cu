@@ -19,13 +19,13 @@
 // accumulators so that a tile's epilogue runs under the next tile's MMAs.
 //
 // What bounds it: with many tokens the tensor cores, and in long runs the power cap (8192 x 1024 x 4096
-// fp16 forward 74 us in a burst, 1.86 PFLOP/s, 0.99 of the measured burst rate, 93 us in a long run;
-// 16384 x 2048 x 8192 bf16 backward 1.76 ms and 2.03 ms); with few tokens the weights' bytes (40 x 4096 x
-// 10240 e4m3: 16.4 us for 85 MB, 5.2 TB/s).  A pair's 256 x 256 tile took the first two from 107 to 101 us
-// and from 2.26 to 2.06 ms against a lone CTA's 128 x 256, a thread that the compiler knows to be alone
-// for the issue of MMAs from 82 to 74 us and from 1.95 to 1.76 ms (bursts).  The epilogue's arithmetic is
-// not free even where it hides under the MMAs: its warps take issue slots from that thread, hence packed
-// pairs and the short issue loop.
+// fp16 forward 78 us in a burst, 1.76 PFLOP/s, 0.94 of the measured burst rate, 92 us in a long run;
+// 16384 x 2048 x 8192 bf16 backward 1.71 ms and 2.01 ms; 74 us and 1.76 ms on another GPU); with few
+// tokens the weights' bytes (40 x 4096 x 10240 e4m3: 16.4 us for 85 MB, 5.2 TB/s).  A pair's 256 x 256
+// tile took the first two from 107 to 101 us and from 2.26 to 2.06 ms against a lone CTA's 128 x 256, a
+// thread that the compiler knows to be alone for the issue of MMAs from 82 to 74 us and from 1.95 to
+// 1.76 ms (bursts, one GPU).  The epilogue's arithmetic is not free even where it hides under the MMAs:
+// its warps take issue slots from that thread, hence packed pairs and the short issue loop.
 //
 // Ragged sizes: TMA fills what lies outside a matrix with zeros (zero rows and zero k add
 // nothing), and the epilogue stores only rows and columns that exist.
@@ -656,22 +656,24 @@ cudaError_t prepare_glu_kernels(GluUnits* u) {
 // MMA still reads 128, the others being whatever lies behind, and their results are not stored.
 //
 // The cut goes by an estimate of the cycles a launch takes.  Its constants were fitted to the times of
-// all cuts of 192 sizes (12 to 3000 tokens, weights of 520 x 5696 to 4096 x 10240, all modes): the cut
-// that it takes is 1 % slower than the fastest on average, 11 % at worst.
+// all cuts of 192 launches (12 to 3000 tokens, weights of 520 x 5696 to 4096 x 10240, all modes) before the
+// wide tiles had sixteen epilogue warps; with them, the cut that it takes is still 1 % slower than the
+// fastest on average, 19 % at worst (100 x 1024 x 4096 bf16, 7.0 us where tiles of 32 columns take 5.9).
 //   A k-block costs its products (a 256-column accumulator: 555, narrower ones 8 % more a column; e4m3's
 //   have twice the k), its operand stream from L2 (74 bytes a cycle and SM, 44 where rows do not begin
 //   on a 128-byte line and a box row takes two) or issuing its four MMAs and commit (240, a pair 350),
 //   whichever is longest.
 //   A round of tiles costs its k-blocks or its share of what has to come from memory (3800 bytes a
 //   cycle, which fewer than about 112 SMs do not draw), whichever is longer, and 0.44 of the other; at
-//   least its epilogues, 450 for each turn of the two warps of a lane quarter.
+//   least its epilogues, 450 for each turn of two warps of a lane quarter (the wide tiles' four are
+//   charged the same).
 //   The last tile's epilogue is not hidden: 1200 a turn.
 //   Pairs start later and end later (1950).  Sharing a tile's k-blocks out to a cluster costs two
 //   meetings (1100) and the exchange of the sums (11 bytes a cycle and CTA); the pieces have to fit in
 //   the ring.
 // So wide tiles where there are rounds of them, narrower ones where that fills a last round or
 // spreads the weights of a few rows over all SMs, and shared k-blocks where the tiles are few and
-// the rows long (60 tokens x 2048 x 8192 backward: 110 -> 57 us, most of it dx).
+// the rows long (60 tokens x 2048 x 8192 backward: 110 -> 55 us, most of it dx).
 GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const GluUnits& u) {
   const bool two = mode == GLU_FORWARD || mode == GLU_SLOPES;
   const int64_t twice = mode == GLU_DW ? 2 : 1;

@@ -391,7 +391,7 @@ void tfl_attn_destroy(tfl_attn* a);
  */
 typedef struct tfl_rmsnorm tfl_rmsnorm;
 
-/* d_model in 1 .. 2^24, eps >= 0 and finite.  Unless y is e4m3 the handle also holds the
+/* d_model in 1 .. 2^24, eps >= 0 and finite.  Where y is of x's type the handle also holds the
  * backward's scratch (at most max(64 MiB, 4 d_model bytes)).
  * Errors: INVALID_ARG, UNSUPPORTED (types, device), OOM, CUDA. */
 int tfl_rmsnorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int32_t y_type, float eps,
@@ -448,7 +448,7 @@ void tfl_rmsnorm_destroy(tfl_rmsnorm* n);
  * as tfl_rmsnorm_forward writes x), and an fp16 or bf16 output.
  */
 #define TFL_ACT_SILU 0   /* z / (1 + e^-z) */
-#define TFL_ACT_GELU 1   /* exact erf form */
+#define TFL_ACT_GELU 1   /* z Phi(z), the exact erf form (Phi to 7.5e-8 absolute) */
 typedef struct tfl_glu tfl_glu;
 
 /* d_model and d_ff: multiples of 8 (16 for e4m3 operands) up to 2^24.
