@@ -47,7 +47,8 @@ def test_every_size_is_cut_within_the_kernels_limits(units):
 
 
 @pytest.mark.parametrize("args", [(0, 64, 2, 0, 1), (64, 0, 2, 0, 1), (64, 64, 0, 0, 1), (64, 64, 2, 4, 1), (64, 64, 2, -1, 1),
-                                  (64, 64, 3, 1, 1), (64, 64, 2, 0, 0), (64, 64, 2, 0, 1 << 31)])
+                                  (64, 64, 3, 1, 1), (64, 64, 2, 0, 0), (64, 64, 2, 0, 1 << 31), ((1 << 24) + 8, 64, 2, 0, 1),
+                                  (64, (1 << 24) + 8, 2, 0, 1)])
 def test_refusals(args):
     with pytest.raises(pkg.TflError) as e:
         pkg.tfl_selftest_glu_plan(*args, (152, 76, 76, 38, 18))
