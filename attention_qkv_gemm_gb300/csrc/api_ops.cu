@@ -475,7 +475,8 @@ int tfl_selftest_glu_plan(int32_t d_model, int32_t d_ff, int32_t in_type, int32_
                           const int32_t* units, int32_t* out) {
   g_err.clear();
   const bool f8 = in_type == TFL_E4M3;
-  if (!out || d_model < 1 || d_model > (1 << 24) || d_ff < 1 || d_ff > (1 << 24) || tokens < 1 || tokens > INT32_MAX - 512 || part < GLU_FORWARD || part > GLU_DW ||
+  if (!out || d_model < 1 || d_model > (1 << 24) || d_ff < 1 || d_ff > (1 << 24) || tokens < 1 ||
+      tokens > INT32_MAX - 512 || part < GLU_FORWARD || part > GLU_DW ||
       !(f8 ? part == GLU_FORWARD : type_16bit(in_type)))
     return fail(TFL_ERR_INVALID_ARG, "no such launch");
   GluUnits u;
