@@ -40,6 +40,7 @@ EXPORTS = ("tfl_default_options", "tfl_workspace_bytes", "tfl_create", "tfl_forw
            "tfl_status", "tfl_destroy", "tfl_last_error", "tfl_profile_forward", "tfl_launch_count",
            "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu", "tfl_selftest_glu_plan",
            "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy",
+           "tfl_layernorm_create", "tfl_layernorm_forward", "tfl_layernorm_backward", "tfl_layernorm_destroy",
            "tfl_glu_create", "tfl_glu_forward", "tfl_glu_backward", "tfl_glu_status", "tfl_glu_destroy")
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -142,6 +143,14 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.tfl_rmsnorm_backward.restype = ctypes.c_int
     lib.tfl_rmsnorm_destroy.argtypes = [vp]
     lib.tfl_rmsnorm_destroy.restype = None
+    lib.tfl_layernorm_create.argtypes = [i32, i32, i32, i32, ctypes.c_float, ctypes.POINTER(vp)]
+    lib.tfl_layernorm_create.restype = ctypes.c_int
+    lib.tfl_layernorm_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_layernorm_forward.restype = ctypes.c_int
+    lib.tfl_layernorm_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_layernorm_backward.restype = ctypes.c_int
+    lib.tfl_layernorm_destroy.argtypes = [vp]
+    lib.tfl_layernorm_destroy.restype = None
     lib.tfl_glu_create.argtypes = [i32, i32, i32, i32, i32, i64, ctypes.POINTER(vp)]
     lib.tfl_glu_create.restype = ctypes.c_int
     lib.tfl_glu_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -267,6 +276,34 @@ def tfl_rmsnorm_backward(handle: int, rows: int, sum: int, gamma: int, dy: int, 
 def tfl_rmsnorm_destroy(handle: int) -> None:
     if handle:
         load().tfl_rmsnorm_destroy(handle)
+
+
+def tfl_layernorm_create(d_model: int, x_type: int, res_type: int, y_type: int, eps: float = 1e-5) -> int:
+    """A layer norm with the residual's addition; types are ``TFL_F32`` and so on."""
+    h = ctypes.c_void_p()
+    _check(load().tfl_layernorm_create(int(d_model), int(x_type), int(res_type), int(y_type), float(eps),
+                                       ctypes.byref(h)))
+    return h.value
+
+
+def tfl_layernorm_forward(handle: int, rows: int, x: int, res: Optional[int], gamma: int, beta: Optional[int],
+                          res_out: Optional[int], y: int, y_scale: Optional[int] = None, stats: Optional[int] = None,
+                          stream: int = 0) -> None:
+    """res_out = x + res; y = its layer norm times gamma plus beta (device pointers to [rows, d_model]);
+    stats: [rows, 2], each row's mean and 1 / sqrt(var + eps), for the backward."""
+    _check(load().tfl_layernorm_forward(handle, rows, x, res, gamma, beta, res_out, y, y_scale, stats, stream))
+
+
+def tfl_layernorm_backward(handle: int, rows: int, sum: int, stats: int, gamma: int, dy: int, dres: Optional[int],
+                           dx: Optional[int], dsum: Optional[int], dgamma: int, dbeta: Optional[int],
+                           stream: int = 0) -> None:
+    """The gradient of x + res (as dx in x's type, as dsum in the residual's), of gamma and of beta."""
+    _check(load().tfl_layernorm_backward(handle, rows, sum, stats, gamma, dy, dres, dx, dsum, dgamma, dbeta, stream))
+
+
+def tfl_layernorm_destroy(handle: int) -> None:
+    if handle:
+        load().tfl_layernorm_destroy(handle)
 
 
 def tfl_glu_create(d_model: int, d_ff: int, in_type: int, out_type: int, act: int = TFL_ACT_SILU,

@@ -1,5 +1,5 @@
 // api_ops.cu -- the C ABI of the operators that stand on their own (include/tfl.h): the
-// root-mean-square norm and the gated feed-forward.
+// root-mean-square norm, layer norm, the gated feed-forward and the linear layer.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -64,6 +64,26 @@ int same_device(int device) {
   return TFL_OK;
 }
 
+// What the two norms are created with.
+int check_norm(int32_t d_model, int32_t x_type, int32_t res_type, int32_t y_type, float eps) {
+  if (d_model < 1 || d_model > (1 << 24)) return fail(TFL_ERR_INVALID_ARG, "d_model must be in 1 .. 2^24");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(TFL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (x_type != TFL_F32 && !type_16bit(x_type)) return fail(TFL_ERR_UNSUPPORTED, "x must be fp32, fp16 or bf16");
+  if (res_type != TFL_F32 && res_type != x_type)
+    return fail(TFL_ERR_UNSUPPORTED, "the residual must be fp32 or of x's type");
+  if (!(y_type == x_type || y_type == TFL_E4M3 || (x_type == TFL_F32 && type_16bit(y_type))))
+    return fail(TFL_ERR_UNSUPPORTED, "y must be of x's type or e4m3, or fp16 or bf16 for an fp32 x");
+  return TFL_OK;
+}
+
+// Rows of partial sums of a backward, one a block: as many blocks as fill the GPU, but no more rows of
+// `values` floats than 64 MiB hold.
+int partial_rows(int64_t values, int sms) {
+  const int64_t fit = ((int64_t)64 << 20) / (values * 4);
+  const int64_t want = (int64_t)sms * 4;
+  return (int)(fit < 1 ? 1 : fit < want ? fit : want);
+}
+
 }  // namespace
 
 // ---------------------------------------------------------------------------
@@ -83,13 +103,7 @@ int tfl_rmsnorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int32_
   g_err.clear();
   if (!out) return fail(TFL_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
-  if (d_model < 1 || d_model > (1 << 24)) return fail(TFL_ERR_INVALID_ARG, "d_model must be in 1 .. 2^24");
-  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(TFL_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  if (x_type != TFL_F32 && !type_16bit(x_type)) return fail(TFL_ERR_UNSUPPORTED, "x must be fp32, fp16 or bf16");
-  if (res_type != TFL_F32 && res_type != x_type)
-    return fail(TFL_ERR_UNSUPPORTED, "the residual must be fp32 or of x's type");
-  if (!(y_type == x_type || y_type == TFL_E4M3 || (x_type == TFL_F32 && type_16bit(y_type))))
-    return fail(TFL_ERR_UNSUPPORTED, "y must be of x's type or e4m3, or fp16 or bf16 for an fp32 x");
+  if (int rc = check_norm(d_model, x_type, res_type, y_type, eps)) return rc;
   int dev = 0, sms = 0;
   if (int rc = usable_device(&dev, &sms)) return rc;
   tfl_rmsnorm* n = new (std::nothrow) tfl_rmsnorm();
@@ -102,11 +116,7 @@ int tfl_rmsnorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int32_
   n->device = dev;
   n->num_sms = sms;
   if (y_type == x_type) {
-    // one row of partial sums a block of the backward: as many blocks as fill the GPU, but
-    // no more rows than 64 MiB hold
-    const int64_t fit = ((int64_t)64 << 20) / ((int64_t)d_model * 4);
-    const int64_t want = (int64_t)sms * 4;
-    n->blocks = (int)(fit < 1 ? 1 : fit < want ? fit : want);
+    n->blocks = partial_rows(d_model, sms);
     if (cudaMalloc(&n->partial, (size_t)n->blocks * d_model * sizeof(float)) != cudaSuccess) {
       cudaGetLastError();
       delete n;
@@ -208,6 +218,165 @@ int tfl_rmsnorm_backward(tfl_rmsnorm* n, int64_t rows, const void* sum, const fl
 }
 
 void tfl_rmsnorm_destroy(tfl_rmsnorm* n) {
+  if (!n) return;
+  release(n->device, n->partial);
+  delete n;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Layer norm.
+struct tfl_layernorm {
+  int D = 0, x_type = 0, res_type = 0, y_type = 0;
+  float eps = 0.f;
+  int device = 0, num_sms = 0;
+  float* partial = nullptr;  // [blocks, 2 D], the backward's partial sums of dgamma and dbeta
+  int blocks = 0;
+};
+
+extern "C" {
+
+int tfl_layernorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int32_t y_type, float eps,
+                         tfl_layernorm** out) {
+  g_err.clear();
+  if (!out) return fail(TFL_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (int rc = check_norm(d_model, x_type, res_type, y_type, eps)) return rc;
+  int dev = 0, sms = 0;
+  if (int rc = usable_device(&dev, &sms)) return rc;
+  tfl_layernorm* n = new (std::nothrow) tfl_layernorm();
+  if (!n) return fail(TFL_ERR_OOM, "handle allocation failed");
+  n->D = d_model;
+  n->x_type = x_type;
+  n->res_type = res_type;
+  n->y_type = y_type;
+  n->eps = eps;
+  n->device = dev;
+  n->num_sms = sms;
+  if (y_type == x_type) {
+    n->blocks = partial_rows((int64_t)d_model * 2, sms);
+    if (cudaMalloc(&n->partial, (size_t)n->blocks * d_model * 2 * sizeof(float)) != cudaSuccess) {
+      cudaGetLastError();
+      delete n;
+      return fail(TFL_ERR_OOM, "scratch allocation for the norm's backward failed");
+    }
+  }
+  *out = n;
+  return TFL_OK;
+}
+
+int tfl_layernorm_forward(tfl_layernorm* n, int64_t rows, const void* x, const void* res, const float* gamma,
+                          const float* beta, void* res_out, void* y, float* y_scale, float* stats, tfl_stream stream) {
+  g_err.clear();
+  if (!n) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  if (rows < 0 || rows >= ((int64_t)1 << 31)) return fail(TFL_ERR_INVALID_ARG, "rows must be in 0 .. 2^31 - 1");
+  if (rows == 0) return TFL_OK;
+  if (!x || !gamma || !y) return fail(TFL_ERR_INVALID_ARG, "x, gamma and y must be non-NULL device pointers");
+  if ((n->y_type == TFL_E4M3) != (y_scale != nullptr))
+    return fail(TFL_ERR_INVALID_ARG, "y_scale goes with an e4m3 y, and only with one");
+  const size_t xs = type_size(n->x_type), rs = type_size(n->res_type), ys = type_size(n->y_type);
+  if (misaligned(x, xs) || misaligned(res, rs) || misaligned(res_out, rs) || misaligned(y, ys) ||
+      misaligned(gamma, 4) || misaligned(beta, 4) || misaligned(y_scale, 4))
+    return fail(TFL_ERR_INVALID_ARG, "a buffer is not aligned to its elements");
+  if (misaligned(stats, 8)) return fail(TFL_ERR_INVALID_ARG, "stats must be 8-byte aligned");
+  const size_t count = (size_t)rows * n->D, D = n->D;
+  const Span ins[4] = {{x, count * xs, n->x_type}, {res, count * rs, n->res_type}, {gamma, D * 4, TFL_F32}, {beta, D * 4, TFL_F32}};
+  const Span outs[4] = {{res_out, count * rs, n->res_type},
+                        {y, count * ys, n->y_type},
+                        {y_scale, (size_t)rows * 4, TFL_F32},
+                        {stats, (size_t)rows * 8, TFL_F32}};
+  bool bad = false;
+  for (int o = 0; o < 4; ++o) {
+    // res_out may be res or x, y may be x
+    for (int i = 0; i < 4; ++i) bad = bad || overlap(outs[o], ins[i], (o == 0 && i < 2) || (o == 1 && i == 0));
+    for (int k = 0; k < o; ++k) bad = bad || overlap(outs[o], outs[k], false);
+  }
+  if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+  if (int rc = same_device(n->device)) return rc;
+  LnArgs a;
+  a.rows = rows;
+  a.D = n->D;
+  a.inv_d = 1.0f / (float)n->D;
+  a.eps = n->eps;
+  a.x_type = n->x_type;
+  a.res_type = n->res_type;
+  a.y_type = n->y_type;
+  a.x = x;
+  a.res = res;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.res_out = res_out;
+  a.y = y;
+  a.y_scale = y_scale;
+  a.stats = reinterpret_cast<float2*>(stats);
+  TFL_CUDA(launch_ln_forward(a, n->num_sms, static_cast<cudaStream_t>(stream)), "layer norm forward");
+  return TFL_OK;
+}
+
+int tfl_layernorm_backward(tfl_layernorm* n, int64_t rows, const void* sum, const float* stats, const float* gamma,
+                           const void* dy, const void* dres, void* dx, void* dsum, float* dgamma, float* dbeta,
+                           tfl_stream stream) {
+  g_err.clear();
+  if (!n) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  if (n->y_type != n->x_type) return fail(TFL_ERR_UNSUPPORTED, "the backward needs a norm whose y is of x's type");
+  if (rows < 0 || rows >= ((int64_t)1 << 31)) return fail(TFL_ERR_INVALID_ARG, "rows must be in 0 .. 2^31 - 1");
+  if (!dgamma || misaligned(dgamma, 4)) return fail(TFL_ERR_INVALID_ARG, "dgamma must be a 4-byte aligned device pointer");
+  if (misaligned(dbeta, 4)) return fail(TFL_ERR_INVALID_ARG, "dbeta must be 4-byte aligned");
+  const size_t D = n->D;
+  const Span sd[2] = {{dgamma, D * 4, TFL_F32}, {dbeta, D * 4, TFL_F32}};
+  if (overlap(sd[0], sd[1], false)) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+  if (int rc = same_device(n->device)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    TFL_CUDA(cudaMemsetAsync(dgamma, 0, D * 4, st), "dgamma clear");
+    if (dbeta) TFL_CUDA(cudaMemsetAsync(dbeta, 0, D * 4, st), "dbeta clear");
+    return TFL_OK;
+  }
+  if (!sum || !stats || !gamma || !dy)
+    return fail(TFL_ERR_INVALID_ARG, "sum, stats, gamma and dy must be non-NULL device pointers");
+  if (!dx && !dsum) return fail(TFL_ERR_INVALID_ARG, "dx or dsum must be given");
+  const size_t xs = type_size(n->x_type), rs = type_size(n->res_type);
+  if (misaligned(sum, rs) || misaligned(gamma, 4) || misaligned(dy, xs) || misaligned(dres, rs) ||
+      misaligned(dx, xs) || misaligned(dsum, rs))
+    return fail(TFL_ERR_INVALID_ARG, "a buffer is not aligned to its elements");
+  if (misaligned(stats, 8)) return fail(TFL_ERR_INVALID_ARG, "stats must be 8-byte aligned");
+  const size_t count = (size_t)rows * D;
+  const Span ins[3] = {{sum, count * rs, n->res_type}, {dy, count * xs, n->x_type}, {dres, count * rs, n->res_type}};
+  const Span outs[2] = {{dx, count * xs, n->x_type}, {dsum, count * rs, n->res_type}};
+  const Span sg{gamma, D * 4, TFL_F32}, ss{stats, (size_t)rows * 8, TFL_F32};
+  bool bad = overlap(outs[0], outs[1], false);
+  for (const Span& o : outs) {
+    for (const Span& i : ins) bad = bad || overlap(o, i, true);
+    bad = bad || overlap(o, sg, false) || overlap(o, ss, false) || overlap(o, sd[0], false) || overlap(o, sd[1], false);
+  }
+  for (const Span& d : sd) {
+    for (const Span& i : ins) bad = bad || overlap(d, i, false);
+    bad = bad || overlap(d, sg, false) || overlap(d, ss, false);
+  }
+  if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+  LnGradArgs a;
+  a.rows = rows;
+  a.D = n->D;
+  a.inv_d = 1.0f / (float)n->D;
+  a.x_type = n->x_type;
+  a.res_type = n->res_type;
+  a.sum = sum;
+  a.stats = reinterpret_cast<const float2*>(stats);
+  a.gamma = gamma;
+  a.dy = dy;
+  a.dres = dres;
+  a.dx = dx;
+  a.dsum = dsum;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.partial = n->partial;
+  a.blocks = n->blocks;
+  TFL_CUDA(launch_ln_backward(a, n->num_sms, st), "layer norm backward");
+  return TFL_OK;
+}
+
+void tfl_layernorm_destroy(tfl_layernorm* n) {
   if (!n) return;
   release(n->device, n->partial);
   delete n;

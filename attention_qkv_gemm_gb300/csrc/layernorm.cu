@@ -1,0 +1,697 @@
+// layernorm.cu -- layer norm with the residual's addition, forward and backward.
+//
+//   s = x + res,  m = mean(s),  r = 1 / sqrt(mean((s - m)^2) + eps),  t = (s - m) r,  y = t gamma + beta
+// and, with a = dy gamma, the gradients of s, gamma and beta:
+//   ds = dres + r (a - mean(a) - t mean(a t)),   dgamma = sum over rows of dy t,   dbeta = sum of dy
+//
+// Every value is read once and written once: bandwidth bounds it.  As in rmsnorm.cu a row lives in the
+// registers of TPR threads between its loads and its stores.  The variance is taken from the centred
+// values of the row in registers, never as mean(s^2) - m^2, which loses everything where the mean is
+// large.  The mean itself is off by the rounding of a sum of D terms; the centred values' own mean d
+// repairs it (m + d, and (s - m)^2 less d^2), which costs one more sum in the same butterfly.
+//
+// The backward takes m and r from the forward (8 bytes a row): from s alone it would need two more
+// sums a row that wait for each other before the two that the gradient needs.
+//
+// Widths that 8 does not divide, unaligned buffers and rows too long for registers take the
+// element-wise kernels.
+#include "rowops.cuh"
+
+namespace tfl {
+
+namespace {
+
+// gamma and beta: read by every row, from L1
+__device__ __forceinline__ void load_params2(const float* p, uint64_t* v) {
+  float f[8];
+  load8(p, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+}
+
+// From the sums over a row's centred values c = s - m0: sum c and sum c^2, the row's mean and 1 / sqrt(var + eps).
+__device__ __forceinline__ void finish_stats(float m0, float sum, float square, const LnArgs& a, float& shift, float& mean,
+                                             float& rstd) {
+  shift = sum * a.inv_d;  // a NaN stays one
+  mean = m0 + shift;
+  rstd = rsqrtf(max_nan(square * a.inv_d - shift * shift, 0.f) + a.eps);
+}
+
+template <class X, class R, class Y, int NV>
+__global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
+  constexpr bool Q = sizeof(Y) == 1;
+  __shared__ float red[64];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const int tpr = a.tpr, t = threadIdx.x & (tpr - 1);
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+  const bool live = row < a.rows;  // the whole block meets at group_reduce's barriers
+  const int nvec = a.D >> 3;
+  const size_t base = (size_t)row * a.D;
+  float s[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = t + j * tpr;
+    if (live && c < nvec) {
+      load8(static_cast<const X*>(a.x) + base + c * 8, s[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[j][i] = 0.f;
+    }
+  }
+  if (a.res) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = t + j * tpr;
+      if (live && c < nvec) {
+        float r[8];
+        load8(static_cast<const R*>(a.res) + base + c * 8, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] += r[i];
+      }
+    }
+  }
+  // While this row is reduced, the rows of the block that will take this one's place start on
+  // their way to L2.
+  const int64_t later = row + a.ahead;
+  if (later < a.rows) {
+    lines_to_l2(static_cast<const X*>(a.x) + (size_t)later * a.D, a.D * (int)sizeof(X), t, tpr);
+    if (a.res) lines_to_l2(static_cast<const R*>(a.res) + (size_t)later * a.D, a.D * (int)sizeof(R), t, tpr);
+  }
+  float v[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[0] += s[j][i];
+  }
+  if (a.res_out) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = t + j * tpr;
+      if (live && c < nvec) store8(static_cast<R*>(a.res_out) + base + c * 8, s[j]);
+    }
+  }
+  group_reduce<1>(v, tpr, false, red);
+  const float m0 = v[0] * a.inv_d;
+  v[0] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (t + j * tpr < nvec) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[j][i] -= m0;
+        v[0] += s[j][i];
+        v[1] = fmaf(s[j][i], s[j][i], v[1]);
+      }
+    }
+  }
+  group_reduce<2>(v, tpr, false, red);
+  float shift, mean, r;
+  finish_stats(m0, v[0], v[1], a, shift, mean, r);
+  if (a.stats && live && t == 0) a.stats[row] = make_float2(mean, r);
+  v[0] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = t + j * tpr;
+    if (live && c < nvec) {
+      float g[8], b[8];
+      load8(a.gamma + c * 8, g);
+      if (a.beta) {
+        load8(a.beta + c * 8, b);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[j][i] = fmaf((s[j][i] - shift) * r, g[i], b[i]);
+        if (Q) v[0] = max_nan(v[0], fabsf(s[j][i]));
+      }
+      if (!Q) store8(static_cast<Y*>(a.y) + base + c * 8, s[j]);
+    }
+  }
+  if constexpr (Q) {
+    group_reduce<1>(v, tpr, true, red);
+    const float amax = max_nan(v[0], kMinAmax);
+    if (live && t == 0) a.y_scale[row] = amax / kE4m3Max;
+    const float to8 = kE4m3Max / amax;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = t + j * tpr;
+      if (live && c < nvec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[j][i] *= to8;
+        store8(static_cast<Y*>(a.y) + base + c * 8, s[j]);
+      }
+    }
+  }
+}
+
+// Backward.  As in rms_backward_kernel: a row group keeps its columns over all its rows, so each thread
+// holds gamma and sums dgamma and dbeta of its own columns in registers; the groups of a block are joined
+// in shared memory and every block writes one row of partial sums, which column_sums_kernel adds in block
+// order: the result depends on the sizes and the SM count only.  The next row is loaded, as stored, before
+// the current one is worked on.
+template <class X, class R, int NV, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGradArgs a) {
+  constexpr bool AHEAD = NV == 1 || (NV == 2 && sizeof(R) == 2);  // room for the next row
+  constexpr bool KEEP = NV == 1;                                  // room for gamma
+  __shared__ float2 red[2][32];
+  extern __shared__ float part[];  // [groups][D + 4] when the block has more than one group
+  grid_launch_dependents();
+  grid_wait_prior();
+  const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr;
+  const int nvec = a.D >> 3, rows = (int)a.rows;
+  const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
+  bool in[NV];  // vectors of this thread that exist
+  uint64_t dg[NV][4], db[NV][4], gk[KEEP ? NV : 1][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    in[j] = t + j * tpr < nvec;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dg[j][i] = db[j][i] = 0;  // two zeros
+    if constexpr (KEEP) {
+      if (in[j]) {
+        load_params2(a.gamma + (t + j * tpr) * 8, gk[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gk[j][i] = 0;
+      }
+    }
+  }
+  // this thread's first vector of the row to load next and of the row to write next
+  const size_t step = (size_t)stride * a.D, begin = (size_t)first * a.D + t * 8;
+  const R* sp = static_cast<const R*>(a.sum) + begin;
+  const X* yp = static_cast<const X*>(a.dy) + begin;
+  const R* ep = a.dres ? static_cast<const R*>(a.dres) + begin : nullptr;
+  const R* ep_late = ep;
+  const float2* stat = a.stats + first;
+  R* dsum = a.dsum ? static_cast<R*>(a.dsum) + begin : nullptr;
+  X* dx = a.dx ? static_cast<X*>(a.dx) + begin : nullptr;
+  const int jump = tpr * 8;  // from one vector of a thread to its next
+  Raw8<R> s1[NV], e1[NV], e[NV];
+  Raw8<X> y1[NV];
+  float2 st1 = make_float2(0.f, 0.f);
+  auto fetch = [&](bool live) {
+    if (live) st1 = *stat;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (live && in[j]) {
+        load_raw(sp + j * jump, s1[j]);
+        load_raw(yp + j * jump, y1[j]);
+        if (AHEAD && ep) load_raw(ep + j * jump, e1[j]);
+      } else {
+        zero_raw(s1[j]);
+        zero_raw(y1[j]);
+      }
+    }
+    stat += stride;
+    sp += step;
+    yp += step;
+    if (AHEAD && ep) ep += step;
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) zero_raw(e1[j]);
+  int parity = 0;
+  if (AHEAD) fetch(first < rows);
+  // groups that share a warp go through the same number of rows (its shuffles need all lanes)
+  const int lead = tpr < 32 ? first / (32 / tpr) * (32 / tpr) : first;  // of the warp's groups
+  int64_t next = first;
+  for (int64_t at = lead; at < rows; at += stride) {
+    const bool live = next < rows;
+    next += stride;
+    if (!AHEAD) fetch(live);
+    uint64_t s[NV][4], y[NV][4];
+    const float2 st = st1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      widen2(s1[j], s[j]);
+      widen2(y1[j], y[j]);
+      e[j] = e1[j];
+    }
+    if (AHEAD) fetch(next < rows);
+    const uint64_t mean2 = f2_splat(st.x), r2 = f2_splat(st.y);
+    uint64_t sa = 0, at2 = 0;  // two zeros each
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint64_t g[4] = {0, 0, 0, 0};
+      if (!KEEP && in[j]) load_params2(a.gamma + (t + j * tpr) * 8, g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[j][i] = f2_mul(f2_sub(s[j][i], mean2), r2);  // t
+        const uint64_t w = f2_mul(y[j][i], KEEP ? gk[KEEP ? j : 0][i] : g[i]);
+        sa = f2_add(sa, w);
+        at2 = f2_fma(w, s[j][i], at2);
+      }
+    }
+    float v0, v1, hi;
+    f2_unpack(sa, v0, hi);
+    v0 += hi;
+    f2_unpack(at2, v1, hi);
+    v1 += hi;
+    row_sums(v0, v1, tpr, group, parity, red);
+    parity ^= 1;
+    const uint64_t k0 = f2_splat(-(v0 * a.inv_d)), k1 = f2_splat(-(v1 * a.inv_d));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (live && in[j]) {
+        uint64_t g[4], o[4];
+        if constexpr (!KEEP) load_params2(a.gamma + (t + j * tpr) * 8, g);
+        if (!AHEAD && ep_late) load_raw(ep_late + j * jump, e[j]);
+        widen2(e[j], o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dg[j][i] = f2_fma(y[j][i], s[j][i], dg[j][i]);
+          db[j][i] = f2_add(y[j][i], db[j][i]);
+          const uint64_t d = f2_fma(s[j][i], k1, f2_fma(y[j][i], KEEP ? gk[KEEP ? j : 0][i] : g[i], k0));
+          o[i] = f2_fma(d, r2, o[i]);
+        }
+        float of[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(o[i], of[2 * i], of[2 * i + 1]);
+        if (dsum) store8(dsum + j * jump, of);
+        if (dx) store8(dx + j * jump, of);
+      }
+    }
+    if (dsum) dsum += step;
+    if (dx) dx += step;
+    if (!AHEAD && ep_late) ep_late += step;
+  }
+  const int pitch = a.D + 4;  // columns of 8 rows in a row lie in different banks
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    float* out = (which ? a.part_beta : a.part_gamma);
+    if (!out) break;  // no dbeta
+    out += (size_t)blockIdx.x * a.part_stride;
+    float f[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f2_unpack(which ? db[j][i] : dg[j][i], f[j][2 * i], f[j][2 * i + 1]);
+    if (groups == 1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = t + j * tpr;
+        if (c < nvec) store8(out + c * 8, f[j]);
+      }
+      continue;
+    }
+    if (which) __syncthreads();  // dgamma's sums have been read
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = t + j * tpr;
+      if (c < nvec) store8(part + group * pitch + c * 8, f[j]);
+    }
+    __syncthreads();
+    if (groups > 32) {  // short rows: a warp a column (in turn, 768 rows would be a long chain of additions)
+      for (int c = threadIdx.x >> 5; c < a.D; c += THREADS / 32) {
+        float v = 0.f;
+        for (int g = threadIdx.x & 31; g < groups; g += 32) v += part[g * pitch + c];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if ((threadIdx.x & 31) == 0) out[c] = v;
+      }
+    } else {
+      for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+        float v = 0.f;
+        for (int g = 0; g < groups; ++g) v += part[g * pitch + c];
+        out[c] = v;
+      }
+    }
+  }
+}
+
+// ---- element-wise forms: any width and element-aligned buffers
+// Rows of up to T NE values, one block a row: T threads with NE each in registers, all loads at once.
+template <class X, class R, int T, int NE>
+__global__ void __launch_bounds__(T) ln_forward_values_kernel(const LnArgs a) {
+  __shared__ float red[64];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const size_t base = (size_t)blockIdx.x * a.D + threadIdx.x;
+  const X* x = static_cast<const X*>(a.x) + base;
+  const R* res = a.res ? static_cast<const R*>(a.res) + base : nullptr;
+  float s[NE], v[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < NE; ++j) s[j] = (int)threadIdx.x + j * T < a.D ? value(x[j * T]) : 0.f;
+  if (res) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+      if ((int)threadIdx.x + j * T < a.D) s[j] += value(res[j * T]);
+  }
+  const int64_t later = blockIdx.x + a.ahead;  // as in ln_forward_kernel
+  if (later < a.rows) {
+    lines_to_l2(static_cast<const X*>(a.x) + (size_t)later * a.D, a.D * (int)sizeof(X), threadIdx.x, T);
+    if (a.res) lines_to_l2(static_cast<const R*>(a.res) + (size_t)later * a.D, a.D * (int)sizeof(R), threadIdx.x, T);
+  }
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    v[0] += s[j];
+    if ((int)threadIdx.x + j * T < a.D && a.res_out) assign(static_cast<R*>(a.res_out)[base + j * T], s[j]);
+  }
+  group_reduce<1>(v, T, false, red);
+  const float m0 = v[0] * a.inv_d;
+  v[0] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    if ((int)threadIdx.x + j * T < a.D) {
+      s[j] -= m0;
+      v[0] += s[j];
+      v[1] = fmaf(s[j], s[j], v[1]);
+    }
+  }
+  group_reduce<2>(v, T, false, red);
+  float shift, mean, r;
+  finish_stats(m0, v[0], v[1], a, shift, mean, r);
+  if (a.stats && threadIdx.x == 0) a.stats[blockIdx.x] = make_float2(mean, r);
+  v[0] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    const int c = threadIdx.x + j * T;
+    if (c < a.D) {
+      s[j] = fmaf((s[j] - shift) * r, a.gamma[c], a.beta ? a.beta[c] : 0.f);
+      v[0] = max_nan(v[0], fabsf(s[j]));
+    }
+  }
+  float to8 = 1.0f;
+  if (a.y_type == TFL_E4M3) {
+    group_reduce<1>(v, T, true, red);
+    const float amax = max_nan(v[0], kMinAmax);
+    if (threadIdx.x == 0) a.y_scale[blockIdx.x] = amax / kE4m3Max;
+    to8 = kE4m3Max / amax;
+  }
+#pragma unroll
+  for (int j = 0; j < NE; ++j)
+    if ((int)threadIdx.x + j * T < a.D) store1(a.y, a.y_type, base + j * T, s[j] * to8);
+}
+
+// Groups of G threads take rows of up to G NE values, all groups of a block together T threads.  The
+// next row is on its way while one is worked on, without its residual gradient where registers are
+// short (NE > 4), and gamma then comes from L1.
+template <class X, class R, int T, int G, int NE>
+__global__ void __launch_bounds__(T, 1024 / T) ln_backward_values_kernel(const LnGradArgs a) {
+  constexpr bool ROOM = NE <= 4;
+  constexpr int GROUPS = T / G;
+  __shared__ float2 red[2][32];
+  __shared__ float part[GROUPS > 1 ? T * NE : 1];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const int t = threadIdx.x % G, group = threadIdx.x / G, D = a.D;
+  const int64_t stride = (int64_t)gridDim.x * GROUPS;
+  float dg[NE], db[NE], gk[ROOM ? NE : 1];
+#pragma unroll
+  for (int j = 0; j < NE; ++j) {
+    dg[j] = db[j] = 0.f;
+    if (ROOM || j == 0) gk[ROOM ? j : 0] = t + j * G < D ? a.gamma[t + j * G] : 0.f;
+  }
+  auto gamma = [&](int j) { return ROOM ? gk[ROOM ? j : 0] : a.gamma[t + j * G]; };
+  R s1[NE], e1[NE];
+  X y1[NE];
+  float2 st1 = make_float2(0.f, 0.f);
+  auto fetch_res = [&](int64_t row) {
+    const R* p = static_cast<const R*>(a.dres) + (size_t)row * D + t;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) e1[j] = a.dres && row < a.rows && t + j * G < D ? p[j * G] : R(0.f);
+  };
+  auto fetch = [&](int64_t row) {
+    const R* p = static_cast<const R*>(a.sum) + (size_t)row * D + t;
+    const X* q = static_cast<const X*>(a.dy) + (size_t)row * D + t;
+    if (row < a.rows) st1 = a.stats[row];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const bool in = row < a.rows && t + j * G < D;
+      s1[j] = in ? p[j * G] : R(0.f);
+      y1[j] = in ? q[j * G] : X(0.f);
+    }
+    if (ROOM) fetch_res(row);
+  };
+  int parity = 0;
+  int64_t row = (int64_t)blockIdx.x * GROUPS + group;
+  fetch(row);
+  for (; row < a.rows; row += stride) {
+    float s[NE], y[NE], e[NE];
+    const float2 st = st1;
+    if (!ROOM) fetch_res(row);
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      s[j] = (value(s1[j]) - st.x) * st.y;  // t
+      y[j] = value(y1[j]);
+      if (ROOM) e[j] = value(e1[j]);
+    }
+    fetch(row + stride);
+    float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      if (t + j * G < D) {
+        const float w = y[j] * gamma(j);
+        v0 += w;
+        v1 = fmaf(w, s[j], v1);
+      }
+    }
+    row_sums<32>(v0, v1, G, group, parity, red);
+    parity ^= 1;
+    const float k0 = -(v0 * a.inv_d), k1 = -(v1 * a.inv_d);
+    const size_t base = (size_t)row * D + t;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      if (t + j * G < D) {
+        if (!ROOM) e[j] = value(e1[j]);
+        dg[j] = fmaf(y[j], s[j], dg[j]);
+        db[j] += y[j];
+        const float o = fmaf(fmaf(s[j], k1, fmaf(y[j], gamma(j), k0)), st.y, e[j]);
+        if (a.dsum) assign(static_cast<R*>(a.dsum)[base + j * G], o);
+        if (a.dx) assign(static_cast<X*>(a.dx)[base + j * G], o);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    float* out = (which ? a.part_beta : a.part_gamma);
+    if (!out) break;
+    out += (size_t)blockIdx.x * a.part_stride;
+    if constexpr (GROUPS == 1) {
+#pragma unroll
+      for (int j = 0; j < NE; ++j)
+        if (t + j * G < D) out[t + j * G] = which ? db[j] : dg[j];
+    } else {
+      if (which) __syncthreads();  // dgamma's sums have been read
+#pragma unroll
+      for (int j = 0; j < NE; ++j) part[(group * NE + j) * G + t] = which ? db[j] : dg[j];
+      __syncthreads();
+      for (int c = threadIdx.x; c < D; c += T) {
+        float v = 0.f;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) v += part[g * NE * G + c];
+        out[c] = v;
+      }
+    }
+  }
+}
+
+// Wider rows: three passes, the later ones from L1 / L2.
+__global__ void __launch_bounds__(256) ln_forward_any_kernel(const LnArgs a) {
+  __shared__ float red[64];
+  grid_launch_dependents();
+  grid_wait_prior();
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const size_t base = (size_t)row * a.D;
+    auto sum = [&](int c) {
+      const float s = load1(a.x, a.x_type, base + c);
+      return a.res ? s + load1(a.res, a.res_type, base + c) : s;
+    };
+    auto norm = [&](float t, int c) { return fmaf(t, a.gamma[c], a.beta ? a.beta[c] : 0.f); };
+    float v[2] = {0.f, 0.f};
+    for (int c = threadIdx.x; c < a.D; c += 256) v[0] += sum(c);
+    group_reduce<1>(v, 256, false, red);
+    const float m0 = v[0] * a.inv_d;
+    v[0] = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += 256) {
+      const float d = sum(c) - m0;
+      v[0] += d;
+      v[1] = fmaf(d, d, v[1]);
+    }
+    group_reduce<2>(v, 256, false, red);
+    float shift, mean, r;
+    finish_stats(m0, v[0], v[1], a, shift, mean, r);
+    if (a.stats && threadIdx.x == 0) a.stats[row] = make_float2(mean, r);
+    float to8 = 1.0f;
+    if (a.y_type == TFL_E4M3) {
+      v[0] = 0.f;
+      for (int c = threadIdx.x; c < a.D; c += 256)
+        v[0] = max_nan(v[0], fabsf(norm((sum(c) - m0 - shift) * r, c)));
+      group_reduce<1>(v, 256, true, red);
+      const float amax = max_nan(v[0], kMinAmax);
+      if (threadIdx.x == 0) a.y_scale[row] = amax / kE4m3Max;
+      to8 = kE4m3Max / amax;
+    }
+    for (int c = threadIdx.x; c < a.D; c += 256) {
+      const float s = sum(c);
+      if (a.res_out) store1(a.res_out, a.res_type, base + c, s);
+      store1(a.y, a.y_type, base + c, norm((s - m0 - shift) * r, c) * to8);
+    }
+  }
+}
+
+// The thread that owns column c in every row of the block also adds up its dgamma and dbeta, in the
+// block's row of partial sums.
+__global__ void __launch_bounds__(256) ln_backward_any_kernel(const LnGradArgs a) {
+  __shared__ float red[64];
+  grid_launch_dependents();
+  grid_wait_prior();
+  float* pg = a.part_gamma + (size_t)blockIdx.x * a.part_stride;
+  float* pb = a.part_beta ? a.part_beta + (size_t)blockIdx.x * a.part_stride : nullptr;
+  for (int c = threadIdx.x; c < a.D; c += 256) {
+    pg[c] = 0.f;
+    if (pb) pb[c] = 0.f;
+  }
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const size_t base = (size_t)row * a.D;
+    const float2 st = a.stats[row];
+    float v[2] = {0.f, 0.f};
+    for (int c = threadIdx.x; c < a.D; c += 256) {
+      const float w = load1(a.dy, a.x_type, base + c) * a.gamma[c];
+      v[0] += w;
+      v[1] = fmaf(w, (load1(a.sum, a.res_type, base + c) - st.x) * st.y, v[1]);
+    }
+    group_reduce<2>(v, 256, false, red);
+    const float k0 = -(v[0] * a.inv_d), k1 = -(v[1] * a.inv_d);
+    for (int c = threadIdx.x; c < a.D; c += 256) {
+      const float t = (load1(a.sum, a.res_type, base + c) - st.x) * st.y, dy = load1(a.dy, a.x_type, base + c);
+      const float d = fmaf(t, k1, fmaf(dy, a.gamma[c], k0));
+      const float o = fmaf(d, st.y, a.dres ? load1(a.dres, a.res_type, base + c) : 0.f);
+      pg[c] = fmaf(dy, t, pg[c]);
+      if (pb) pb[c] += dy;
+      if (a.dsum) store1(a.dsum, a.res_type, base + c, o);
+      if (a.dx) store1(a.dx, a.x_type, base + c, o);
+    }
+  }
+}
+
+template <class X, class R, class Y>
+cudaError_t forward(LnArgs a, int num_sms, cudaStream_t s) {
+  const int nvec = a.D / 8;
+  const int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4;
+  a.tpr = pow2_at_least((nvec + nv - 1) / nv);
+  const int threads = a.tpr > 256 ? a.tpr : 256;
+  const int64_t per = threads / a.tpr;
+  const unsigned grid = (unsigned)((a.rows + per - 1) / per);
+  a.ahead = per * num_sms * (1024 / threads);  // 64 registers a thread: 1024 threads an SM
+  if (nv == 1) return launch_dependent(ln_forward_kernel<X, R, Y, 1>, grid, threads, 0, s, a);
+  if (nv == 2) return launch_dependent(ln_forward_kernel<X, R, Y, 2>, grid, threads, 0, s, a);
+  return launch_dependent(ln_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
+}
+
+// Blocks of a backward over groups of rows: what the GPU holds at once, and one alone for so few that
+// a second launch would cost more than their turns; a lone block writes dgamma and dbeta itself, where
+// they take the 16-byte stores of the partial rows.
+int backward_blocks(LnGradArgs& a, int64_t groups_of_rows, int at_once) {
+  int64_t n = at_once < a.blocks ? at_once : a.blocks;
+  if (groups_of_rows < n) n = groups_of_rows <= 3 ? 1 : groups_of_rows;
+  const bool lone = n == 1 && aligned(a.dgamma, 16) && aligned(a.dbeta, 16);
+  a.part_stride = 2 * (size_t)a.D;
+  a.part_gamma = lone ? a.dgamma : a.partial;
+  a.part_beta = !a.dbeta ? nullptr : lone ? a.dbeta : a.partial + a.D;
+  return (int)n;
+}
+
+cudaError_t add_partials(const LnGradArgs& a, int n, cudaStream_t s) {
+  if (a.part_gamma == a.dgamma) return cudaSuccess;
+  return launch_column_sums(a.partial, n, 2 * a.D, a.dbeta ? 2 * a.D : a.D, a.D, a.dgamma, a.dbeta, s);
+}
+
+template <class X, class R, int NV, int THREADS, int BLOCKS>
+cudaError_t backward_with(LnGradArgs a, int num_sms, cudaStream_t s) {
+  a.tpr = pow2_at_least((a.D / 8 + NV - 1) / NV);
+  const int groups = THREADS / a.tpr;
+  const int grid = backward_blocks(a, (a.rows + groups - 1) / groups, num_sms * BLOCKS);
+  const size_t smem = groups > 1 ? (size_t)groups * (a.D + 4) * sizeof(float) : 0;  // at most 36 KB
+  const cudaError_t e = launch_dependent(ln_backward_kernel<X, R, NV, THREADS, BLOCKS>, grid, THREADS, smem, s, a);
+  return e == cudaSuccess ? add_partials(a, grid, s) : e;
+}
+
+template <class X, class R, int T, int G, int NE>
+cudaError_t backward_values(LnGradArgs a, int num_sms, cudaStream_t s) {
+  const int grid = backward_blocks(a, (a.rows + T / G - 1) / (T / G), num_sms * (1024 / T));
+  const cudaError_t e = launch_dependent(ln_backward_values_kernel<X, R, T, G, NE>, grid, T, 0, s, a);
+  return e == cudaSuccess ? add_partials(a, grid, s) : e;
+}
+
+template <class X, class R>
+cudaError_t backward(const LnGradArgs& a, int num_sms, cudaStream_t s) {
+  constexpr int WIDE = sizeof(R) == 4;  // fp32 rows take more registers, and carry more bytes a thread
+  // one wide block an SM where the rows give each of them work (fewer partial rows to add), narrower
+  // ones to spread fewer rows over all SMs
+  if (a.D <= 2048 && a.rows * pow2_at_least(a.D / 8) >= (int64_t)num_sms * 512)
+    return backward_with<X, R, 1, 512, 1>(a, num_sms, s);
+  if (a.D <= 2048) return backward_with<X, R, 1, 256, 2>(a, num_sms, s);
+  if (a.D <= 4096) return WIDE ? backward_with<X, R, 1, 512, 1>(a, num_sms, s) : backward_with<X, R, 2, 256, 2>(a, num_sms, s);
+  if (a.D <= 8192) return backward_with<X, R, 2, 512, 1>(a, num_sms, s);
+  return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
+}
+
+constexpr int kLnMaxValues = 8192;        // widest row the element-wise kernels hold in registers
+constexpr int kLnMaxRegisterRow = 32768;  // widest the vector kernels do (the backward: half)
+
+}  // namespace
+
+cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s) {
+  const bool vec = a.D % 8 == 0 && a.D <= kLnMaxRegisterRow && aligned(a.x, 16) && aligned(a.res, 16) &&
+                   aligned(a.gamma, 16) && aligned(a.beta, 16) && aligned(a.res_out, 16) &&
+                   aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
+  if (!vec && a.D <= kLnMaxValues) {
+    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+      using X = decltype(x);
+      using R = decltype(r);
+      const unsigned n = (unsigned)a.rows;
+      LnArgs b = a;
+      b.ahead = a.D <= 4096 ? (int64_t)num_sms * 8 : a.rows;  // none for the widest
+      if (a.D <= 1024) return launch_dependent(ln_forward_values_kernel<X, R, 256, 4>, n, 256, 0, s, b);
+      if (a.D <= 4096) return launch_dependent(ln_forward_values_kernel<X, R, 256, 16>, n, 256, 0, s, b);
+      return launch_dependent(ln_forward_values_kernel<X, R, 1024, 8>, n, 1024, 0, s, b);
+    });
+  }
+  if (!vec) {
+    const int64_t most = (int64_t)num_sms * 8;
+    return launch_dependent(ln_forward_any_kernel, (unsigned)(a.rows < most ? a.rows : most), 256, 0, s, a);
+  }
+  return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+    using X = decltype(x);
+    using R = decltype(r);
+    if (a.y_type == TFL_E4M3) return forward<X, R, E4m3>(a, num_sms, s);
+    if constexpr (sizeof(X) == 4) {
+      if (a.y_type == TFL_F16) return forward<X, R, __half>(a, num_sms, s);
+      if (a.y_type == TFL_BF16) return forward<X, R, __nv_bfloat16>(a, num_sms, s);
+    }
+    return forward<X, R, X>(a, num_sms, s);
+  });
+}
+
+cudaError_t launch_ln_backward(const LnGradArgs& args, int num_sms, cudaStream_t s) {
+  LnGradArgs a = args;
+  const bool vec = a.D % 8 == 0 && a.D <= kLnMaxRegisterRow / 2 && aligned(a.sum, 16) && aligned(a.gamma, 16) &&
+                   aligned(a.dy, 16) && aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
+  if (!vec) {
+    if (a.D > kLnMaxValues) {
+      const int grid = backward_blocks(a, a.rows, num_sms * 4);
+      const cudaError_t e = launch_dependent(ln_backward_any_kernel, grid, 256, 0, s, a);
+      return e == cudaSuccess ? add_partials(a, grid, s) : e;
+    }
+    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+      using X = decltype(x);
+      using R = decltype(r);
+      if (a.D <= 128) return backward_values<X, R, 256, 32, 4>(a, num_sms, s);
+      if (a.D <= 256) return backward_values<X, R, 256, 64, 4>(a, num_sms, s);
+      if (a.D <= 512) return backward_values<X, R, 256, 128, 4>(a, num_sms, s);
+      if (a.D <= 1024) return backward_values<X, R, 256, 256, 4>(a, num_sms, s);
+      if (a.D <= 2048) return backward_values<X, R, 512, 512, 4>(a, num_sms, s);
+      if (a.D <= 4096) return backward_values<X, R, 1024, 1024, 4>(a, num_sms, s);
+      if (a.D <= 6144) return backward_values<X, R, 1024, 1024, 6>(a, num_sms, s);
+      return backward_values<X, R, 1024, 1024, 8>(a, num_sms, s);
+    });
+  }
+  return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+    return backward<decltype(x), decltype(r)>(a, num_sms, s);
+  });
+}
+
+}  // namespace tfl

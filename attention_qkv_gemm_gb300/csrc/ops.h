@@ -1,6 +1,6 @@
 // ops.h -- argument blocks and host launchers of the operators that stand on their own beside
-// the forward and its attention: the root-mean-square norm (rmsnorm.cu) and the gated
-// feed-forward (glu.cu).
+// the forward and its attention: the root-mean-square norm (rmsnorm.cu), layer norm (layernorm.cu),
+// the gated feed-forward (glu.cu) and the linear layer (linear.cu).
 #pragma once
 #include "kernels.h"
 #include "tfl.h"
@@ -41,6 +41,47 @@ struct RmsGradArgs {
 constexpr int kRmsMaxRegisterRow = 32768;  // widest row the forward holds in registers (the backward: half)
 cudaError_t launch_rms_forward(const RmsArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_rms_backward(const RmsGradArgs& a, int num_sms, cudaStream_t s);
+
+// Layer norm (layernorm.cu).
+struct LnArgs {
+  int64_t rows = 0;
+  int D = 0;
+  int tpr = 0;                   // threads that hold one row (a power of two), set by the launcher
+  int64_t ahead = 0;             // rows between a row and the one prefetched beside it, likewise
+  float inv_d = 0.f, eps = 0.f;
+  int x_type = 0, res_type = 0, y_type = 0;
+  const void* x = nullptr;       // [rows, D]
+  const void* res = nullptr;     // [rows, D] or null
+  const float* gamma = nullptr;  // [D]
+  const float* beta = nullptr;   // [D] or null
+  void* res_out = nullptr;       // [rows, D] of res_type, or null
+  void* y = nullptr;             // [rows, D]
+  float* y_scale = nullptr;      // [rows], e4m3 only
+  float2* stats = nullptr;       // [rows] mean and 1 / sqrt(var + eps), or null
+};
+struct LnGradArgs {
+  int64_t rows = 0;
+  int D = 0;
+  int tpr = 0;
+  float inv_d = 0.f;
+  int x_type = 0, res_type = 0;
+  const void* sum = nullptr;      // [rows, D] of res_type
+  const float2* stats = nullptr;  // [rows]
+  const float* gamma = nullptr;   // [D]
+  const void* dy = nullptr;       // [rows, D] of x_type
+  const void* dres = nullptr;     // [rows, D] of res_type, or null
+  void* dx = nullptr;             // [rows, D] of x_type, or null
+  void* dsum = nullptr;           // [rows, D] of res_type, or null
+  float* dgamma = nullptr;        // [D]
+  float* dbeta = nullptr;         // [D] or null
+  float* partial = nullptr;       // [blocks, 2 D] partial sums of dgamma and dbeta
+  int blocks = 0;
+  // where a block's rows of partial sums go, set by the launcher
+  float *part_gamma = nullptr, *part_beta = nullptr;
+  size_t part_stride = 0;
+};
+cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_ln_backward(const LnGradArgs& a, int num_sms, cudaStream_t s);
 
 // Gated feed-forward (glu.cu).
 enum GluMode : int {

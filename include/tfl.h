@@ -437,6 +437,67 @@ int tfl_rmsnorm_backward(tfl_rmsnorm* n, int64_t rows, const void* sum, const fl
 void tfl_rmsnorm_destroy(tfl_rmsnorm* n);
 
 /*
+ * Layer norm with the residual's addition, the norm of the stack above on its own:
+ *   s = x + res,  m = mean(s),  r = 1 / sqrt(mean((s - m)^2) + eps),
+ *   t = (s - m) r,  y = t gamma + beta   (per row)
+ * s, the sums and y are fp32 inside; res_out is s and y is y, each rounded once
+ * to its type (y is taken from the unrounded s).  The variance is the centred
+ * values' own, so a large mean costs only what fp32 loses of s - m.
+ * var + eps has to lie within fp32's normal range (with eps 0 a constant row has
+ * no norm).  e4m3 output and types: as for the root-mean-square norm above.
+ */
+typedef struct tfl_layernorm tfl_layernorm;
+
+/* d_model in 1 .. 2^24, eps >= 0 and finite.  Where y is of x's type the handle also holds the
+ * backward's scratch (at most max(64 MiB, 8 d_model bytes)).
+ * Errors: INVALID_ARG, UNSUPPORTED (types, device), OOM, CUDA. */
+int tfl_layernorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int32_t y_type, float eps,
+                         tfl_layernorm** out);
+
+/*
+ * Asynchronous on `stream`.  Device pointers, rows of d_model values one after
+ * the other, 0 <= rows < 2^31 (0: nothing is done):
+ *   x        [rows, d_model]
+ *   res      [rows, d_model] of the residual's type, or NULL (s = x)
+ *   gamma    fp32 [d_model];  beta  fp32 [d_model], or NULL (0)
+ *   res_out  [rows, d_model] of the residual's type, or NULL (s is not stored);
+ *            may be res, or x when the types are the same
+ *   y        [rows, d_model]; may be x when the types are the same (and res_out is not x)
+ *   y_scale  fp32 [rows] for an e4m3 y, else NULL
+ *   stats    fp32 [rows, 2], 8-byte aligned: m and r of each row, which the
+ *            backward takes; or NULL (not stored)
+ * Other overlaps of an output are refused.  Any element-aligned buffers and
+ * widths; 16-byte aligned buffers (y: 8 bytes for e4m3) and a d_model that is a
+ * multiple of 8 up to 32768 take the kernels that keep a row in registers.
+ * Calls on one handle may overlap.
+ * Errors: INVALID_ARG (also when the current device is not the handle's), CUDA.
+ */
+int tfl_layernorm_forward(tfl_layernorm* n, int64_t rows, const void* x, const void* res, const float* gamma,
+                          const float* beta, void* res_out, void* y, float* y_scale, float* stats, tfl_stream stream);
+
+/*
+ * The gradients, with a = dy gamma and t = (s - m) r from the forward's m and r:
+ *   ds = dres + r (a - mean(a) - t mean(a t)),   dgamma = sum over rows of dy t,   dbeta = sum over rows of dy
+ *   sum     [rows, d_model] of the residual's type: the forward's res_out (x if it had no residual)
+ *   stats   fp32 [rows, 2], 8-byte aligned: as the forward stored them
+ *   dy      [rows, d_model] of y's type (which must be x's type)
+ *   dres    [rows, d_model] of the residual's type: the gradient that reaches s past the norm, or NULL
+ *   dx      ds in x's type, or NULL;  dsum  ds in the residual's type, or NULL
+ *           (s = x + res, so ds is the gradient of both; at least one is given)
+ *   dgamma  fp32 [d_model], written in full (zeros for rows = 0);  dbeta  the same, or NULL
+ * dx or dsum may be dy, dres or sum where the types are the same; other overlaps
+ * are refused.  No atomics: the same inputs give the same bits.  Calls on one
+ * handle share its scratch and must not overlap on the GPU (graphs that hold such
+ * calls included).  Errors: INVALID_ARG, UNSUPPORTED (y is not of x's type), CUDA.
+ */
+int tfl_layernorm_backward(tfl_layernorm* n, int64_t rows, const void* sum, const float* stats, const float* gamma,
+                           const void* dy, const void* dres, void* dx, void* dsum, float* dgamma, float* dbeta,
+                           tfl_stream stream);
+
+/* Free what the handle owns.  Synchronizes the device.  NULL is a no-op. */
+void tfl_layernorm_destroy(tfl_layernorm* n);
+
+/*
  * Gated feed-forward block: both projections, the activation and the product
  *   h = act(x Wg^T) * (x Wu^T)
  * with Wg, Wu in nn.Linear layout [d_ff, d_model] (one packed [2 d_ff, d_model]
