@@ -28,7 +28,7 @@ TFL_ERR_BAD_LENGTHS = -6
 
 # element types of the operators that stand on their own
 TFL_F32, TFL_F16, TFL_BF16, TFL_E4M3 = 0, 1, 2, 3
-TFL_ACT_SILU, TFL_ACT_GELU = 0, 1
+TFL_ACT_SILU, TFL_ACT_GELU, TFL_ACT_NONE = 0, 1, 2
 TFL_GLU_FORM_FEW, TFL_GLU_FORM_LONE, TFL_GLU_FORM_SHARED, TFL_GLU_FORM_PAIR, TFL_GLU_FORM_WIDE = range(5)
 
 KIND_NAMES = {1: "rownorm", 2: "gemm_qkv", 3: "attention", 4: "gemm_oproj", 5: "gemm_ffn1", 6: "gemm_ffn2",
@@ -41,7 +41,9 @@ EXPORTS = ("tfl_default_options", "tfl_workspace_bytes", "tfl_create", "tfl_forw
            "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu", "tfl_selftest_glu_plan",
            "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy",
            "tfl_layernorm_create", "tfl_layernorm_forward", "tfl_layernorm_backward", "tfl_layernorm_destroy",
-           "tfl_glu_create", "tfl_glu_forward", "tfl_glu_backward", "tfl_glu_status", "tfl_glu_destroy")
+           "tfl_glu_create", "tfl_glu_forward", "tfl_glu_backward", "tfl_glu_status", "tfl_glu_destroy",
+           "tfl_linear_create", "tfl_linear_forward", "tfl_linear_backward", "tfl_linear_status", "tfl_linear_destroy",
+           "tfl_selftest_linear_plan")
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -161,6 +163,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.tfl_glu_status.restype = ctypes.c_int
     lib.tfl_glu_destroy.argtypes = [vp]
     lib.tfl_glu_destroy.restype = None
+    lib.tfl_linear_create.argtypes = [i32, i32, i32, i32, i32, i32, i64, ctypes.POINTER(vp)]
+    lib.tfl_linear_create.restype = ctypes.c_int
+    lib.tfl_linear_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_linear_forward.restype = ctypes.c_int
+    lib.tfl_linear_backward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.tfl_linear_backward.restype = ctypes.c_int
+    lib.tfl_linear_status.argtypes = [vp, vp]
+    lib.tfl_linear_status.restype = ctypes.c_int
+    lib.tfl_linear_destroy.argtypes = [vp]
+    lib.tfl_linear_destroy.restype = None
+    lib.tfl_selftest_linear_plan.argtypes = [i32, i32, i32, i32, i64, ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    lib.tfl_selftest_linear_plan.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -336,6 +350,36 @@ def tfl_glu_destroy(handle: int) -> None:
         load().tfl_glu_destroy(handle)
 
 
+def tfl_linear_create(d_in: int, d_out: int, in_type: int, out_type: int, act: int = TFL_ACT_NONE,
+                      dy_type: int = TFL_F32, max_grad_tokens: int = 0) -> int:
+    """A linear layer; types are ``TFL_F16`` and so on, act ``TFL_ACT_NONE``, ``TFL_ACT_SILU`` or ``TFL_ACT_GELU``."""
+    h = ctypes.c_void_p()
+    _check(load().tfl_linear_create(int(d_in), int(d_out), int(in_type), int(out_type), int(act), int(dy_type),
+                                    int(max_grad_tokens), ctypes.byref(h)))
+    return h.value
+
+
+def tfl_linear_forward(handle: int, tokens: int, x: int, x_scale: Optional[int], w: int, w_scale: Optional[int],
+                       bias: Optional[int], res: Optional[int], z: Optional[int], y: int, stream: int = 0) -> None:
+    """z = x W^T + bias; y = act(z) + res (device pointers; scales for e4m3 operands only)."""
+    _check(load().tfl_linear_forward(handle, tokens, x, x_scale, w, w_scale, bias, res, z, y, stream))
+
+
+def tfl_linear_backward(handle: int, tokens: int, x: Optional[int], w: Optional[int], z: Optional[int], dy: int,
+                        dx: Optional[int], dw: Optional[int], db: Optional[int], stream: int = 0) -> None:
+    """dx, dw and db (each may be None) from the forward's inputs, its z and dy."""
+    _check(load().tfl_linear_backward(handle, tokens, x, w, z, dy, dx, dw, db, stream))
+
+
+def tfl_linear_status(handle: int, stream: int = 0) -> int:
+    return load().tfl_linear_status(handle, stream)
+
+
+def tfl_linear_destroy(handle: int) -> None:
+    if handle:
+        load().tfl_linear_destroy(handle)
+
+
 def tfl_status(handle: int, stream: int = 0) -> int:
     return load().tfl_status(handle, stream)
 
@@ -372,6 +416,14 @@ def tfl_selftest_glu_plan(d_model: int, d_ff: int, in_type: int, part: int, toke
     out = (ctypes.c_int32 * 4)()
     u = None if units is None else (ctypes.c_int32 * 5)(*units)
     _check(load().tfl_selftest_glu_plan(int(d_model), int(d_ff), int(in_type), int(part), int(tokens), u, out))
+    return tuple(out)
+
+
+def tfl_selftest_linear_plan(d_in: int, d_out: int, in_type: int, part: int, tokens: int, units=None):
+    """The same of a launch of the linear layer; part 0 is the forward, 1 and 2 the backward's dx and dw."""
+    out = (ctypes.c_int32 * 4)()
+    u = None if units is None else (ctypes.c_int32 * 5)(*units)
+    _check(load().tfl_selftest_linear_plan(int(d_in), int(d_out), int(in_type), int(part), int(tokens), u, out))
     return tuple(out)
 
 

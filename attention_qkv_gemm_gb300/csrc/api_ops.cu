@@ -390,7 +390,7 @@ struct tfl_glu {
   int D = 0, F = 0, in_type = 0, out_type = 0, act = 0;
   int64_t max_grad_tokens = 0;
   int device = 0;
-  GluUnits units;
+  TileUnits units;
   int* status = nullptr;                          // status word (256 bytes), then dg and du
   uint16_t *dg = nullptr, *du = nullptr;          // [max_grad_tokens, F] in rows of `pitch`
   int pitch = 0;                                  // F to the next 128 bytes: a copied box row is then one line
@@ -412,28 +412,29 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int 
 }
 
 // Kernel attributes and what runs at once on a device: the same for every handle, asked once.
-int glu_units(int dev, int sms, GluUnits* u) {
+int tile_units(int dev, int sms, TileUnits* u) {
   constexpr int kDevices = 64;
   static std::mutex lock;
-  static GluUnits known[kDevices];
+  static TileUnits known[kDevices];
   std::lock_guard<std::mutex> hold(lock);
   if (dev < kDevices && known[dev].sms) {
     *u = known[dev];
     return TFL_OK;
   }
-  TFL_CUDA(prepare_glu_kernels(u), "feed-forward kernel attributes");
+  TFL_CUDA(prepare_tile_kernels(u), "feed-forward kernel attributes");
+  TFL_CUDA(prepare_linear_kernels(), "linear layer kernel attributes");
   u->sms = sms;
   if (dev < kDevices) known[dev] = *u;
   return TFL_OK;
 }
 
 // How the forward and the three launches of the backward are cut.
-GluPlan glu_call_plan(int D, int F, bool f8, int mode, int64_t tokens, const GluUnits& u) {
+TilePlan glu_call_plan(int D, int F, bool f8, int mode, int64_t tokens, const TileUnits& u) {
   const int ke = f8 ? 128 : 64;
   const bool lines = D * (f8 ? 1 : 2) % 128 == 0;
-  if (mode == GLU_DX) return glu_plan(mode, lines, tokens, D, 2 * ((F + ke - 1) / ke), u);
-  if (mode == GLU_DW) return glu_plan(mode, lines, F, D, (tokens + ke - 1) / ke, u);
-  return glu_plan(mode, lines, tokens, F, (D + ke - 1) / ke, u);
+  if (mode == GRAD_DX) return tile_plan(mode, lines, tokens, D, 2 * ((F + ke - 1) / ke), u);
+  if (mode == GRAD_DW) return tile_plan(mode, lines, F, D, (tokens + ke - 1) / ke, u);
+  return tile_plan(mode, lines, tokens, F, (D + ke - 1) / ke, u);
 }
 
 constexpr int kMnBox = 64;  // MN-major operands come in boxes of 64 k rows
@@ -445,8 +446,38 @@ int check_tokens(const tfl_glu* g, int64_t tokens) {
   return TFL_OK;
 }
 
-GluArgs glu_args(const tfl_glu* g) {
-  GluArgs a;
+// What a plan self-test is asked about: the given units, or the current device's.
+int selftest_units(const int32_t* units, TileUnits* u) {
+  if (units) {
+    u->sms = units[0];
+    u->pairs = units[1];
+    for (int i = 0; i < 3; ++i) u->splits[i] = units[2 + i];
+    if (u->sms < 1 || u->pairs < 1) return fail(TFL_ERR_INVALID_ARG, "a device runs lone CTAs and pairs");
+    return TFL_OK;
+  }
+  int dev = 0, sms = 0;
+  if (int rc = usable_device(&dev, &sms)) return rc;
+  return tile_units(dev, sms, u);
+}
+
+void tell_plan(const TilePlan& p, int mode, int32_t* out) {
+  out[0] = tile_form(p, mode);
+  out[1] = p.bno;
+  out[2] = (int32_t)(p.tiles > INT32_MAX ? INT32_MAX : p.tiles);
+  out[3] = p.units;
+}
+
+int read_status(int* status, cudaStream_t stream) {
+  TFL_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+  int v = 0;
+  TFL_CUDA(cudaMemcpy(&v, status, sizeof(int), cudaMemcpyDeviceToHost), "status read");
+  if (v) TFL_CUDA(cudaMemset(status, 0, sizeof(int)), "status clear");
+  if (v & TFL_DEV_TIMEOUT) return fail(TFL_ERR_DEVICE_TIMEOUT, "a device-side wait ran out of time");
+  return TFL_OK;
+}
+
+TileArgs glu_args(const tfl_glu* g) {
+  TileArgs a;
   a.act = g->act;
   a.bf16_operands = g->in_type == TFL_BF16;
   a.bf16_out = g->out_type == TFL_BF16;
@@ -477,8 +508,8 @@ int tfl_glu_create(int32_t d_model, int32_t d_ff, int32_t in_type, int32_t out_t
   int dev = 0, sms = 0;
   if (int rc = usable_device(&dev, &sms)) return rc;
   if (!get_encode()) return fail(TFL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  GluUnits units;
-  if (int rc = glu_units(dev, sms, &units)) return rc;
+  TileUnits units;
+  if (int rc = tile_units(dev, sms, &units)) return rc;
   if (units.pairs < 1) return fail(TFL_ERR_UNSUPPORTED, "the device runs no CTA pairs");
   tfl_glu* g = new (std::nothrow) tfl_glu();
   if (!g) return fail(TFL_ERR_OOM, "handle allocation failed");
@@ -545,13 +576,13 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
     TFL_CUDA(launch_glu_few(g->in_type, a, g->units.sms, static_cast<cudaStream_t>(stream)), "feed-forward");
     return TFL_OK;
   }
-  const GluPlan p = glu_call_plan(g->D, g->F, f8, GLU_FORWARD, tokens, g->units);
-  GluMaps mp;
+  const TilePlan p = glu_call_plan(g->D, g->F, f8, GLU_FORWARD, tokens, g->units);
+  TileMaps mp;
   if (!make_map(&mp.a0, x, tokens, g->D, (int)es, p.a_rows) || !make_map(&mp.b0, wg, g->F, g->D, (int)es, p.bno) ||
       !make_map(&mp.b1, wu, g->F, g->D, (int)es, p.bno))
     return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
   mp.a1 = mp.a0;
-  GluArgs a = glu_args(g);
+  TileArgs a = glu_args(g);
   a.M = (int)tokens;
   a.N = g->F;
   a.num_k = (g->D + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
@@ -560,7 +591,7 @@ int tfl_glu_forward(tfl_glu* g, int64_t tokens, const void* x, const float* x_sc
   a.u_scale = wu_scale;
   a.ldo = g->F;
   a.out = static_cast<uint16_t*>(h);
-  TFL_CUDA(launch_glu(p, GLU_FORWARD, f8, mp, a, static_cast<cudaStream_t>(stream)), "feed-forward");
+  TFL_CUDA(launch_tiles(p, GLU_FORWARD, f8, mp, a, static_cast<cudaStream_t>(stream)), "feed-forward");
   return TFL_OK;
 }
 
@@ -596,10 +627,10 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
 
   const int Di = g->D, Fi = g->F, Ti = (int)tokens;
   const int kd = (Di + 63) / 64, kf = (Fi + 63) / 64, kt = (Ti + 63) / 64;
-  const GluPlan p1 = glu_call_plan(Di, Fi, false, GLU_SLOPES, tokens, g->units);
-  const GluPlan p2 = glu_call_plan(Di, Fi, false, GLU_DX, tokens, g->units);
-  const GluPlan p3 = glu_call_plan(Di, Fi, false, GLU_DW, tokens, g->units);
-  GluMaps m1, m2, m3;
+  const TilePlan p1 = glu_call_plan(Di, Fi, false, GLU_SLOPES, tokens, g->units);
+  const TilePlan p2 = glu_call_plan(Di, Fi, false, GRAD_DX, tokens, g->units);
+  const TilePlan p3 = glu_call_plan(Di, Fi, false, GRAD_DW, tokens, g->units);
+  TileMaps m1, m2, m3;
   bool ok = make_map(&m1.a0, x, tokens, Di, 2, p1.a_rows) && make_map(&m1.b0, wg, Fi, Di, 2, p1.bno) &&
             make_map(&m1.b1, wu, Fi, Di, 2, p1.bno);
   m1.a1 = m1.a0;
@@ -612,7 +643,7 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   m3.b1 = m3.b0;
   if (!ok) return fail(TFL_ERR_CUDA, "feed-forward tensor map encoding failed");
 
-  GluArgs a = glu_args(g);
+  TileArgs a = glu_args(g);
   a.M = Ti;
   a.N = Fi;
   a.num_k = kd;
@@ -620,7 +651,7 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.ldo = g->pitch;
   a.out = g->dg;
   a.out2 = g->du;
-  TFL_CUDA(launch_glu(p1, GLU_SLOPES, false, m1, a, st), "feed-forward slopes");
+  TFL_CUDA(launch_tiles(p1, GLU_SLOPES, false, m1, a, st), "feed-forward slopes");
   a = glu_args(g);
   a.M = Ti;
   a.N = Di;
@@ -628,7 +659,7 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.num_k = 2 * kf;
   a.ldo = Di;
   a.out = static_cast<uint16_t*>(dx);
-  TFL_CUDA(launch_glu(p2, GLU_DX, false, m2, a, st), "feed-forward dx");
+  TFL_CUDA(launch_tiles(p2, GRAD_DX, false, m2, a, st), "feed-forward dx");
   a = glu_args(g);
   a.M = Fi;
   a.N = Di;
@@ -636,7 +667,7 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
   a.ldo = Di;
   a.out = static_cast<uint16_t*>(dwg);
   a.out2 = static_cast<uint16_t*>(dwu);
-  TFL_CUDA(launch_glu(p3, GLU_DW, false, m3, a, st), "feed-forward weight gradients");
+  TFL_CUDA(launch_tiles(p3, GRAD_DW, false, m3, a, st), "feed-forward weight gradients");
   return TFL_OK;
 }
 
@@ -645,45 +676,313 @@ int tfl_selftest_glu_plan(int32_t d_model, int32_t d_ff, int32_t in_type, int32_
   g_err.clear();
   const bool f8 = in_type == TFL_E4M3;
   if (!out || d_model < 1 || d_model > (1 << 24) || d_ff < 1 || d_ff > (1 << 24) || tokens < 1 ||
-      tokens > INT32_MAX - 512 || part < GLU_FORWARD || part > GLU_DW ||
+      tokens > INT32_MAX - 512 || part < GLU_FORWARD || part > GRAD_DW ||
       !(f8 ? part == GLU_FORWARD : type_16bit(in_type)))
     return fail(TFL_ERR_INVALID_ARG, "no such launch");
-  GluUnits u;
-  if (units) {
-    u.sms = units[0];
-    u.pairs = units[1];
-    for (int i = 0; i < 3; ++i) u.splits[i] = units[2 + i];
-    if (u.sms < 1 || u.pairs < 1) return fail(TFL_ERR_INVALID_ARG, "a device runs lone CTAs and pairs");
-  } else {
-    int dev = 0, sms = 0;
-    if (int rc = usable_device(&dev, &sms)) return rc;
-    if (int rc = glu_units(dev, sms, &u)) return rc;
-  }
+  TileUnits u;
+  if (int rc = selftest_units(units, &u)) return rc;
   for (int i = 0; i < 4; ++i) out[i] = 0;
   if (part == GLU_FORWARD && glu_few_fits(tokens, (int64_t)d_model * (f8 ? 1 : 2))) return TFL_OK;
-  const GluPlan p = glu_call_plan(d_model, d_ff, f8, part, tokens, u);
-  out[0] = glu_form(p, part);
-  out[1] = p.bno;
-  out[2] = (int32_t)(p.tiles > INT32_MAX ? INT32_MAX : p.tiles);
-  out[3] = p.units;
+  tell_plan(glu_call_plan(d_model, d_ff, f8, part, tokens, u), part, out);
   return TFL_OK;
 }
 
 int tfl_glu_status(tfl_glu* g, tfl_stream stream) {
   g_err.clear();
   if (!g) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
-  TFL_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(stream)), "cudaStreamSynchronize");
-  int v = 0;
-  TFL_CUDA(cudaMemcpy(&v, g->status, sizeof(int), cudaMemcpyDeviceToHost), "status read");
-  if (v) TFL_CUDA(cudaMemset(g->status, 0, sizeof(int)), "status clear");
-  if (v & TFL_DEV_TIMEOUT) return fail(TFL_ERR_DEVICE_TIMEOUT, "a device-side wait ran out of time");
-  return TFL_OK;
+  return read_status(g->status, static_cast<cudaStream_t>(stream));
 }
 
 void tfl_glu_destroy(tfl_glu* g) {
   if (!g) return;
   release(g->device, g->status);
   delete g;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Linear layer.
+struct tfl_linear {
+  int K = 0, N = 0, in_type = 0, out_type = 0, act = 0, dy_type = 0;
+  int64_t max_grad_tokens = 0;
+  int device = 0;
+  TileUnits units;
+  int* status = nullptr;       // status word (256 bytes), then partial sums of db, then dz
+  float* partial = nullptr;    // [blocks, N]
+  int blocks = 0;
+  uint16_t* dz = nullptr;      // [max_grad_tokens, N] in rows of `pitch`; null where dy serves
+  int pitch = 0;               // N to the next 128 bytes: a copied box row is then one line
+};
+
+namespace {
+
+enum LinPart : int { LIN_PART_FORWARD = 0, LIN_PART_DX = 1, LIN_PART_DW = 2 };
+
+TilePlan linear_call_plan(int K, int N, bool f8, int part, int64_t tokens, const TileUnits& u) {
+  const int ke = f8 ? 128 : 64;
+  const bool lines = K * (f8 ? 1 : 2) % 128 == 0;
+  if (part == LIN_PART_DX) return tile_plan(GRAD_DX, lines, tokens, K, (N + ke - 1) / ke, u);
+  if (part == LIN_PART_DW) return tile_plan(GRAD_DW, lines, N, K, (tokens + ke - 1) / ke, u, 1);
+  return tile_plan(LIN_FORWARD, lines, tokens, N, (K + ke - 1) / ke, u);
+}
+
+int check_tokens(const tfl_linear* l, int64_t tokens) {
+  if (tokens < 0 || tokens > INT32_MAX - 512) return fail(TFL_ERR_INVALID_ARG, "tokens must be in 0 .. 2^31 - 513");
+  if ((tokens + 127) / 128 * ((l->N + 31) / 32) > INT32_MAX || (tokens + 127) / 128 * ((l->K + 31) / 32) > INT32_MAX)
+    return fail(TFL_ERR_UNSUPPORTED, "too many tokens for this width");
+  return TFL_OK;
+}
+
+TileArgs linear_args(const tfl_linear* l) {
+  TileArgs a;
+  a.act = l->act;
+  a.bf16_operands = l->in_type == TFL_BF16;
+  a.bf16_out = l->out_type == TFL_BF16;
+  a.out_f32 = l->out_type == TFL_F32;
+  a.status = l->status;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tfl_linear_create(int32_t d_in, int32_t d_out, int32_t in_type, int32_t out_type, int32_t act, int32_t dy_type,
+                      int64_t max_grad_tokens, tfl_linear** out) {
+  g_err.clear();
+  if (!out) return fail(TFL_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (d_in < 1 || d_out < 1) return fail(TFL_ERR_INVALID_ARG, "d_in and d_out must be >= 1");
+  if (act != TFL_ACT_SILU && act != TFL_ACT_GELU && act != TFL_ACT_NONE)
+    return fail(TFL_ERR_INVALID_ARG, "no such activation");
+  if (max_grad_tokens < 0 || max_grad_tokens > INT32_MAX - 512)
+    return fail(TFL_ERR_INVALID_ARG, "max_grad_tokens must be in 0 .. 2^31 - 513");
+  const bool f8 = in_type == TFL_E4M3;
+  if (!type_16bit(in_type) && !f8) return fail(TFL_ERR_UNSUPPORTED, "the operands must be fp16, bf16 or e4m3");
+  if (out_type != TFL_F32 && !(type_16bit(out_type) && (f8 || out_type == in_type)))
+    return fail(TFL_ERR_UNSUPPORTED, "the output must be fp32 or of the operands' 16-bit type (e4m3: fp16 or bf16)");
+  if (f8 && max_grad_tokens) return fail(TFL_ERR_UNSUPPORTED, "e4m3 operands have no backward");
+  if (max_grad_tokens && dy_type != TFL_F32 && dy_type != in_type)
+    return fail(TFL_ERR_UNSUPPORTED, "dy must be fp32 or of the operands' type");
+  const int step = f8 ? 16 : 8;
+  if (d_in % step || d_out % step || d_in > (1 << 24) || d_out > (1 << 24))
+    return fail(TFL_ERR_UNSUPPORTED, "d_in and d_out must be multiples of 8 (16 for e4m3 operands), at most 2^24");
+  int dev = 0, sms = 0;
+  if (int rc = usable_device(&dev, &sms)) return rc;
+  if (!get_encode()) return fail(TFL_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  TileUnits units;
+  if (int rc = tile_units(dev, sms, &units)) return rc;
+  if (units.pairs < 1) return fail(TFL_ERR_UNSUPPORTED, "the device runs no CTA pairs");
+  tfl_linear* l = new (std::nothrow) tfl_linear();
+  if (!l) return fail(TFL_ERR_OOM, "handle allocation failed");
+  l->K = d_in;
+  l->N = d_out;
+  l->in_type = in_type;
+  l->out_type = out_type;
+  l->act = act;
+  l->dy_type = dy_type;
+  l->max_grad_tokens = max_grad_tokens;
+  l->device = dev;
+  l->units = units;
+  l->pitch = (d_out + 63) / 64 * 64;
+  size_t sums = 0, slopes = 0;
+  if (max_grad_tokens) {
+    l->blocks = partial_rows(d_out, sms * 2);
+    sums = ((size_t)l->blocks * d_out * 4 + 255) / 256 * 256;
+    if (act != TFL_ACT_NONE || dy_type == TFL_F32) slopes = (size_t)max_grad_tokens * l->pitch * 2;
+  }
+  if (cudaMalloc(&l->status, 256 + sums + slopes) != cudaSuccess) {
+    cudaGetLastError();
+    delete l;
+    return fail(TFL_ERR_OOM, "scratch allocation for the linear layer failed");
+  }
+  uint8_t* base = reinterpret_cast<uint8_t*>(l->status);
+  if (sums) l->partial = reinterpret_cast<float*>(base + 256);
+  if (slopes) l->dz = reinterpret_cast<uint16_t*>(base + 256 + sums);
+  if (cudaMemset(l->status, 0, 256) != cudaSuccess) {
+    cudaFree(l->status);
+    delete l;
+    return fail(TFL_ERR_CUDA, "status word clear failed");
+  }
+  *out = l;
+  return TFL_OK;
+}
+
+int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float* x_scale, const void* w,
+                       const float* w_scale, const float* bias, const void* res, void* z, void* y, tfl_stream stream) {
+  g_err.clear();
+  if (!l) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  if (int rc = check_tokens(l, tokens)) return rc;
+  if (tokens == 0) return TFL_OK;
+  if (!x || !w || !y) return fail(TFL_ERR_INVALID_ARG, "x, w and y must be non-NULL device pointers");
+  const bool f8 = l->in_type == TFL_E4M3;
+  if (f8 ? !(x_scale && w_scale) : (x_scale || w_scale))
+    return fail(TFL_ERR_INVALID_ARG, "scales go with e4m3 operands, and only with them");
+  if (z && (f8 || l->act == TFL_ACT_NONE))
+    return fail(TFL_ERR_INVALID_ARG, "z goes with 16-bit operands and an activation, and only with them");
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(y, 16) || misaligned(z, 16) || misaligned(res, 16) ||
+      misaligned(bias, 16) || misaligned(w_scale, 16) || misaligned(x_scale, 4))
+    return fail(TFL_ERR_INVALID_ARG, "every buffer but x's scales must be 16-byte aligned");
+  const size_t es = f8 ? 1 : 2, os = type_size(l->out_type), T = (size_t)tokens, K = l->K, N = l->N;
+  const Span sy{y, T * N * os, l->out_type}, sz{z, T * N * 2, l->in_type}, sr{res, T * N * os, l->out_type};
+  const Span in[5] = {{x, T * K * es, 0}, {w, N * K * es, 0}, {x_scale, T * 4, 0}, {w_scale, N * 4, 0}, {bias, N * 4, 0}};
+  bool bad = overlap(sy, sz, false) || overlap(sy, sr, true) || overlap(sz, sr, false);
+  for (const Span& i : in) bad = bad || overlap(sy, i, false) || overlap(sz, i, false);
+  if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+  if (int rc = same_device(l->device)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (lin_few_fits(tokens, (int64_t)l->K * (int64_t)es)) {
+    LinFewArgs a;
+    a.tokens = (int)tokens;
+    a.d_out = l->N;
+    a.row_bytes = l->K * (int)es;
+    a.act = l->act;
+    a.bf16 = f8 ? l->out_type == TFL_BF16 : l->in_type == TFL_BF16;
+    a.out_f32 = l->out_type == TFL_F32;
+    a.x = static_cast<const uint8_t*>(x);
+    a.w = static_cast<const uint8_t*>(w);
+    a.x_scale = x_scale;
+    a.w_scale = w_scale;
+    a.bias = bias;
+    a.res = res;
+    a.z = static_cast<uint16_t*>(z);
+    a.out = y;
+    TFL_CUDA(launch_lin_few(l->in_type, a, l->units.sms, st), "linear layer");
+    return TFL_OK;
+  }
+  const TilePlan p = linear_call_plan(l->K, l->N, f8, LIN_PART_FORWARD, tokens, l->units);
+  TileMaps mp;
+  if (!make_map(&mp.a0, x, tokens, l->K, (int)es, p.a_rows) || !make_map(&mp.b0, w, l->N, l->K, (int)es, p.bno / p.cg))
+    return fail(TFL_ERR_CUDA, "linear layer tensor map encoding failed");
+  mp.a1 = mp.a0;
+  mp.b1 = mp.b0;
+  TileArgs a = linear_args(l);
+  a.M = (int)tokens;
+  a.N = l->N;
+  a.num_k = (l->K + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
+  a.x_scale = x_scale;
+  a.g_scale = w_scale;
+  a.bias = bias;
+  a.res = res;
+  a.z = static_cast<uint16_t*>(z);
+  a.ldo = l->N;
+  a.out = static_cast<uint16_t*>(y);
+  TFL_CUDA(launch_linear(p, f8, mp, a, st), "linear layer");
+  return TFL_OK;
+}
+
+int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void* w, const void* z, const void* dy,
+                        void* dx, void* dw, float* db, tfl_stream stream) {
+  g_err.clear();
+  if (!l) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  if (int rc = check_tokens(l, tokens)) return rc;
+  if (l->in_type == TFL_E4M3) return fail(TFL_ERR_UNSUPPORTED, "e4m3 operands have no backward");
+  if (tokens > l->max_grad_tokens)
+    return fail(TFL_ERR_INVALID_ARG, "more tokens than the max_grad_tokens the handle was created with");
+  if (!dx && !dw && !db) return fail(TFL_ERR_INVALID_ARG, "one of dx, dw and db must be given");
+  if (misaligned(x, 16) || misaligned(w, 16) || misaligned(z, 16) || misaligned(dy, 16) || misaligned(dx, 16) ||
+      misaligned(dw, 16) || misaligned(db, 16))
+    return fail(TFL_ERR_INVALID_ARG, "every buffer must be 16-byte aligned");
+  const size_t T = (size_t)tokens, K = l->K, N = l->N;
+  const Span outs[3] = {{dx, T * K * 2, 0}, {dw, N * K * 2, 0}, {db, N * 4, 0}};
+  const Span ins[4] = {{x, T * K * 2, 0}, {w, N * K * 2, 0}, {z, T * N * 2, 0}, {dy, T * N * type_size(l->dy_type), 0}};
+  bool bad = overlap(outs[0], outs[1], false) || overlap(outs[0], outs[2], false) || overlap(outs[1], outs[2], false);
+  for (const Span& o : outs)
+    for (const Span& i : ins) bad = bad || overlap(o, i, false);
+  if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
+  if (tokens && (!dy || (dx && !w) || (dw && !x)))
+    return fail(TFL_ERR_INVALID_ARG, "dy, w for dx and x for dw must be non-NULL device pointers");
+  const bool act = l->act != TFL_ACT_NONE;
+  if (tokens && act != (z != nullptr))
+    return fail(TFL_ERR_INVALID_ARG, "z goes with an activation, and only with one");
+  if (int rc = same_device(l->device)) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    if (dw) TFL_CUDA(cudaMemsetAsync(dw, 0, N * K * 2, st), "dw clear");
+    if (db) TFL_CUDA(cudaMemsetAsync(db, 0, N * 4, st), "db clear");
+    return TFL_OK;
+  }
+  const int Ki = l->K, Ni = l->N, Ti = (int)tokens;
+  const int kn = (Ni + 63) / 64, kt = (Ti + 63) / 64;
+  const bool slopes = l->dz && (dx || dw);
+  const void* dz = slopes ? l->dz : dy;
+  const int pitch = slopes ? l->pitch : Ni;
+  const TilePlan p1 = linear_call_plan(Ki, Ni, false, LIN_PART_DX, tokens, l->units);
+  const TilePlan p2 = linear_call_plan(Ki, Ni, false, LIN_PART_DW, tokens, l->units);
+  TileMaps m1, m2;
+  if (dx && !(make_map(&m1.a0, dz, tokens, Ni, 2, p1.a_rows, pitch) && make_map(&m1.b0, w, Ni, Ki, 2, kMnBox)))
+    return fail(TFL_ERR_CUDA, "linear layer tensor map encoding failed");
+  if (dw && !(make_map(&m2.a0, dz, tokens, Ni, 2, kMnBox, pitch) && make_map(&m2.b0, x, tokens, Ki, 2, kMnBox)))
+    return fail(TFL_ERR_CUDA, "linear layer tensor map encoding failed");
+  m1.a1 = m1.a0;
+  m1.b1 = m1.b0;
+  m2.a1 = m2.a0;
+  m2.b1 = m2.b0;
+  if (slopes || db) {
+    LinSlopeArgs a;
+    a.rows = tokens;
+    a.cols = Ni;
+    a.pitch = l->pitch;
+    a.dy_type = l->dy_type;
+    a.type = l->in_type;
+    a.act = l->act;
+    a.dy = dy;
+    a.z = static_cast<const uint16_t*>(z);
+    a.dz = slopes ? l->dz : nullptr;
+    a.db = db;
+    a.partial = l->partial;
+    a.blocks = l->blocks;
+    TFL_CUDA(launch_lin_slopes(a, l->units.sms, st), "linear layer slopes");
+  }
+  TileArgs a = linear_args(l);
+  a.bf16_out = a.bf16_operands;
+  if (dx) {
+    a.M = Ti;
+    a.N = Ki;
+    a.num_k = a.k_half = kn;
+    a.ldo = Ki;
+    a.out = static_cast<uint16_t*>(dx);
+    TFL_CUDA(launch_tiles(p1, GRAD_DX, false, m1, a, st), "linear layer dx");
+  }
+  if (dw) {
+    a.M = Ni;
+    a.N = Ki;
+    a.num_k = kt;
+    a.planes = 1;
+    a.ldo = Ki;
+    a.out = static_cast<uint16_t*>(dw);
+    TFL_CUDA(launch_tiles(p2, GRAD_DW, false, m2, a, st), "linear layer weight gradient");
+  }
+  return TFL_OK;
+}
+
+int tfl_selftest_linear_plan(int32_t d_in, int32_t d_out, int32_t in_type, int32_t part, int64_t tokens,
+                             const int32_t* units, int32_t* out) {
+  g_err.clear();
+  const bool f8 = in_type == TFL_E4M3;
+  if (!out || d_in < 1 || d_in > (1 << 24) || d_out < 1 || d_out > (1 << 24) || tokens < 1 || tokens > INT32_MAX - 512 ||
+      part < LIN_PART_FORWARD || part > LIN_PART_DW || !(f8 ? part == LIN_PART_FORWARD : type_16bit(in_type)))
+    return fail(TFL_ERR_INVALID_ARG, "no such launch");
+  TileUnits u;
+  if (int rc = selftest_units(units, &u)) return rc;
+  for (int i = 0; i < 4; ++i) out[i] = 0;
+  if (part == LIN_PART_FORWARD && lin_few_fits(tokens, (int64_t)d_in * (f8 ? 1 : 2))) return TFL_OK;
+  const int mode = part == LIN_PART_FORWARD ? LIN_FORWARD : part == LIN_PART_DX ? GRAD_DX : GRAD_DW;
+  tell_plan(linear_call_plan(d_in, d_out, f8, part, tokens, u), mode, out);
+  return TFL_OK;
+}
+
+int tfl_linear_status(tfl_linear* l, tfl_stream stream) {
+  g_err.clear();
+  if (!l) return fail(TFL_ERR_INVALID_ARG, "handle is NULL");
+  return read_status(l->status, static_cast<cudaStream_t>(stream));
+}
+
+void tfl_linear_destroy(tfl_linear* l) {
+  if (!l) return;
+  release(l->device, l->status);
+  delete l;
 }
 
 }  // extern "C"

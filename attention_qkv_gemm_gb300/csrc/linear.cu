@@ -1,0 +1,150 @@
+// linear.cu -- the linear layer with its epilogue, y = act(x W^T + b) + res, forward and backward.
+//
+// Forward: the tiled tcgen05 kernel (tile_gemm.cuh) in mode LIN_FORWARD.  Bias, activation and residual are
+// applied to the fp32 accumulators, so only y is rounded, once; for training z = x W^T + b is stored too,
+// rounded to the operands' type, since the backward would need the whole product again for act'(z)
+// (half as much work as both gradients) where reading z costs 2 bytes a value.
+//
+// Backward, with dz = dy act'(z):
+//   dx = dz W       GRAD_DX of the same kernel, W read as [k, n] (MN-major)
+//   dW = dz^T x     GRAD_DW, a sum over the tokens, both operands MN-major
+//   db = sum dz     and dz itself, in one pass over dy and z; fp32 sums of the unrounded dz
+// dz is rounded to the operands' type, which the tensor cores take.  Without an activation and with dy of
+// that type it is dy, and the pass only adds up its columns.
+#include "tile_gemm.cuh"
+
+#include "rowops.cuh"
+
+namespace tfl {
+
+// Both operand types in every (CTAs of a tile, form).
+#define TFL_LIN_VARIANTS(X)                                                                        \
+  X(2, false, kWide) X(2, true, kWide) X(2, false, kNarrow) X(2, true, kNarrow)                    \
+  X(1, false, kNarrow) X(1, true, kNarrow) X(1, false, kSplit) X(1, true, kSplit)
+
+cudaError_t prepare_linear_kernels() {
+  cudaError_t e = cudaSuccess;
+#define TFL_PREP(CG, F8, FORM) \
+  if (e == cudaSuccess) e = prepare_one<CG, LIN_FORWARD, F8, FORM>();
+  TFL_LIN_VARIANTS(TFL_PREP)
+#undef TFL_PREP
+  return e;
+}
+
+cudaError_t launch_linear(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s) {
+  const int is = tile_form(p, LIN_FORWARD);
+  const int form = is == TFL_GLU_FORM_SHARED ? kSplit : is == TFL_GLU_FORM_WIDE ? kWide : kNarrow;
+#define TFL_LAUNCH(CG, F8, FORM) \
+  if (p.cg == CG && form == FORM && f8 == F8) return launch_one<CG, LIN_FORWARD, F8, FORM>(mp, a, p, s);
+  TFL_LIN_VARIANTS(TFL_LAUNCH)
+#undef TFL_LAUNCH
+  return cudaErrorInvalidValue;
+}
+
+namespace {
+
+// z within +-1e4, where the slopes are 0 and 1 to the last bit: at infinity their products are no numbers.
+__device__ __forceinline__ float bounded(float z) { return fabsf(z) > 1e4f ? copysignf(1e4f, z) : z; }
+
+// dz = dy act'(z) and this block's sums of its columns: TX threads across 8 columns each, 256 / TX rows at
+// a time, the rows of a column slab shared out to gridDim.y blocks.  Every value is read once: bandwidth
+// bounds it.
+template <class DY, class T, int ACT>
+__global__ void __launch_bounds__(256) lin_slopes_kernel(const LinSlopeArgs a) {
+  constexpr int AT_ONCE = sizeof(DY) == 4 ? 2 : 4;  // rows in flight a thread
+  __shared__ float part[256 * 8];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const int tx = a.tx, x = threadIdx.x & (tx - 1), y = threadIdx.x / tx, ys = 256 / tx;
+  const int c = (blockIdx.x * tx + x) * 8;
+  const bool in = c < a.cols;
+  // whole turns of the block's rows
+  const int64_t turns = (a.rows + ys - 1) / ys, t0 = turns * blockIdx.y / gridDim.y, t1 = turns * (blockIdx.y + 1) / gridDim.y;
+  const int64_t end = t1 * ys < a.rows ? t1 * ys : a.rows;
+  const DY* dy = static_cast<const DY*>(a.dy) + c;
+  const T* z = reinterpret_cast<const T*>(a.z) + c;
+  T* dz = reinterpret_cast<T*>(a.dz) + c;
+  uint64_t sum[4] = {0, 0, 0, 0};  // two zeros each
+  for (int64_t row = t0 * ys + y; row < end; row += AT_ONCE * ys) {
+    Raw8<DY> d1[AT_ONCE];
+    Raw8<T> z1[AT_ONCE];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int64_t r = row + (int64_t)j * ys;
+      if (in && r < end) {
+        load_raw(dy + (size_t)r * a.cols, d1[j]);
+        if (ACT != TFL_ACT_NONE) load_raw(z + (size_t)r * a.cols, z1[j]);
+      } else {
+        zero_raw(d1[j]);
+        zero_raw(z1[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int64_t r = row + (int64_t)j * ys;
+      uint64_t d[4];
+      widen2(d1[j], d);
+      if constexpr (ACT != TFL_ACT_NONE) {
+        float f[8];
+        widen(z1[j], f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // an infinite z (fp16 overflows past 65504) has the slope of a large one; a NaN stays one
+          uint64_t unused, slope;
+          act2<ACT, true>(f2_pack(bounded(f[2 * i]), bounded(f[2 * i + 1])), unused, slope);
+          d[i] = f2_mul(d[i], slope);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = f2_add(sum[i], d[i]);
+      if (a.dz && in && r < end) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f2_unpack(d[i], o[2 * i], o[2 * i + 1]);
+        store8(dz + (size_t)r * a.pitch, o);
+      }
+    }
+  }
+  if (!a.db) return;
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(sum[i], f[2 * i], f[2 * i + 1]);
+  store8(part + threadIdx.x * 8, f);
+  __syncthreads();
+  for (int i = threadIdx.x; i < tx * 8; i += 256) {
+    const int col = blockIdx.x * tx * 8 + i;
+    float v = 0.f;
+    for (int k = 0; k < ys; ++k) v += part[k * tx * 8 + i];
+    if (col < a.cols) a.partial[(size_t)blockIdx.y * a.cols + col] = v;
+  }
+}
+
+template <class DY, class T>
+cudaError_t slopes(LinSlopeArgs a, int num_sms, cudaStream_t s) {
+  a.tx = pow2_at_least(a.cols / 8);
+  if (a.tx > 32) a.tx = 32;
+  const int64_t slabs = (a.cols / 8 + a.tx - 1) / a.tx, ys = 256 / a.tx, turns = (a.rows + ys - 1) / ys;
+  int64_t n = ((int64_t)num_sms * 8 + slabs - 1) / slabs;  // blocks of a slab
+  if (n > turns) n = turns;
+  if (n > a.blocks) n = a.blocks;
+  if (n > 65535) n = 65535;
+  const bool lone = n == 1;
+  if (lone) a.partial = a.db;
+  const dim3 grid((unsigned)slabs, (unsigned)n);
+  const cudaError_t e = a.act == TFL_ACT_SILU   ? launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_SILU>, grid, 256, 0, s, a)
+                        : a.act == TFL_ACT_GELU ? launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_GELU>, grid, 256, 0, s, a)
+                                                : launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_NONE>, grid, 256, 0, s, a);
+  if (e != cudaSuccess || !a.db || lone) return e;
+  return launch_column_sums(a.partial, (int)n, a.cols, a.cols, a.cols, a.db, nullptr, s);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_slopes(const LinSlopeArgs& a, int num_sms, cudaStream_t s) {
+  if (a.type == TFL_F16)
+    return a.dy_type == TFL_F32 ? slopes<float, __half>(a, num_sms, s) : slopes<__half, __half>(a, num_sms, s);
+  return a.dy_type == TFL_F32 ? slopes<float, __nv_bfloat16>(a, num_sms, s)
+                              : slopes<__nv_bfloat16, __nv_bfloat16>(a, num_sms, s);
+}
+
+}  // namespace tfl

@@ -83,52 +83,62 @@ struct LnGradArgs {
 cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_ln_backward(const LnGradArgs& a, int num_sms, cudaStream_t s);
 
-// Gated feed-forward (glu.cu).
-enum GluMode : int {
+// Matrix products of the gated feed-forward (glu.cu) and the linear layer (linear.cu), tile by tile
+// (tile_gemm.cuh).
+enum TileMode : int {
   GLU_FORWARD = 0,  // out[M, N] = act(A B0^T) * (A B1^T)
   GLU_SLOPES = 1,   // out[M, N] = dh u act'(g), out2[M, N] = dh act(g), g = A B0^T, u = A B1^T
-  GLU_DX = 2,       // out[M, N] = A0 B0 + A1 B1
-  GLU_DW = 3,       // out[M, N] = A0^T B0, out2[M, N] = A1^T B0
+  GRAD_DX = 2,      // out[M, N] = A0 B0 + A1 B1, the second sum empty for the linear layer
+  GRAD_DW = 3,      // out[M, N] = A0^T B0, out2[M, N] = A1^T B0, the second for the feed-forward only
+  LIN_FORWARD = 4,  // z[M, N] = A B0^T + bias, out[M, N] = act(z) + res
 };
-struct GluArgs {
+struct TileArgs {
   int M = 0, N = 0;              // rows and columns of the output
   int num_k = 0;                 // k-blocks of a tile
   int k_half = 0;                // DX: k-blocks of the first product
+  int planes = 2;                // DW: outputs
   int bno = 0, split = 1, stages = 0, stage_bytes = 0, a_bytes = 0;  // set by the launcher from the plan
   int act = 0;
   int bf16_operands = 0;         // 16-bit operands: bf16, else fp16
   int bf16_out = 0;              // 16-bit outputs (and dh): bf16, else fp16
   int ldo = 0;                   // row pitch of out and out2
   const uint16_t* dh = nullptr;  // SLOPES: [M, N]
-  uint16_t* out = nullptr;
+  uint16_t* out = nullptr;       // (LINEAR: of fp32 with out_f32)
   uint16_t* out2 = nullptr;
   const float *x_scale = nullptr, *g_scale = nullptr, *u_scale = nullptr;  // e4m3: [M], [N], [N]
+  const float* bias = nullptr;   // LINEAR: [N] or null
+  const void* res = nullptr;     // LINEAR: [M, N] of the output's type, or null
+  uint16_t* z = nullptr;         // LINEAR: [M, N] of the operands' type, or null
+  int out_f32 = 0;               // LINEAR: out (and res) fp32
   int* status = nullptr;
   int64_t timeout_ns = 2000000000LL;
 };
-constexpr int kGluRows = 128;  // rows of A a CTA takes
-struct GluMaps {
+constexpr int kTileRows = 128;  // rows of A a CTA takes
+struct TileMaps {
   CUtensorMap a0, a1, b0, b1;
 };
 // How a call is cut: CTAs of a pair (2) or lone ones (1), lone CTAs that share a tile's k-blocks,
 // output columns of a tile, tiles that run at once,
 // rows of A a CTA loads for a tile, tiles in all.
-struct GluPlan {
+struct TilePlan {
   int cg = 0, split = 1, bno = 0, units = 0, a_rows = 0;
   int64_t tiles = 0;
 };
 // What runs at once on a device: lone CTAs, CTA pairs, and clusters of 2, 4 and 8 lone CTAs.
-struct GluUnits {
+struct TileUnits {
   int sms = 0, pairs = 0, splits[3] = {};
 };
-// whole_lines: the rows of x and the weights begin on 128-byte lines.
-GluPlan glu_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const GluUnits& u);
-int glu_form(const GluPlan& p, int mode);  // TFL_GLU_FORM_* of the kernel it runs in
+// whole_lines: the rows of x and the weights begin on 128-byte lines.  planes: GRAD_DW's outputs.
+TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const TileUnits& u, int planes = 2);
+int tile_form(const TilePlan& p, int mode);  // TFL_GLU_FORM_* of the kernel it runs in
 // Kernel attributes, and all of *u but sms for the current device.
-cudaError_t prepare_glu_kernels(GluUnits* u);
-cudaError_t launch_glu(const GluPlan& p, int mode, bool f8, const GluMaps& mp, const GluArgs& a, cudaStream_t s);
+cudaError_t prepare_tile_kernels(TileUnits* u);
+cudaError_t prepare_linear_kernels();
+// All modes but LIN_FORWARD, and that one.
+cudaError_t launch_tiles(const TilePlan& p, int mode, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
+cudaError_t launch_linear(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
 
-// The forward for at most kGluFewTokens tokens (glu_few.cu).
+// The gated feed-forward's forward for at most kGluFewTokens tokens (glu_few.cu).
 constexpr int kGluFewTokens = 16;
 struct GluFewArgs {
   int tokens = 0, d_ff = 0;
@@ -140,5 +150,37 @@ struct GluFewArgs {
 };
 bool glu_few_fits(int64_t tokens, int64_t row_bytes);  // whether this kernel is the faster one
 cudaError_t launch_glu_few(int type, const GluFewArgs& a, int num_sms, cudaStream_t s);
+
+// The linear layer's forward for at most kLinFewTokens tokens (linear_few.cu).
+constexpr int kLinFewTokens = 16;
+struct LinFewArgs {
+  int tokens = 0, d_out = 0;
+  int row_bytes = 0;             // of x and W: d_in elements
+  int act = 0, bf16 = 0;         // 16-bit outputs and z: bf16, else fp16
+  int out_f32 = 0;
+  const uint8_t *x = nullptr, *w = nullptr;
+  const float *x_scale = nullptr, *w_scale = nullptr;  // e4m3
+  const float* bias = nullptr;
+  const void* res = nullptr;
+  uint16_t* z = nullptr;
+  void* out = nullptr;
+};
+bool lin_few_fits(int64_t tokens, int64_t row_bytes);  // whether this kernel is the faster one
+cudaError_t launch_lin_few(int type, const LinFewArgs& a, int num_sms, cudaStream_t s);
+
+// The linear layer's dz = dy act'(z) and the sums of its columns (linear.cu).
+struct LinSlopeArgs {
+  int64_t rows = 0;
+  int cols = 0, pitch = 0;       // of dy and z; row pitch of dz
+  int tx = 0;                    // threads across 8 columns each, set by the launcher
+  int dy_type = 0, type = 0, act = 0;
+  const void* dy = nullptr;
+  const uint16_t* z = nullptr;   // unused without an activation
+  uint16_t* dz = nullptr;        // or null
+  float* db = nullptr;           // [cols] or null
+  float* partial = nullptr;      // [blocks, cols]
+  int blocks = 0;                // rows of partial sums there is room for
+};
+cudaError_t launch_lin_slopes(const LinSlopeArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace tfl

@@ -510,6 +510,7 @@ void tfl_layernorm_destroy(tfl_layernorm* n);
  */
 #define TFL_ACT_SILU 0   /* z / (1 + e^-z) */
 #define TFL_ACT_GELU 1   /* z Phi(z), the exact erf form (Phi to 7.5e-8 absolute) */
+#define TFL_ACT_NONE 2   /* z: the linear layer below only */
 typedef struct tfl_glu tfl_glu;
 
 /* d_model and d_ff: multiples of 8 (16 for e4m3 operands) up to 2^24.
@@ -553,6 +554,78 @@ int tfl_glu_backward(tfl_glu* g, int64_t tokens, const void* x, const void* wg, 
 int tfl_glu_status(tfl_glu* g, tfl_stream stream);
 
 void tfl_glu_destroy(tfl_glu* g);
+
+/*
+ * Linear layer with its epilogue, the projections and the feed-forward halves of the
+ * stack above on their own:
+ *   z = x W^T + bias,   y = act(z) + res
+ * with W in nn.Linear layout [d_out, d_in].  Products accumulate in fp32; bias,
+ * activation and residual are applied to the fp32 sums and y is rounded once.
+ *
+ * Operands (x, W): fp16 or bf16; or e4m3 with one fp32 scale a row (the stored
+ * value times its row's scale is the operand's value, as the norms above write x).
+ * y and res: fp32, or 16 bits, the operands' type where they have 16.  bias is fp32.
+ */
+typedef struct tfl_linear tfl_linear;
+
+/* d_in and d_out: multiples of 8 (16 for e4m3 operands) up to 2^24.  act: TFL_ACT_NONE,
+ * TFL_ACT_SILU or TFL_ACT_GELU.
+ * max_grad_tokens: the most tokens tfl_linear_backward will be given (0: no
+ * backward; e4m3 operands have none), and dy_type the type of its dy, fp32 or the
+ * operands' (not looked at without a backward).  The handle holds 4 d_out bytes a row
+ * of at most 64 MiB (one row at least) of partial sums for it, and with an activation or an
+ * fp32 dy 2 max_grad_tokens d_out bytes more (d_out to the next multiple of 64).
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
+int tfl_linear_create(int32_t d_in, int32_t d_out, int32_t in_type, int32_t out_type, int32_t act, int32_t dy_type,
+                      int64_t max_grad_tokens, tfl_linear** out);
+
+/*
+ * Asynchronous on `stream`.  Device pointers, 16-byte aligned, row-major and
+ * contiguous; any number of tokens from 0 (nothing is done):
+ *   x [tokens, d_in], w [d_out, d_in], bias fp32 [d_out] or NULL
+ *   x_scale fp32 [tokens] (4-byte aligned), w_scale fp32 [d_out] for e4m3
+ *   operands, else NULL
+ *   res  [tokens, d_out] of y's type, or NULL; may be y
+ *   z    [tokens, d_out] of the operands' type, which the backward of a layer
+ *        with an activation takes; or NULL (not stored; always so without an
+ *        activation and for e4m3 operands)
+ *   y    [tokens, d_out]
+ * Other overlaps of an output are refused.  Rows do not affect one another.
+ * Calls on one handle may overlap.  Errors: INVALID_ARG (also when the current
+ * device is not the handle's), UNSUPPORTED, CUDA; a device-side wait that ran out
+ * surfaces through tfl_linear_status.
+ */
+int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float* x_scale, const void* w,
+                       const float* w_scale, const float* bias, const void* res, void* z, void* y, tfl_stream stream);
+
+/*
+ * The gradients, with dz = dy act'(z) (dy without an activation; res's gradient is dy):
+ *   dx = dz W  [tokens, d_in],   dw = dz^T x  [d_out, d_in],   db = sum over tokens of dz  fp32 [d_out]
+ *   x, w  as in the forward;  z  as it stored it, NULL without an activation
+ *   dy    [tokens, d_out] of the handle's dy_type
+ * dx, dw and db may each be NULL (not computed; w is then not read for dx, nor x for
+ * dw, and may be NULL too); one at least is given.
+ * dx and dw are of the operands' type.  dz is rounded to it once for the products (in
+ * fp16 it overflows past 65504: scale the loss); db sums dz unrounded; sums are
+ * fp32, each gradient is rounded once.  Outputs are written in full (dw, db:
+ * zeros for 0 tokens) and must not overlap anything.  No atomics: the same
+ * inputs give the same bits.  Calls on one handle share its scratch and must not
+ * overlap on the GPU (graphs that hold such calls included).
+ * Errors: INVALID_ARG (also for more than max_grad_tokens), UNSUPPORTED, CUDA.
+ */
+int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void* w, const void* z, const void* dy,
+                        void* dx, void* dw, float* db, tfl_stream stream);
+
+/* Synchronize `stream`, read and clear the status word: TFL_OK or TFL_ERR_DEVICE_TIMEOUT. */
+int tfl_linear_status(tfl_linear* l, tfl_stream stream);
+
+/* Free what the handle owns.  Synchronizes the device.  NULL is a no-op. */
+void tfl_linear_destroy(tfl_linear* l);
+
+/* Which kernel a launch of the linear layer takes, as tfl_selftest_glu_plan tells it of
+ * the feed-forward; part 0 the forward, 1 and 2 the backward's dx and dw. */
+int tfl_selftest_linear_plan(int32_t d_in, int32_t d_out, int32_t in_type, int32_t part, int64_t tokens,
+                             const int32_t* units, int32_t* out);
 
 #ifdef __cplusplus
 }
