@@ -411,6 +411,18 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int 
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A row-major [rows, cols] output or residual in boxes of 64 bytes by 32 rows, 64-byte swizzle.
+bool make_io_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem) {
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(cols * elem)};
+  cuuint32_t box[2] = {(cuuint32_t)(64 / elem), 32};
+  cuuint32_t es[2] = {1, 1};
+  return get_encode()(m, elem == 4 ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                      const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Kernel attributes and what runs at once on a device: the same for every handle, asked once.
 int tile_units(int dev, int sms, TileUnits* u) {
   constexpr int kDevices = 64;
@@ -853,10 +865,10 @@ int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float
   }
   const TilePlan p = linear_call_plan(l->K, l->N, f8, LIN_PART_FORWARD, tokens, l->units);
   TileMaps mp;
-  if (!make_map(&mp.a0, x, tokens, l->K, (int)es, p.a_rows) || !make_map(&mp.b0, w, l->N, l->K, (int)es, p.bno / p.cg))
+  if (!make_map(&mp.a0, x, tokens, l->K, (int)es, p.a_rows) || !make_map(&mp.b0, w, l->N, l->K, (int)es, p.bno / p.cg) ||
+      !make_io_map(&mp.a1, y, tokens, l->N, (int)os) || !make_io_map(&mp.b1, z ? z : y, tokens, l->N, z ? 2 : (int)os) ||
+      !make_io_map(&mp.r, res ? res : y, tokens, l->N, (int)os))
     return fail(TFL_ERR_CUDA, "linear layer tensor map encoding failed");
-  mp.a1 = mp.a0;
-  mp.b1 = mp.b0;
   TileArgs a = linear_args(l);
   a.M = (int)tokens;
   a.N = l->N;
@@ -865,9 +877,8 @@ int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float
   a.g_scale = w_scale;
   a.bias = bias;
   a.res = res;
-  a.z = static_cast<uint16_t*>(z);
+  a.z = z != nullptr;
   a.ldo = l->N;
-  a.out = static_cast<uint16_t*>(y);
   TFL_CUDA(launch_linear(p, f8, mp, a, st), "linear layer");
   return TFL_OK;
 }

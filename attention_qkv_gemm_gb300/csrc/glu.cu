@@ -92,13 +92,13 @@ TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num
     if (units < 1) continue;
     const int64_t tile_rows = kTileRows * cg, num_m = (M + tile_rows - 1) / tile_rows;
     const int64_t rows = M < kTileRows ? M : kTileRows;  // rows of A outside the matrix cost no reads
-    // tcgen05.mma takes N in steps of 16, a pair's in steps of 32
-    for (int bn = kMaxBN; bn >= 32; bn -= 16 * cg) {
+    // tcgen05.mma takes N in steps of 16, a pair's in steps of 32; the linear layer stores 32 columns at a time
+    for (int bn = kMaxBN; bn >= 32; bn -= mode == LIN_FORWARD ? 32 : 16 * cg) {
       const int bno = two ? bn / 2 : bn, chunks = (bno + 31) / 32;
       const int64_t tiles = num_m * ((N + bno - 1) / bno) * twice;
       const int64_t rounds = (tiles + units - 1) / units, last = tiles - (rounds - 1) * units;
       const int pieces = (chunks + split - 1) / split;
-      if (split > 1 && (rounds > 1 || (split - 1) * pieces * kTileRows * (two ? 256 : 128) > ring_bytes(false))) continue;
+      if (split > 1 && (rounds > 1 || (split - 1) * pieces * kTileRows * (two ? 256 : 128) > ring_bytes(false, mode == LIN_FORWARD))) continue;
       double block = (bn == kMaxBN ? 555.0 : 600.0) * bn / kMaxBN;
       const double stream = (double)(rows + bn / cg) * kKBytes / (whole_lines ? 74.0 : 44.0);
       if (block < stream) block = stream;

@@ -101,21 +101,22 @@ struct TileArgs {
   int act = 0;
   int bf16_operands = 0;         // 16-bit operands: bf16, else fp16
   int bf16_out = 0;              // 16-bit outputs (and dh): bf16, else fp16
-  int ldo = 0;                   // row pitch of out and out2
+  int ldo = 0;                   // row pitch of out and out2 (LINEAR: of the residual)
   const uint16_t* dh = nullptr;  // SLOPES: [M, N]
-  uint16_t* out = nullptr;       // (LINEAR: of fp32 with out_f32)
+  uint16_t* out = nullptr;
   uint16_t* out2 = nullptr;
   const float *x_scale = nullptr, *g_scale = nullptr, *u_scale = nullptr;  // e4m3: [M], [N], [N]
   const float* bias = nullptr;   // LINEAR: [N] or null
   const void* res = nullptr;     // LINEAR: [M, N] of the output's type, or null
-  uint16_t* z = nullptr;         // LINEAR: [M, N] of the operands' type, or null
-  int out_f32 = 0;               // LINEAR: out (and res) fp32
+  int z = 0;                     // LINEAR: z is stored
+  int out_f32 = 0;               // LINEAR: y (and res) fp32
   int* status = nullptr;
   int64_t timeout_ns = 2000000000LL;
 };
 constexpr int kTileRows = 128;  // rows of A a CTA takes
 struct TileMaps {
-  CUtensorMap a0, a1, b0, b1;
+  CUtensorMap a0, a1, b0, b1;  // LIN_FORWARD: a1 is y, b1 z, in boxes of 64 bytes by 32 rows
+  CUtensorMap r;               // LIN_FORWARD: the residual, in the same boxes
 };
 // How a call is cut: CTAs of a pair (2) or lone ones (1), lone CTAs that share a tile's k-blocks,
 // output columns of a tile, tiles that run at once,

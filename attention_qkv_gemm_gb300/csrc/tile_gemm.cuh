@@ -24,9 +24,14 @@ constexpr int kMaxBN = 256;        // accumulator columns of a tile, at most
 constexpr int kMaxStages = 12;
 // Shared memory: ring, one 32-row transpose stage an epilogue warp, barriers.
 constexpr int kBarrierBytes = 256;
-__host__ __device__ constexpr int xpose_bytes(bool wide) { return wide ? 32768 : 16384; }
+__host__ __device__ constexpr int xpose_bytes(bool sixteen) { return sixteen ? 32768 : 16384; }
 constexpr int kTileSmem = 232448;
-__host__ __device__ constexpr int ring_bytes(bool wide) { return kTileSmem - 1024 - xpose_bytes(wide) - kBarrierBytes; }
+// lin: sixteen stages that TMA swizzles (on 512 bytes), and a barrier for each.
+constexpr int kLinRing = 193 * 1024, kLinResBar = 31;  // (bytes; the first of those barriers, behind the others)
+__host__ __device__ constexpr int ring_bytes(bool wide, bool lin = false) {
+  return lin ? kLinRing : kTileSmem - 1024 - xpose_bytes(wide) - kBarrierBytes;
+}
+static_assert(1024 + kLinRing + xpose_bytes(true) + (kLinResBar + 16) * 8 <= kTileSmem, "shared memory");
 
 // The activation of a packed pair of fp32 values (FMA-pipe work runs two lanes an instruction;
 // the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
@@ -119,11 +124,13 @@ __device__ __forceinline__ void unpack16(const uint4& w, float* v, int bf16) {
   }
 }
 
-// W 16-bit columns of the warp's 32 rows from the stage to global memory; rows by mask,
+// W 16-bit columns of the warp's 32 rows through the stage to global memory; rows by mask,
 // columns (8 a chunk) below `cols`.
 template <int W>
-__device__ __forceinline__ void flush_cols(uint8_t* st, int lane, uint16_t* row0, size_t pitch, uint32_t rows, int cols) {
+__device__ __forceinline__ void store_cols(uint8_t* st, int lane, const uint4* v, uint16_t* row0, size_t pitch,
+                                           uint32_t rows, int cols) {
   using X = XStage<W * 2>;
+  X::put_row(st, lane, v);
   __syncwarp();
   uint4 o[X::CPR];
 #pragma unroll
@@ -136,13 +143,6 @@ __device__ __forceinline__ void flush_cols(uint8_t* st, int lane, uint16_t* row0
     if (((rows >> i) & 1u) && q * 8 < cols) *reinterpret_cast<uint4*>(row0 + (size_t)i * pitch + q * 8) = o[k];
   }
   __syncwarp();
-}
-// The same, each thread putting its row there first.
-template <int W>
-__device__ __forceinline__ void store_cols(uint8_t* st, int lane, const uint4* v, uint16_t* row0, size_t pitch,
-                                           uint32_t rows, int cols) {
-  XStage<W * 2>::put_row(st, lane, v);
-  flush_cols<W>(st, lane, row0, pitch, rows, cols);
 }
 // The same way back: this thread's row of W 16-bit columns (zeros outside).
 template <int W>
@@ -175,37 +175,6 @@ struct Tile {
   int m, n, z;
 };
 
-// The same for 16 fp32 columns (32 rows of 64 bytes: a warp's whole stage).
-__device__ __forceinline__ void store_cols_f32(uint8_t* st, int lane, const float* v, float* row0, size_t pitch,
-                                               uint32_t rows, int cols) {
-  using X = XStage<64>;
-  uint4 w[4];
-  pack_f32x16(v, w);
-  X::put_row(st, lane, w);
-  __syncwarp();
-  const int q = lane % X::CPR;
-  uint4 o[X::CPR];
-#pragma unroll
-  for (int k = 0; k < X::CPR; ++k) o[k] = *reinterpret_cast<const uint4*>(st + X::off(X::RPI * k + lane / X::CPR, q));
-#pragma unroll
-  for (int k = 0; k < X::CPR; ++k) {
-    const int i = X::RPI * k + lane / X::CPR;
-    if (((rows >> i) & 1u) && q * 4 < cols) *reinterpret_cast<uint4*>(row0 + (size_t)i * pitch + q * 4) = o[k];
-  }
-  __syncwarp();
-}
-__device__ __forceinline__ void fetch_cols_f32(int lane, uint4* f, const float* row0, size_t pitch, uint32_t rows,
-                                               int cols) {
-  using X = XStage<64>;
-  const int q = lane % X::CPR;
-#pragma unroll
-  for (int k = 0; k < X::CPR; ++k) {
-    const int i = X::RPI * k + lane / X::CPR;
-    f[k] = ((rows >> i) & 1u) && q * 4 < cols ? *reinterpret_cast<const uint4*>(row0 + (size_t)i * pitch + q * 4)
-                                              : make_uint4(0, 0, 0, 0);
-  }
-}
-
 // Tiles in groups of kGroupM row blocks, column by column inside a group, so that the tiles in
 // flight share operands through L2.  DW: first all of dWg, then all of dWu.
 constexpr int kGroupM = 8;
@@ -231,12 +200,13 @@ enum TileForm : int { kWide = 0, kNarrow = 1, kSplit = 2 };
 // Epilogue warps: sixteen for the wide tiles, 32 columns each, which a short k needs (8192 x 1024 x 4096
 // e4m3 47.5 -> 45.4 us; the eight before computed 32 columns at a time and stored 64, these 16 and 32,
 // and have the registers for it).  Eight for the narrow tiles, most of which have one or two chunks.
-__host__ __device__ constexpr int epi_warps(int form) { return form == kWide ? 16 : 8; }
-__host__ __device__ constexpr int tile_threads(int form) { return 64 + 32 * epi_warps(form); }
+__host__ __device__ constexpr int epi_warps(int form, bool lin) { return form == kWide || lin ? 16 : 8; }
+__host__ __device__ constexpr int tile_threads(int form, int mode) { return 64 + 32 * epi_warps(form, mode == LIN_FORWARD); }
 template <int CG, int MODE, bool F8, int FORM>
-__global__ void __launch_bounds__(tile_threads(FORM), 1)
+__global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
-               const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1, const TileArgs args) {
+               const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                const __grid_constant__ CUtensorMap tmR, const TileArgs args) {
   constexpr bool WIDE = FORM == kWide, SPLIT = FORM == kSplit;
   static_assert(!SPLIT || CG == 1, "lone CTAs share a tile's k-blocks");
   constexpr bool TWO = MODE == GLU_FORWARD || MODE == GLU_SLOPES;  // two products side by side
@@ -246,20 +216,21 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
   extern __shared__ uint8_t smem_raw[];
   grid_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* xpose = smem + ring_bytes(WIDE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + xpose_bytes(WIDE));
+  uint8_t* xpose = smem + ring_bytes(WIDE, LIN);
+  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + xpose_bytes(WIDE || LIN));
   uint64_t* empty = full + kMaxStages;
   uint64_t* accf = empty + kMaxStages;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint64_t* res_bar = full + kLinResBar;  // LIN_FORWARD: one an epilogue warp
   int* never_flag = abort_flag + 1;  // stays 0: lets the drain waits ignore abort_flag
 
   constexpr int kWideStage = (kTileRows + kMaxBN / CG) * kKBytes;
   const int bno = WIDE ? (TWO ? kMaxBN / 2 : kMaxBN) : args.bno;  // output columns of a tile
   const int bn = TWO ? 2 * bno : bno;                             // accumulator columns
-  const int stages = WIDE ? ring_bytes(true) / kWideStage : args.stages;
+  const int stages = WIDE ? ring_bytes(true, LIN) / kWideStage : args.stages;
   const int stage_bytes = WIDE ? kWideStage : args.stage_bytes;
   const int a_bytes = WIDE ? kTileRows * kKBytes : args.a_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -271,9 +242,12 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&accf[a], 1);
-      mbar_init(&acce[a], CG * epi_warps(FORM));
+      mbar_init(&acce[a], CG * epi_warps(FORM, LIN));
     }
     mbar_init(drain, 1);
+    if constexpr (LIN) {
+      for (int w = 0; w < epi_warps(FORM, LIN); ++w) mbar_init(&res_bar[w], 1);
+    }
     *abort_flag = 0;
     *never_flag = 0;
     fence_barrier_init();
@@ -428,13 +402,38 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    constexpr int H = epi_warps(FORM) / 4;  // warps of a lane quarter, which take the chunks in turn
+    constexpr int H = epi_warps(FORM, LIN) / 4;  // warps of a lane quarter, which take the chunks in turn
     constexpr int W = 32;                   // columns stored at a time
     constexpr int LD = H == 4 ? 16 : 32;    // columns computed at a time
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* st = xpose + (warp - 2) * (32 * 2 * W);
     int acc = 0;
     uint32_t acc_phase = 0;
+    // The linear layer's stage: free once the last store has read it; a piece of the residual on its way into it
+    // (nothing where no row or column of it exists: what is added there is not stored), and out of it.
+    uint64_t* res_in = res_bar + (warp - 2);
+    uint32_t res_phase = 0;
+    bool res_flying = false, dead = false;
+    auto stage_free = [&]() {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+    };
+    auto load_res = [&](int n, int m0) {
+      res_flying = true;
+      if (lane == 0) {
+        const bool exists = n < args.N && m0 < args.M;
+        mbar_arrive_expect_tx(res_in, exists ? 2048 : 0);
+        if (exists) tma_load_2d(st, &tmR, res_in, n, m0);
+      }
+    };
+    auto store_stage = [&](const CUtensorMap* map, int n, int m0, bool exists) {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0 && exists) {
+        tma_store_2d(map, st, n, m0);
+        bulk_commit();
+      }
+    };
     const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], 0) : 0, CG == 2 ? map_rank(&acce[1], 0) : 0};
     for (int t = unit; t < total; t += units) {
       const Tile tl = tile_at(t, num_m, num_n, kGroupM);
@@ -455,12 +454,15 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
         sx = m < args.M ? args.x_scale[m] : 0.f;  // written by the kernel before this one: a plain load
         fetch_scales(part + split * half);
       }
-      // the residual's rows set out for L2 while the products finish, a line or two a row and chunk
+      // the first piece's residual sets out while the products finish, and the other chunks' for L2
       if constexpr (LIN) {
-        if (args.res && m < args.M) {
-          const size_t size = args.out_f32 ? 4 : 2;
-          const uint8_t* r = static_cast<const uint8_t*>(args.res) + (size_t)m * args.ldo * size;
-          for (int c = part + split * half; c * W < bno; c += H * split)
+        int c = part + split * half;
+        if (args.res && c * W < bno) {
+          stage_free();
+          load_res(n_tile + c * W, m0);
+          const int size = args.out_f32 ? 4 : 2;
+          const uint8_t* r = static_cast<const uint8_t*>(args.res) + (size_t)min(m, args.M - 1) * args.ldo * size;
+          while ((c += H * split) * W < bno)
             if (n_tile + c * W < args.N) prefetch_l2(r + (n_tile + c * W) * size);
         }
       }
@@ -517,22 +519,27 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
         const int n0 = n_tile + c * W;                       // first output column
         const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
         if constexpr (LIN) {
-          // In halves of 16 columns, each packed straight into the stage: with sixteen warps there are 96
-          // registers.  z takes a round of its own, which reads the sums a second time, for the same reason.
-          using X = XStage<W * 2>;
-          const size_t to = (size_t)m0 * args.ldo + n0;
-          auto sums = [&](int b, float* g) {  // z of this lane's row
+          // In halves of 16 columns (there are 96 registers): the residual's piece comes into the warp's stage by
+          // TMA, each lane adds it to its row and puts the result in its place, and TMA stores the piece: 32
+          // columns of 16 bits or 16 of fp32.  z, held packed, takes the stage after y.
+          auto at = [&](int i) { return reinterpret_cast<uint4*>(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)); };
+          const bool exists = n0 < args.N && m0 < args.M;
+          uint4 z[4];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const int n = n0 + b * 16, cols = args.N - n;
+            float g[16];
             tmem_ld16(tb + c * W + b * 16, g);
             float4 bias[4], ws[F8 ? 4 : 1] = {};  // the same for all lanes, from L1
             auto fetch = [&](const float* p, float4* v) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                v[i] = p && b * 16 + i * 4 < cols ? *reinterpret_cast<const float4*>(p + n0 + b * 16 + i * 4)
-                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[i] = p && i * 4 < cols ? *reinterpret_cast<const float4*>(p + n + i * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
             };
             fetch(args.bias, bias);
             if constexpr (F8) fetch(args.g_scale, ws);
             tmem_wait_ld();
+            if (!SPLIT && b == 1 && c == last) hand_back();
             if constexpr (SPLIT) {
               for (int k = 0; k < split - 1; ++k) {
                 const uint8_t* from = smem + (k * pieces + c / split) * kPiece + (q * 32 + lane) * 16 + b * 4 * kPart;
@@ -554,53 +561,64 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
               finish2(g + 4 * i, s.x, s.y, bias[i].x, bias[i].y);
               finish2(g + 4 * i + 2, s.z, s.w, bias[i].z, bias[i].w);
             }
-          };
-          auto stage_half = [&](int b, const float* g, int bf16) {
-            uint4 w[2];
-            pack16<16>(g, w, bf16);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(st + X::off(lane, b * 2 + i)) = w[i];
-          };
-          if (args.z) {
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-              float g[16];
-              sums(b, g);
-              stage_half(b, g, args.bf16_operands);
-            }
-            flush_cols<W>(st, lane, args.z + to, args.ldo, rows, cols);
-          }
-          uint4 held[4];  // the residual: of the chunk in 16 bits, of half of it in fp32
-          if (args.res && !args.out_f32)
-            load_cols<W>(st, lane, held, static_cast<const uint16_t*>(args.res) + to, args.ldo, rows, cols);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if (args.res && args.out_f32)
-              fetch_cols_f32(lane, held, static_cast<const float*>(args.res) + to + b * 16, args.ldo, rows, cols - b * 16);
-            float g[16];
-            sums(b, g);
-            if (!SPLIT && b == 1 && c == last) hand_back();
+            if (args.z) pack16<16>(g, z + b * 2, args.bf16_operands);
             if (args.act == TFL_ACT_SILU)
               activate<TFL_ACT_SILU, 16>(g);
             else if (args.act == TFL_ACT_GELU)
               activate<TFL_ACT_GELU, 16>(g);
-            if (args.out_f32) {
-              if (args.res) xp_add_fetched_f32x16(st, lane, g, held);
-              store_cols_f32(st, lane, g, reinterpret_cast<float*>(args.out) + to + b * 16, args.ldo, rows, cols - b * 16);
-            } else {
+            if (b == 0 || args.out_f32) {  // the stage is this piece's
               if (args.res) {
-                float r[8];
+                if (!__all_sync(0xffffffffu, wait_bounded(res_in, res_phase, wc))) {
+                  dead = true;
+                  break;
+                }
+                res_flying = false;
+                res_phase ^= 1u;
+              } else {
+                stage_free();
+              }
+            }
+            if (args.out_f32) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  unpack16(held[b * 2 + i], r, args.bf16_out);
+              for (int i = 0; i < 4; ++i) {
+                uint4* s = at(i);
+                if (args.res) {
+                  const uint4 r = *s;
+                  g[4 * i] += __uint_as_float(r.x), g[4 * i + 1] += __uint_as_float(r.y);
+                  g[4 * i + 2] += __uint_as_float(r.z), g[4 * i + 3] += __uint_as_float(r.w);
+                }
+                *s = make_uint4(__float_as_uint(g[4 * i]), __float_as_uint(g[4 * i + 1]), __float_as_uint(g[4 * i + 2]),
+                                __float_as_uint(g[4 * i + 3]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint4* s = at(b * 2 + i);
+                if (args.res) {
+                  float r[8];
+                  unpack16(*s, r, args.bf16_out);
 #pragma unroll
                   for (int k = 0; k < 8; ++k) g[8 * i + k] += r[k];
                 }
+                pack16<8>(g + 8 * i, s, args.bf16_out);
               }
-              stage_half(b, g, args.bf16_out);
+              if (b == 0) continue;
+            }
+            store_stage(&tmA1, args.out_f32 ? n : n0, m0, exists && (!args.out_f32 || n < args.N));
+            if (b == 1 && args.z) {
+              stage_free();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) *at(i) = z[i];
+              store_stage(&tmB1, n0, m0, exists);
+            }
+            // the next piece's residual
+            const int next = args.out_f32 && b == 0 ? n + 16 : c + H * split < chunks ? n0 + H * split * W : -1;
+            if (args.res && next >= 0) {
+              stage_free();
+              load_res(next, m0);
             }
           }
-          if (!args.out_f32) flush_cols<W>(st, lane, args.out + to, args.ldo, rows, cols);
+          if (dead) break;
         } else {
           uint4 o[W / 8], o2[W / 8];
           if constexpr (MODE == GLU_SLOPES)
@@ -678,10 +696,17 @@ __global__ void __launch_bounds__(tile_threads(FORM), 1)
           if constexpr (MODE == GLU_SLOPES) store_cols<W>(st, lane, o2, args.out2 + to, args.ldo, rows, cols);
         }
       }
+      if (dead) break;
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
+    }
+    if constexpr (LIN) {
+      // nothing may land in or be read from this CTA's shared memory once it is gone
+      const WaitCtl dc{args.status, never_flag, 100000000LL};
+      if (res_flying) wait_bounded(res_in, res_phase, dc);
+      if (lane == 0) bulk_wait<0>();
     }
   }
 
@@ -718,12 +743,12 @@ cudaError_t launch_one(const TileMaps& mp, TileArgs a, const TilePlan& p, cudaSt
   const bool b_mn = MODE == GRAD_DX || MODE == GRAD_DW;
   a.a_bytes = p.a_rows * kKBytes;
   a.stage_bytes = a.a_bytes + (b_mn ? (bn / CG + 63) / 64 * kMnChunk : bn / CG * kKBytes);
-  a.stages = ring_bytes(FORM == kWide) / a.stage_bytes;
+  a.stages = ring_bytes(FORM == kWide, MODE == LIN_FORWARD) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   const int cluster = CG * p.split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tiles < p.units ? p.tiles : p.units) * cluster);
-  cfg.blockDim = dim3(tile_threads(FORM));
+  cfg.blockDim = dim3(tile_threads(FORM, MODE));
   cfg.dynamicSmemBytes = kTileSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -734,7 +759,7 @@ cudaError_t launch_one(const TileMaps& mp, TileArgs a, const TilePlan& p, cudaSt
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, tile_kernel<CG, MODE, F8, FORM>, mp.a0, mp.a1, mp.b0, mp.b1, a);
+  return cudaLaunchKernelEx(&cfg, tile_kernel<CG, MODE, F8, FORM>, mp.a0, mp.a1, mp.b0, mp.b1, mp.r, a);
 }
 
 template <int CG, int MODE, bool F8, int FORM>
@@ -748,7 +773,7 @@ template <int CG, int FORM>
 cudaError_t clusters_at_once(int size, int* n) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(size);
-  cfg.blockDim = dim3(tile_threads(FORM));
+  cfg.blockDim = dim3(tile_threads(FORM, GLU_FORWARD));
   cfg.dynamicSmemBytes = kTileSmem;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
