@@ -1,6 +1,7 @@
 // linear.cu -- the linear layer with its epilogue, y = act(x W^T + b) + res, forward and backward.
 //
-// Forward: the tiled tcgen05 kernel (tile_gemm.cuh) in mode LIN_FORWARD.  Bias, activation and residual are
+// Forward: the tiled tcgen05 kernel (tile_gemm.cuh) in mode LIN_FORWARD (a translation unit for each form of
+// it: linear_wide.cu, linear_pair.cu, linear_lone.cu, linear_shared.cu).  Bias, activation and residual are
 // applied to the fp32 accumulators, so only y is rounded, once; for training z = x W^T + b is stored too,
 // rounded to the operands' type, since the backward would need the whole product again for act'(z)
 // (half as much work as both gradients) where reading z costs 2 bytes a value.
@@ -17,28 +18,20 @@
 
 namespace tfl {
 
-// Both operand types in every (CTAs of a tile, form).
-#define TFL_LIN_VARIANTS(X)                                                                        \
-  X(2, false, kWide) X(2, true, kWide) X(2, false, kNarrow) X(2, true, kNarrow)                    \
-  X(1, false, kNarrow) X(1, true, kNarrow) X(1, false, kSplit) X(1, true, kSplit)
-
 cudaError_t prepare_linear_kernels() {
-  cudaError_t e = cudaSuccess;
-#define TFL_PREP(CG, F8, FORM) \
-  if (e == cudaSuccess) e = prepare_one<CG, LIN_FORWARD, F8, FORM>();
-  TFL_LIN_VARIANTS(TFL_PREP)
-#undef TFL_PREP
-  return e;
+  cudaError_t e = prepare_linear_wide();
+  if (e == cudaSuccess) e = prepare_linear_pair();
+  if (e == cudaSuccess) e = prepare_linear_lone();
+  return e == cudaSuccess ? prepare_linear_shared() : e;
 }
 
 cudaError_t launch_linear(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s) {
-  const int is = tile_form(p, LIN_FORWARD);
-  const int form = is == TFL_GLU_FORM_SHARED ? kSplit : is == TFL_GLU_FORM_WIDE ? kWide : kNarrow;
-#define TFL_LAUNCH(CG, F8, FORM) \
-  if (p.cg == CG && form == FORM && f8 == F8) return launch_one<CG, LIN_FORWARD, F8, FORM>(mp, a, p, s);
-  TFL_LIN_VARIANTS(TFL_LAUNCH)
-#undef TFL_LAUNCH
-  return cudaErrorInvalidValue;
+  switch (tile_form(p, LIN_FORWARD)) {
+    case TFL_GLU_FORM_WIDE: return launch_linear_wide(p, f8, mp, a, s);
+    case TFL_GLU_FORM_PAIR: return launch_linear_pair(p, f8, mp, a, s);
+    case TFL_GLU_FORM_SHARED: return launch_linear_shared(p, f8, mp, a, s);
+  }
+  return launch_linear_lone(p, f8, mp, a, s);
 }
 
 namespace {

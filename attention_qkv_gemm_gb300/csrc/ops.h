@@ -138,6 +138,14 @@ cudaError_t prepare_linear_kernels();
 // All modes but LIN_FORWARD, and that one.
 cudaError_t launch_tiles(const TilePlan& p, int mode, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
 cudaError_t launch_linear(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
+#define TFL_DECLARE_LINEAR_FORM(NAME)   \
+  cudaError_t prepare_linear_##NAME();  \
+  cudaError_t launch_linear_##NAME(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
+TFL_DECLARE_LINEAR_FORM(wide)
+TFL_DECLARE_LINEAR_FORM(pair)
+TFL_DECLARE_LINEAR_FORM(lone)
+TFL_DECLARE_LINEAR_FORM(shared)
+#undef TFL_DECLARE_LINEAR_FORM
 
 // The gated feed-forward's forward for at most kGluFewTokens tokens (glu_few.cu).
 constexpr int kGluFewTokens = 16;

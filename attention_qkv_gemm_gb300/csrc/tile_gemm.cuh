@@ -26,12 +26,13 @@ constexpr int kMaxStages = 12;
 constexpr int kBarrierBytes = 256;
 __host__ __device__ constexpr int xpose_bytes(bool sixteen) { return sixteen ? 32768 : 16384; }
 constexpr int kTileSmem = 232448;
-// lin: sixteen stages that TMA swizzles (on 512 bytes), and a barrier for each.
-constexpr int kLinRing = 193 * 1024, kLinResBar = 31;  // (bytes; the first of those barriers, behind the others)
+// lin: two stages a warp that TMA swizzles (on 512 bytes), and a barrier for each.
+constexpr int kLinStage = 2048, kLinRing = 161 * 1024;
+constexpr int kLinResBar = 31;  // the first of those barriers, behind the others
 __host__ __device__ constexpr int ring_bytes(bool wide, bool lin = false) {
   return lin ? kLinRing : kTileSmem - 1024 - xpose_bytes(wide) - kBarrierBytes;
 }
-static_assert(1024 + kLinRing + xpose_bytes(true) + (kLinResBar + 16) * 8 <= kTileSmem, "shared memory");
+static_assert(1024 + kLinRing + 32 * kLinStage + (kLinResBar + 32) * 8 <= kTileSmem, "shared memory");
 
 // The activation of a packed pair of fp32 values (FMA-pipe work runs two lanes an instruction;
 // the busy epilogue warps otherwise take issue slots from the thread that issues the MMAs):
@@ -167,6 +168,13 @@ __device__ __forceinline__ void load_cols(uint8_t* st, int lane, uint4* v, const
   __syncwarp();
 }
 
+// Until at most N of the warp's last tile stores still read shared memory.
+template <int N>
+__device__ __forceinline__ void stores_read() {
+  if ((threadIdx.x & 31) == 0) bulk_wait_read<N>();
+  __syncwarp();
+}
+
 // The feed-forward's e4m3 scales of output column n, gate's and up's (glu.cu).
 template <int MODE>
 __device__ __forceinline__ float2 column_scales(const TileArgs& args, int n);
@@ -202,7 +210,9 @@ enum TileForm : int { kWide = 0, kNarrow = 1, kSplit = 2 };
 // and have the registers for it).  Eight for the narrow tiles, most of which have one or two chunks.
 __host__ __device__ constexpr int epi_warps(int form, bool lin) { return form == kWide || lin ? 16 : 8; }
 __host__ __device__ constexpr int tile_threads(int form, int mode) { return 64 + 32 * epi_warps(form, mode == LIN_FORWARD); }
-template <int CG, int MODE, bool F8, int FORM>
+// EPI: what the linear layer's epilogue does besides bias and activation.
+enum EpiBits : int { kEpiF32 = 1, kEpiZ = 2, kEpiRes = 4 };  // y (and the residual) fp32; z stored; residual added
+template <int CG, int MODE, bool F8, int FORM, int EPI>
 __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     tile_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
@@ -217,14 +227,14 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   grid_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xpose = smem + ring_bytes(WIDE, LIN);
-  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + xpose_bytes(WIDE || LIN));
+  uint64_t* full = reinterpret_cast<uint64_t*>(xpose + (LIN ? 32 * kLinStage : xpose_bytes(WIDE)));
   uint64_t* empty = full + kMaxStages;
   uint64_t* accf = empty + kMaxStages;
   uint64_t* acce = accf + 2;
   uint64_t* drain = acce + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  uint64_t* res_bar = full + kLinResBar;  // LIN_FORWARD: one an epilogue warp
+  uint64_t* res_bar = full + kLinResBar;  // LIN_FORWARD: two an epilogue warp
   int* never_flag = abort_flag + 1;  // stays 0: lets the drain waits ignore abort_flag
 
   constexpr int kWideStage = (kTileRows + kMaxBN / CG) * kKBytes;
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     }
     mbar_init(drain, 1);
     if constexpr (LIN) {
-      for (int w = 0; w < epi_warps(FORM, LIN); ++w) mbar_init(&res_bar[w], 1);
+      for (int w = 0; w < 2 * epi_warps(FORM, LIN); ++w) mbar_init(&res_bar[w], 1);
     }
     *abort_flag = 0;
     *never_flag = 0;
@@ -406,32 +416,31 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     constexpr int W = 32;                   // columns stored at a time
     constexpr int LD = H == 4 ? 16 : 32;    // columns computed at a time
     const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* st = xpose + (warp - 2) * (32 * 2 * W);
+    uint8_t* st = xpose + (warp - 2) * (LIN ? 2 * kLinStage : 32 * 2 * W);
     int acc = 0;
     uint32_t acc_phase = 0;
-    // The linear layer's stage: free once the last store has read it; a piece of the residual on its way into it
-    // (nothing where no row or column of it exists: what is added there is not stored), and out of it.
-    uint64_t* res_in = res_bar + (warp - 2);
-    uint32_t res_phase = 0;
-    bool res_flying = false, dead = false;
-    auto stage_free = [&]() {
-      if (lane == 0) bulk_wait_read<0>();
-      __syncwarp();
-    };
-    auto load_res = [&](int n, int m0) {
-      res_flying = true;
+    // The linear layer's two stages a warp.  Pieces go out in turn, so that with one store still reading its
+    // stage the other stage is free.  A residual's piece that does not exist (no row or column of it) takes no
+    // copy: what is added there is not stored.
+    uint64_t* res_in = res_bar + (warp - 2) * 2;
+    const int swizzle = ((lane >> 1) & 3) << 4;  // TMA's 64-byte swizzle: the piece of 16 bytes by bits of the row
+    uint32_t res_phase = 0, res_flying = 0;      // a bit a stage
+    int turn = 0;
+    bool dead = false;
+    auto load_res = [&](int stage, int n, int m0) {
+      res_flying |= 1u << stage;
       if (lane == 0) {
         const bool exists = n < args.N && m0 < args.M;
-        mbar_arrive_expect_tx(res_in, exists ? 2048 : 0);
-        if (exists) tma_load_2d(st, &tmR, res_in, n, m0);
+        mbar_arrive_expect_tx(&res_in[stage], exists ? kLinStage : 0);
+        if (exists) tma_load_2d(st + stage * kLinStage, &tmR, &res_in[stage], n, m0);
       }
     };
-    auto store_stage = [&](const CUtensorMap* map, int n, int m0, bool exists) {
+    auto store_stage = [&](const CUtensorMap* map, int stage, int n, int m0, bool exists) {
       fence_async_smem();
       __syncwarp();
-      if (lane == 0 && exists) {
-        tma_store_2d(map, st, n, m0);
-        bulk_commit();
+      if (lane == 0) {
+        if (exists) tma_store_2d(map, st + stage * kLinStage, n, m0);
+        bulk_commit();  // (an empty group where nothing is stored: the waits count groups)
       }
     };
     const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], 0) : 0, CG == 2 ? map_rank(&acce[1], 0) : 0};
@@ -457,10 +466,11 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
       // the first piece's residual sets out while the products finish, and the other chunks' for L2
       if constexpr (LIN) {
         int c = part + split * half;
-        if (args.res && c * W < bno) {
-          stage_free();
-          load_res(n_tile + c * W, m0);
-          const int size = args.out_f32 ? 4 : 2;
+        if ((EPI & kEpiRes) && c * W < bno) {
+          if (EPI & kEpiZ) turn = 0;
+          stores_read<1>();
+          load_res(turn, n_tile + c * W, m0);
+          const int size = EPI & kEpiF32 ? 4 : 2;
           const uint8_t* r = static_cast<const uint8_t*>(args.res) + (size_t)min(m, args.M - 1) * args.ldo * size;
           while ((c += H * split) * W < bno)
             if (n_tile + c * W < args.N) prefetch_l2(r + (n_tile + c * W) * size);
@@ -514,111 +524,138 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
         __syncwarp();
         cluster_sync();  // the sums have arrived
       }
+      // The linear layer's 32 columns from c on, in halves of 16 (there are 96 registers): y's piece (32 columns
+      // of 16 bits or 16 of fp32) is put into a stage and stored by TMA; the residual's piece comes into that
+      // stage by TMA before, and each lane adds it to its row in place.  Without z the two stages take turns, and
+      // the next piece's residual sets out before this one is worked on; with z, held packed, y has the first
+      // stage and z the second.  False: a wait ran out.
+      [[maybe_unused]] auto lin_chunk = [&](int c) -> bool {
+        constexpr bool RES = EPI & kEpiRes, Z = EPI & kEpiZ, OUT32 = EPI & kEpiF32;
+        const int n0 = n_tile + c * W;
+        const bool exists = n0 < args.N && m0 < args.M;
+        uint4 z[Z ? 4 : 1];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int n = n0 + b * 16;
+          float g[16];
+          tmem_ld16(tb + c * W + b * 16, g);
+          float4 bias[4];
+          [[maybe_unused]] float4 ws[4];  // the same for all lanes, from L1
+          auto fetch = [&](const float* p, float4* v) {
+            if (n + 16 <= args.N) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4*>(p + n + i * 4);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[i] = n + i * 4 < args.N ? *reinterpret_cast<const float4*>(p + n + i * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          };
+          if (args.bias) fetch(args.bias, bias);
+          if constexpr (F8) fetch(args.g_scale, ws);
+          tmem_wait_ld();
+          if (!SPLIT && b == 1 && c == last) hand_back();
+          if constexpr (SPLIT) {
+            for (int k = 0; k < split - 1; ++k) {
+              const uint8_t* from = smem + (k * pieces + c / split) * kPiece + (q * 32 + lane) * 16 + b * 4 * kPart;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 a = *reinterpret_cast<const float4*>(from + i * kPart);
+                g[4 * i] += a.x, g[4 * i + 1] += a.y, g[4 * i + 2] += a.z, g[4 * i + 3] += a.w;
+              }
+            }
+          }
+          auto each2 = [&](const float4* v, auto f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f2_unpack(f(f2_pack(g[4 * i], g[4 * i + 1]), f2_pack(v[i].x, v[i].y)), g[4 * i], g[4 * i + 1]);
+              f2_unpack(f(f2_pack(g[4 * i + 2], g[4 * i + 3]), f2_pack(v[i].z, v[i].w)), g[4 * i + 2], g[4 * i + 3]);
+            }
+          };
+          if constexpr (F8) {
+            const uint64_t sx2 = f2_splat(sx);
+            each2(ws, [&](uint64_t v, uint64_t s) { return f2_mul(v, f2_mul(sx2, s)); });
+          }
+          if (args.bias) each2(bias, [](uint64_t v, uint64_t s) { return f2_add(v, s); });
+          if constexpr (Z) pack16<16>(g, z + b * 2, args.bf16_operands);
+          if (args.act == TFL_ACT_SILU)
+            activate<TFL_ACT_SILU, 16>(g);
+          else if (args.act == TFL_ACT_GELU)
+            activate<TFL_ACT_GELU, 16>(g);
+          const int stage = Z ? 0 : turn;
+          const int next = OUT32 && b == 0 ? n + 16 : c + H * split < chunks ? n0 + H * split * W : -1;
+          if (b == 0 || OUT32) {  // a piece begins: its stage
+            if constexpr (RES) {
+              if (!Z && next >= 0) {  // the other stage's store was the last
+                stores_read<0>();
+                load_res(stage ^ 1, next, m0);
+              }
+              if (!__all_sync(0xffffffffu, wait_bounded(&res_in[stage], (res_phase >> stage) & 1u, wc))) return false;
+              res_flying &= ~(1u << stage);
+              res_phase ^= 1u << stage;
+            } else if (Z && b == 1) {  // the last store was from this stage, in any other case from the other one
+              stores_read<0>();
+            } else {
+              stores_read<1>();
+            }
+          }
+          uint8_t* own = st + stage * kLinStage + lane * 64;
+          auto at = [&](int i) { return reinterpret_cast<uint4*>(own + ((i << 4) ^ swizzle)); };
+          if constexpr (OUT32) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4* s = at(i);
+              if constexpr (RES) {
+                const uint4 r = *s;
+                g[4 * i] += __uint_as_float(r.x), g[4 * i + 1] += __uint_as_float(r.y);
+                g[4 * i + 2] += __uint_as_float(r.z), g[4 * i + 3] += __uint_as_float(r.w);
+              }
+              *s = make_uint4(__float_as_uint(g[4 * i]), __float_as_uint(g[4 * i + 1]), __float_as_uint(g[4 * i + 2]),
+                              __float_as_uint(g[4 * i + 3]));
+            }
+          } else {
+            if constexpr (RES) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float r[8];
+                unpack16(*at(b * 2 + i), r, args.bf16_out);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[8 * i + k] += r[k];
+              }
+            }
+            uint4 w[2];
+            pack16<16>(g, w, args.bf16_out);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) *at(b * 2 + i) = w[i];
+            if (b == 0) continue;
+          }
+          store_stage(&tmA1, stage, OUT32 ? n : n0, m0, exists && (!OUT32 || n < args.N));
+          turn ^= 1;
+          if constexpr (Z) {
+            if (b == 1) {
+              stores_read<1>();
+              own = st + kLinStage + lane * 64;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) *at(i) = z[i];
+              store_stage(&tmB1, 1, n0, m0, exists);
+            }
+            if (RES && next >= 0) {
+              stores_read<0>();
+              load_res(0, next, m0);
+            }
+          }
+        }
+        return true;
+      };
 #pragma unroll 1
       for (int c = part + split * half; c < chunks; c += H * split) {
         const int n0 = n_tile + c * W;                       // first output column
         const int cols = min(args.N - n0, bno - c * W);      // columns of this chunk that exist
         if constexpr (LIN) {
-          // In halves of 16 columns (there are 96 registers): the residual's piece comes into the warp's stage by
-          // TMA, each lane adds it to its row and puts the result in its place, and TMA stores the piece: 32
-          // columns of 16 bits or 16 of fp32.  z, held packed, takes the stage after y.
-          auto at = [&](int i) { return reinterpret_cast<uint4*>(st + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)); };
-          const bool exists = n0 < args.N && m0 < args.M;
-          uint4 z[4];
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int n = n0 + b * 16, cols = args.N - n;
-            float g[16];
-            tmem_ld16(tb + c * W + b * 16, g);
-            float4 bias[4], ws[F8 ? 4 : 1] = {};  // the same for all lanes, from L1
-            auto fetch = [&](const float* p, float4* v) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                v[i] = p && i * 4 < cols ? *reinterpret_cast<const float4*>(p + n + i * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-            };
-            fetch(args.bias, bias);
-            if constexpr (F8) fetch(args.g_scale, ws);
-            tmem_wait_ld();
-            if (!SPLIT && b == 1 && c == last) hand_back();
-            if constexpr (SPLIT) {
-              for (int k = 0; k < split - 1; ++k) {
-                const uint8_t* from = smem + (k * pieces + c / split) * kPiece + (q * 32 + lane) * 16 + b * 4 * kPart;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float4 a = *reinterpret_cast<const float4*>(from + i * kPart);
-                  g[4 * i] += a.x, g[4 * i + 1] += a.y, g[4 * i + 2] += a.z, g[4 * i + 3] += a.w;
-                }
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              auto finish2 = [&](float* v, float s0, float s1, float b0, float b1) {
-                uint64_t w = f2_pack(v[0], v[1]);
-                if constexpr (F8) w = f2_mul(w, f2_mul(f2_splat(sx), f2_pack(s0, s1)));
-                f2_unpack(f2_add(w, f2_pack(b0, b1)), v[0], v[1]);
-              };
-              const float4 s = ws[F8 ? i : 0];
-              finish2(g + 4 * i, s.x, s.y, bias[i].x, bias[i].y);
-              finish2(g + 4 * i + 2, s.z, s.w, bias[i].z, bias[i].w);
-            }
-            if (args.z) pack16<16>(g, z + b * 2, args.bf16_operands);
-            if (args.act == TFL_ACT_SILU)
-              activate<TFL_ACT_SILU, 16>(g);
-            else if (args.act == TFL_ACT_GELU)
-              activate<TFL_ACT_GELU, 16>(g);
-            if (b == 0 || args.out_f32) {  // the stage is this piece's
-              if (args.res) {
-                if (!__all_sync(0xffffffffu, wait_bounded(res_in, res_phase, wc))) {
-                  dead = true;
-                  break;
-                }
-                res_flying = false;
-                res_phase ^= 1u;
-              } else {
-                stage_free();
-              }
-            }
-            if (args.out_f32) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4* s = at(i);
-                if (args.res) {
-                  const uint4 r = *s;
-                  g[4 * i] += __uint_as_float(r.x), g[4 * i + 1] += __uint_as_float(r.y);
-                  g[4 * i + 2] += __uint_as_float(r.z), g[4 * i + 3] += __uint_as_float(r.w);
-                }
-                *s = make_uint4(__float_as_uint(g[4 * i]), __float_as_uint(g[4 * i + 1]), __float_as_uint(g[4 * i + 2]),
-                                __float_as_uint(g[4 * i + 3]));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint4* s = at(b * 2 + i);
-                if (args.res) {
-                  float r[8];
-                  unpack16(*s, r, args.bf16_out);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) g[8 * i + k] += r[k];
-                }
-                pack16<8>(g + 8 * i, s, args.bf16_out);
-              }
-              if (b == 0) continue;
-            }
-            store_stage(&tmA1, args.out_f32 ? n : n0, m0, exists && (!args.out_f32 || n < args.N));
-            if (b == 1 && args.z) {
-              stage_free();
-#pragma unroll
-              for (int i = 0; i < 4; ++i) *at(i) = z[i];
-              store_stage(&tmB1, n0, m0, exists);
-            }
-            // the next piece's residual
-            const int next = args.out_f32 && b == 0 ? n + 16 : c + H * split < chunks ? n0 + H * split * W : -1;
-            if (args.res && next >= 0) {
-              stage_free();
-              load_res(next, m0);
-            }
+          if (!lin_chunk(c)) {
+            dead = true;
+            break;
           }
-          if (dead) break;
         } else {
           uint4 o[W / 8], o2[W / 8];
           if constexpr (MODE == GLU_SLOPES)
@@ -705,8 +742,9 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     if constexpr (LIN) {
       // nothing may land in or be read from this CTA's shared memory once it is gone
       const WaitCtl dc{args.status, never_flag, 100000000LL};
-      if (res_flying) wait_bounded(res_in, res_phase, dc);
-      if (lane == 0) bulk_wait<0>();
+      for (int s = 0; s < 2; ++s)
+        if (res_flying & (1u << s)) wait_bounded(&res_in[s], (res_phase >> s) & 1u, dc);
+      stores_read<0>();
     }
   }
 
@@ -735,7 +773,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   }
 }
 
-template <int CG, int MODE, bool F8, int FORM>
+template <int CG, int MODE, bool F8, int FORM, int EPI = 0>
 cudaError_t launch_one(const TileMaps& mp, TileArgs a, const TilePlan& p, cudaStream_t s) {
   a.bno = p.bno;
   a.split = p.split;
@@ -759,12 +797,12 @@ cudaError_t launch_one(const TileMaps& mp, TileArgs a, const TilePlan& p, cudaSt
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster == 1 ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, tile_kernel<CG, MODE, F8, FORM>, mp.a0, mp.a1, mp.b0, mp.b1, mp.r, a);
+  return cudaLaunchKernelEx(&cfg, tile_kernel<CG, MODE, F8, FORM, EPI>, mp.a0, mp.a1, mp.b0, mp.b1, mp.r, a);
 }
 
-template <int CG, int MODE, bool F8, int FORM>
+template <int CG, int MODE, bool F8, int FORM, int EPI = 0>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(tile_kernel<CG, MODE, F8, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
+  return cudaFuncSetAttribute(tile_kernel<CG, MODE, F8, FORM, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileSmem);
 }
 
 // Clusters of `size` CTAs that the GPU holds at once, one CTA an SM (a cluster stays within a GPU
@@ -781,7 +819,7 @@ cudaError_t clusters_at_once(int size, int* n) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(n, tile_kernel<CG, GLU_FORWARD, false, FORM>, &cfg);
+  return cudaOccupancyMaxActiveClusters(n, tile_kernel<CG, GLU_FORWARD, false, FORM, 0>, &cfg);
 }
 
 }  // namespace
