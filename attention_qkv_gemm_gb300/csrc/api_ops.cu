@@ -746,6 +746,11 @@ int check_tokens(const tfl_linear* l, int64_t tokens) {
   return TFL_OK;
 }
 
+// Row blocks of a group of tiles: a wave of 76 tiles of 256 x 256 touches the fewest operands as 8 or 9 of each;
+// where all columns of the output are fewer tiles than that they go first, so that no row block is left to
+// another wave (100000 x 4096 x 1024 bf16 read 1.8 GB instead of 1.3).
+int tile_group(const TilePlan& p, int64_t cols) { return (cols + p.bno - 1) / p.bno <= 8 ? 1 : 8; }
+
 TileArgs linear_args(const tfl_linear* l) {
   TileArgs a;
   a.act = l->act;
@@ -878,6 +883,7 @@ int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float
   a.bias = bias;
   a.res = res;
   a.z = z != nullptr;
+  a.group_m = tile_group(p, l->N);
   a.ldo = l->N;
   TFL_CUDA(launch_linear(p, f8, mp, a, st), "linear layer");
   return TFL_OK;
@@ -952,6 +958,7 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     a.M = Ti;
     a.N = Ki;
     a.num_k = a.k_half = kn;
+    a.group_m = tile_group(p1, Ki);
     a.ldo = Ki;
     a.out = static_cast<uint16_t*>(dx);
     TFL_CUDA(launch_tiles(p1, GRAD_DX, false, m1, a, st), "linear layer dx");
@@ -961,6 +968,7 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     a.N = Ki;
     a.num_k = kt;
     a.planes = 1;
+    a.group_m = tile_group(p2, Ki);
     a.ldo = Ki;
     a.out = static_cast<uint16_t*>(dw);
     TFL_CUDA(launch_tiles(p2, GRAD_DW, false, m2, a, st), "linear layer weight gradient");

@@ -92,11 +92,23 @@ enum TileMode : int {
   GRAD_DW = 3,      // out[M, N] = A0^T B0, out2[M, N] = A1^T B0, the second for the feed-forward only
   LIN_FORWARD = 4,  // z[M, N] = A B0^T + bias, out[M, N] = act(z) + res
 };
+// A divisor of tile numbers, with what stands in for the division (tile_gemm.cuh).
+struct Divisor {
+  int d = 1, shift = -1;
+  uint32_t factor = 0;
+};
+// The order of tiles: planes of tiles, groups of `rows` row blocks in them.
+struct TileOrder {
+  int num_m = 0;
+  Divisor plane, group, rows, last_rows;
+};
 struct TileArgs {
   int M = 0, N = 0;              // rows and columns of the output
   int num_k = 0;                 // k-blocks of a tile
   int k_half = 0;                // DX: k-blocks of the first product
   int planes = 2;                // DW: outputs
+  int group_m = 8;               // row blocks of a group of tiles
+  TileOrder order;               // set by the launcher
   int bno = 0, split = 1, stages = 0, stage_bytes = 0, a_bytes = 0;  // set by the launcher from the plan
   int act = 0;
   int bf16_operands = 0;         // 16-bit operands: bf16, else fp16

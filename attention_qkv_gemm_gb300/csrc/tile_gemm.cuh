@@ -80,14 +80,34 @@ __device__ __forceinline__ void forward_values(float* g, const float* u) {
     f2_unpack(f2_mul(a, f2_pack(u[i], u[i + 1])), g[i], g[i + 1]);
   }
 }
-// g <- act(g)
+// g <- act(g).  GELU as gelu2_as7126 folds it, max(g, 0) - |g| erfc / 2, with |g| held below 1e4 so that an
+// infinity's product with erfc = 0 is 0 (a NaN reaches erfc): three instructions a value fewer than act2's.
 template <int ACT, int N>
 __device__ __forceinline__ void activate(float* g) {
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    uint64_t a, unused;
-    act2<ACT, false>(f2_pack(g[i], g[i + 1]), a, unused);
-    f2_unpack(a, g[i], g[i + 1]);
+    const uint64_t x = f2_pack(g[i], g[i + 1]);
+    if constexpr (ACT == TFL_ACT_GELU) {
+      constexpr float p_s = 0.3275911f * 0.7071067811865476f;
+      constexpr float h1 = 0.5f * 0.254829592f, h2 = 0.5f * -0.284496736f, h3 = 0.5f * 1.421413741f,
+                      h4 = 0.5f * -1.453152027f, h5 = 0.5f * 1.061405429f;
+      const uint64_t size = f2_pack(fminf(fabsf(g[i]), 1e4f), fminf(fabsf(g[i + 1]), 1e4f));
+      float d0, d1;
+      f2_unpack(f2_fma(size, f2_splat(p_s), f2_splat(1.0f)), d0, d1);
+      const uint64_t t = f2_pack(rcp_approx(d0), rcp_approx(d1));
+      // minus the polynomial, so that the last product is an addition
+      uint64_t poly = f2_fma(f2_splat(-h5), t, f2_splat(-h4));
+      poly = f2_fma(poly, t, f2_splat(-h3));
+      poly = f2_fma(poly, t, f2_splat(-h2));
+      poly = f2_fma(poly, t, f2_splat(-h1));
+      f2_unpack(f2_mul(f2_mul(x, x), f2_splat(-0.7213475204444817f)), d0, d1);
+      const uint64_t erfc = f2_mul(f2_mul(t, poly), f2_pack(ex2(d0), ex2(d1)));
+      f2_unpack(f2_fma(size, erfc, f2_pack(fmaxf(g[i], 0.f), fmaxf(g[i + 1], 0.f))), g[i], g[i + 1]);
+    } else {
+      uint64_t a, unused;
+      act2<ACT, false>(x, a, unused);
+      f2_unpack(a, g[i], g[i + 1]);
+    }
   }
 }
 // g <- dh u act'(g), u <- dh act(g).
@@ -183,19 +203,22 @@ struct Tile {
   int m, n, z;
 };
 
-// Tiles in groups of kGroupM row blocks, column by column inside a group, so that the tiles in
-// flight share operands through L2.  DW: first all of dWg, then all of dWu.
-constexpr int kGroupM = 8;
-__device__ __forceinline__ Tile tile_at(int t, int num_m, int num_n, int group_m) {
+// Tiles in groups of row blocks, column by column inside a group, so that the tiles in flight share
+// operands through L2.  DW: first all of dWg, then all of dWu.
+// n / d for n < 2^31 by a multiplication with ceil(2^(31 + s) / d), s = ceil(log2 d) (the round-up method of
+// Granlund and Montgomery): every warp finds every tile, and three divisions a tile cost it some 400 cycles.
+__device__ __forceinline__ int over(int n, const Divisor& d) {
+  return d.shift < 0 ? n : (int)(__umulhi((uint32_t)n, d.factor) >> d.shift);
+}
+__device__ __forceinline__ Tile tile_at(int t, const TileOrder& o) {
   Tile r;
-  const int per = num_m * num_n;
-  r.z = t / per;
-  t -= r.z * per;
-  const int g = t / (group_m * num_n), first = g * group_m;
-  const int gm = min(num_m - first, group_m);
-  t -= g * group_m * num_n;
-  r.n = t / gm;
-  r.m = first + t - r.n * gm;
+  r.z = over(t, o.plane);
+  t -= r.z * o.plane.d;
+  const int g = over(t, o.group), first = g * o.rows.d;
+  t -= g * o.group.d;
+  const bool whole = o.num_m - first >= o.rows.d;  // the last group of a plane may have fewer row blocks
+  r.n = over(t, whole ? o.rows : o.last_rows);
+  r.m = first + t - r.n * (whole ? o.rows.d : o.last_rows.d);
   return r;
 }
 
@@ -271,7 +294,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   if constexpr ((MODE == GLU_FORWARD || LIN) && CG == 1) {
     if (threadIdx.x == 64) {
       const int n = SPLIT ? args.split : 1, part = SPLIT ? (int)cluster_rank() : 0;
-      const Tile tl = tile_at(blockIdx.x / n, (args.M + kTileRows - 1) / kTileRows, (args.N + bno - 1) / bno, kGroupM);
+      const Tile tl = tile_at(blockIdx.x / n, args.order);
       const int kb = args.num_k * part / n, end = min(kb + stages, args.num_k * (part + 1) / n);
       for (int k = kb; k < end; ++k) {
         tma_prefetch_2d(&tmB0, k * KE, tl.n * bno);
@@ -288,8 +311,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   const WaitCtl wc{args.status, abort_flag, args.timeout_ns};
   grid_wait_prior();  // everything below reads or writes what earlier kernels use
 
-  const int num_m = (args.M + kTileRows * CG - 1) / (kTileRows * CG), num_n = (args.N + bno - 1) / bno;
-  const int total = num_m * num_n * (MODE == GRAD_DW ? args.planes : 1);
+  const int total = args.order.plane.d * (MODE == GRAD_DW ? args.planes : 1);
   const int split = SPLIT ? args.split : 1, part = SPLIT ? (int)cluster_rank() : 0;
   const int unit = blockIdx.x / (CG * split), units = gridDim.x / (CG * split);
   const int kb0 = args.num_k * part / split, kb1 = args.num_k * (part + 1) / split;  // this CTA's k-blocks
@@ -304,7 +326,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = tile_at(t, num_m, num_n, kGroupM);
+        const Tile tl = tile_at(t, args.order);
         const int m0 = (tl.m * CG + rank) * kTileRows;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
@@ -427,6 +449,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     uint32_t res_phase = 0, res_flying = 0;      // a bit a stage
     int turn = 0;
     bool dead = false;
+    float warm[F8 ? 4 : 2] = {};
     auto load_res = [&](int stage, int n, int m0) {
       res_flying |= 1u << stage;
       if (lane == 0) {
@@ -445,7 +468,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     };
     const uint32_t acce_addr[2] = {CG == 2 ? map_rank(&acce[0], 0) : 0, CG == 2 ? map_rank(&acce[1], 0) : 0};
     for (int t = unit; t < total; t += units) {
-      const Tile tl = tile_at(t, num_m, num_n, kGroupM);
+      const Tile tl = tile_at(t, args.order);
       const int m0 = (tl.m * CG + rank) * kTileRows + q * 32, m = m0 + lane;
       const uint32_t rows = __ballot_sync(0xffffffffu, m < args.M);
       const int n_tile = tl.n * bno;  // first output column of the tile
@@ -462,6 +485,21 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
       if constexpr (F8) {
         sx = m < args.M ? args.x_scale[m] : 0.f;  // written by the kernel before this one: a plain load
         fetch_scales(part + split * half);
+      }
+      // The lines of the next tile's bias and scales into L1 (from L2 they came some 700 cycles late, twice a
+      // tile); the loads' results are taken, for nothing, a tile later, when they have long arrived.
+      if constexpr (LIN) {
+#pragma unroll
+        for (float& v : warm) asm volatile("" ::"f"(v));
+        const int n = t + units < total ? tile_at(t + units, args.order).n * bno + lane : args.N;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int col = n + (part + split * (half + i * H)) * W;
+          if (col < args.N) {
+            if (args.bias) warm[i] = args.bias[col];
+            if constexpr (F8) warm[2 + i] = args.g_scale[col];
+          }
+        }
       }
       // the first piece's residual sets out while the products finish, and the other chunks' for L2
       if constexpr (LIN) {
@@ -773,10 +811,28 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   }
 }
 
+Divisor divisor(int d) {
+  Divisor r;
+  r.d = d;
+  if (d == 1) return r;  // shift -1
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  r.factor = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  r.shift = s - 1;
+  return r;
+}
+
 template <int CG, int MODE, bool F8, int FORM, int EPI = 0>
 cudaError_t launch_one(const TileMaps& mp, TileArgs a, const TilePlan& p, cudaStream_t s) {
   a.bno = p.bno;
   a.split = p.split;
+  const int num_m = (a.M + kTileRows * CG - 1) / (kTileRows * CG), num_n = (a.N + p.bno - 1) / p.bno;
+  const int group = a.group_m < num_m ? a.group_m : num_m;
+  a.order.num_m = num_m;
+  a.order.plane = divisor(num_m * num_n);
+  a.order.group = divisor(group * num_n);
+  a.order.rows = divisor(group);
+  a.order.last_rows = divisor(num_m % group ? num_m % group : group);
   const int bn = (MODE == GLU_FORWARD || MODE == GLU_SLOPES) ? 2 * p.bno : p.bno;
   const bool b_mn = MODE == GRAD_DX || MODE == GRAD_DW;
   a.a_bytes = p.a_rows * kKBytes;
