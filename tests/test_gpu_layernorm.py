@@ -323,12 +323,43 @@ def test_wide_rows_over_several_turns(rows, d):
     _check_backward(rows, d, "bf16", "f32", _backward(rows, d, "bf16", "f32", seed=d))
 
 
+# rows that begin inside a 16-byte vector: every shift, widths around those where the thread groups change, one
+# row a group and several turns of the blocks
+@pytest.mark.parametrize("d", [9, 10, 12, 15, 17, 250, 1001, 1002, 1004, 2033, 2034, 2035, 4081, 4082, 4083])
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+def test_backward_of_rows_that_begin_inside_a_vector(d, xt, rt):
+    for rows in (1, 2, 7, 9, 160, 6007 if d < 2000 else 1501, 40009 if d < 20 else 303):
+        _check_backward(rows, d, xt, rt, _backward(rows, d, xt, rt, with_beta=rows != 9, seed=rows + d))
+
+
+@pytest.mark.parametrize("rows,d", [(30, 9), (6011, 1001), (700, 1002), (40, 4081), (6011, 1000), (30, 4099)])
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16")])
+def test_backward_keeps_rows_without_numbers_to_themselves(rows, d, xt, rt):
+    import torch
+    pkg = _pkg()
+    s, stats, dy, dres, gamma, dx, dsum, _, _ = _backward(rows, d, xt, rt, seed=2)
+    bad = sorted({1, rows // 2, rows - 2})
+    s2, dy2, dres2 = s.clone(), dy.clone(), dres.clone()
+    s2[bad[0]], dy2[bad[1]], dres2[bad[2]] = float("nan"), float("inf"), float("nan")
+    dx2, dsum2, g, b = torch.empty_like(dx), torch.empty_like(s), torch.empty_like(gamma), torch.empty_like(gamma)
+    h = pkg.tfl_layernorm_create(d, _code(xt), _code(rt), _code(xt), EPS)
+    pkg.tfl_layernorm_backward(h, rows, s2.data_ptr(), stats.data_ptr(), gamma.data_ptr(), dy2.data_ptr(), dres2.data_ptr(),
+                               dx2.data_ptr(), dsum2.data_ptr() if xt != rt else None, g.data_ptr(), b.data_ptr(), _stream())
+    torch.cuda.synchronize()
+    pkg.tfl_layernorm_destroy(h)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    assert torch.equal(dx2[keep], dx[keep]) and not dx2[bad].isfinite().all(dim=1).any()
+    if xt != rt:
+        assert torch.equal(dsum2[keep], dsum[keep])
+
+
 BUFFERS = ("sum", "gamma", "dy", "dres", "dx", "dsum", "dgamma", "dbeta")
 
 
 # each buffer alone one element past its alignment, then all
 @pytest.mark.parametrize("which", [(b,) for b in BUFFERS] + [BUFFERS])
-@pytest.mark.parametrize("rows,d", [(1, 512), (3, 8), (333, 1024), (40, 8192), (700, 16384)])
+@pytest.mark.parametrize("rows,d", [(1, 512), (3, 8), (333, 1024), (333, 1002), (40, 8192), (700, 16384)])
 def test_backward_of_unaligned_buffers(rows, d, which):
     import torch
     pkg = _pkg()
@@ -393,7 +424,7 @@ def test_backward_gives_the_same_bits_every_time_and_in_place():
     import torch
     pkg = _pkg()
     P = lambda t: t.data_ptr()  # noqa: E731
-    for d in (512, 513):
+    for d in (512, 513, 516):
         s, stats, dy, dres, gamma, dx, _, dgamma, dbeta = _backward(3000, d, "bf16", "bf16", both=False, seed=4)
         again = _backward(3000, d, "bf16", "bf16", both=False, seed=4)
         assert torch.equal(dx, again[5]) and torch.equal(dgamma, again[7]) and torch.equal(dbeta, again[8])
