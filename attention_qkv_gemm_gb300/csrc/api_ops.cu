@@ -849,7 +849,7 @@ int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float
   if (bad) return fail(TFL_ERR_INVALID_ARG, "an output overlaps another buffer");
   if (int rc = same_device(l->device)) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (lin_few_fits(tokens, (int64_t)l->K * (int64_t)es)) {
+  if (lin_few_fits(tokens, (int64_t)l->K * (int64_t)es, l->N, f8, l->units.sms)) {
     LinFewArgs a;
     a.tokens = (int)tokens;
     a.d_out = l->N;
@@ -986,7 +986,7 @@ int tfl_selftest_linear_plan(int32_t d_in, int32_t d_out, int32_t in_type, int32
   TileUnits u;
   if (int rc = selftest_units(units, &u)) return rc;
   for (int i = 0; i < 4; ++i) out[i] = 0;
-  if (part == LIN_PART_FORWARD && lin_few_fits(tokens, (int64_t)d_in * (f8 ? 1 : 2))) return TFL_OK;
+  if (part == LIN_PART_FORWARD && lin_few_fits(tokens, (int64_t)d_in * (f8 ? 1 : 2), d_out, f8, u.sms)) return TFL_OK;
   const int mode = part == LIN_PART_FORWARD ? LIN_FORWARD : part == LIN_PART_DX ? GRAD_DX : GRAD_DW;
   tell_plan(linear_call_plan(d_in, d_out, f8, part, tokens, u), mode, out);
   return TFL_OK;

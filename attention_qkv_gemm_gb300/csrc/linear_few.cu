@@ -42,8 +42,8 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 // flight a warp, 512 G bytes of weights each; LINES: 128-byte lines of them, a row and warp, that are
 // prefetched.
 template <int TYPE, int NT, int G, int U, int LINES>
-__global__ void __launch_bounds__(256) lin_few_kernel(const LinFewArgs a) {
-  __shared__ float red[8][G * 4][32];
+__global__ void __launch_bounds__(512) lin_few_kernel(const LinFewArgs a) {
+  __shared__ float red[16][G * 4][32];
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -130,29 +130,53 @@ __global__ void __launch_bounds__(256) lin_few_kernel(const LinFewArgs a) {
   }
 }
 
-// Warps a block (they split k): as few as still give every SM 24 warps, no more than a row feeds.
-int few_warps(const LinFewArgs& a, int g, int u, int num_sms) {
-  int warps = 2;
-  while (warps < 8 && warps * u * 64 < a.row_bytes && (int64_t)(a.d_out / (8 * g)) * warps < (int64_t)num_sms * 24) warps *= 2;
-  return warps;
+template <int TYPE, int NT, int G, int U, int LINES>
+cudaError_t launch_form(const LinFewArgs& a, int warps, cudaStream_t s) {
+  return launch_dependent(lin_few_kernel<TYPE, NT, G, U, LINES>, (a.d_out + 8 * G - 1) / (8 * G), warps * 32, 0, s, a);
 }
 
-template <int TYPE, int NT, int G, int U, int LINES>
-cudaError_t launch_form(const LinFewArgs& a, int num_sms, cudaStream_t s) {
-  return launch_dependent(lin_few_kernel<TYPE, NT, G, U, LINES>, (a.d_out + 8 * G - 1) / (8 * G),
-                          few_warps(a, G, U, num_sms) * 32, 0, s, a);
+// A warp loads all its steps, then multiplies: so a row in one turn of a block's warps (up to sixteen, four
+// steps each; two turns of 8 KB rows), 8 columns a block where the GPU holds all blocks at once and 16 where
+// it does not: a second wave of blocks costs more than their loads (one token x 2048 x 8192 bf16, 1024 blocks of
+// sixteen warps 11.5 us, 512 of them 7.0).
+struct FewForm {
+  int g = 0, warps = 0;  // column groups of a block; 0: none fits
+};
+FewForm few_form(int64_t row_bytes, int64_t d_out, int num_sms) {
+  int w = 1;
+  while (w < 16 && w * 256 < row_bytes) w *= 2;
+  // columns the GPU holds at once: `regs` registers a thread
+  auto wave = [&](int g, int warps, int regs) {
+    const int by_registers = 65536 / (regs * warps * 32), by_warps = 64 / warps, most = by_registers < by_warps ? by_registers : by_warps;
+    return (int64_t)num_sms * (most < 32 ? most : 32) * 8 * g;
+  };
+  if (d_out <= wave(1, w, 40)) return {1, w};
+  if (d_out <= wave(2, w, 60)) return {2, w};
+  if (w > 1 && d_out <= wave(2, w / 2, 60)) return {2, w / 2};
+  return {};
+}
+
+template <int TYPE, int NT>
+cudaError_t launch_tokens(const LinFewArgs& a, int num_sms, cudaStream_t s) {
+  const FewForm f = few_form(a.row_bytes, a.d_out, num_sms);
+  if (f.g == 1) return launch_dependent(lin_few_kernel<TYPE, NT, 1, 4, 2>, a.d_out / 8, f.warps * 32, 0, s, a);
+  return launch_dependent(lin_few_kernel<TYPE, NT, 2, 4, 2>, (a.d_out + 15) / 16, f.warps * 32, 0, s, a);
 }
 
 template <int TYPE>
 cudaError_t launch_type(const LinFewArgs& a, int num_sms, cudaStream_t s) {
-  if (a.tokens > 8) return launch_form<TYPE, 2, 1, 4, 2>(a, num_sms, s);
-  return launch_form<TYPE, 1, 1, 8, 4>(a, num_sms, s);
+  return a.tokens > 8 ? launch_tokens<TYPE, 2>(a, num_sms, s) : launch_tokens<TYPE, 1>(a, num_sms, s);
 }
 
 }  // namespace
 
-bool lin_few_fits(int64_t tokens, int64_t row_bytes) {
-  return (tokens <= 8 && row_bytes <= 16 * 1024) || (tokens <= kLinFewTokens && tokens * row_bytes <= 32 * 1024);
+// Against the tiled kernel (in graphs): 8 tokens x 1024 x 4096 bf16 3.6 against 6.2 us, 16 x 4096 x 4096 8.1
+// against 9.8, but rows of 16 KB or weights that take a second wave of blocks are the tiled kernel's (8 x 8192 x
+// 512 8.5 against 7.8, 8 x 4096 x 16384 27.7 against 23.1), and e4m3 weights past 16 MB with two groups of tokens
+// (16 x 8192 x 4096 12.3 against 10.0).
+bool lin_few_fits(int64_t tokens, int64_t row_bytes, int64_t d_out, bool f8, int num_sms) {
+  if (tokens > kLinFewTokens || row_bytes > 8192 || (f8 && tokens > 8 && row_bytes * d_out > (16 << 20))) return false;
+  return few_form(row_bytes, d_out, num_sms).g != 0;
 }
 
 cudaError_t launch_lin_few(int type, const LinFewArgs& a, int num_sms, cudaStream_t s) {

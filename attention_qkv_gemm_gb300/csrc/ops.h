@@ -186,7 +186,8 @@ struct LinFewArgs {
   uint16_t* z = nullptr;
   void* out = nullptr;
 };
-bool lin_few_fits(int64_t tokens, int64_t row_bytes);  // whether this kernel is the faster one
+// Whether this kernel is the faster one.
+bool lin_few_fits(int64_t tokens, int64_t row_bytes, int64_t d_out, bool f8, int num_sms);
 cudaError_t launch_lin_few(int type, const LinFewArgs& a, int num_sms, cudaStream_t s);
 
 // The linear layer's dz = dy act'(z) and the sums of its columns (linear.cu).
