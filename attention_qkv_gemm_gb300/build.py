@@ -26,7 +26,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxe
          "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["gemm.cu", "attention.cu", "attention_bwd.cu", "postchain.cu", "stack.cu", "rows.cu", "rmsnorm.cu",
            "layernorm.cu", "glu.cu", "glu_few.cu", "linear.cu", "linear_few.cu",
-           "linear_wide.cu", "linear_pair.cu", "linear_lone.cu", "linear_shared.cu", "api.cu", "api_ops.cu"]
+           "linear_wide.cu", "linear_pair.cu", "linear_lone.cu", "linear_shared.cu", "linear_shares.cu", "api.cu", "api_ops.cu"]
 
 # The attention kernels that run two CTAs of 256 threads per SM move registers from their first
 # warpgroup to the second with setmaxnreg (64 and 192 a thread).  That balances only when the

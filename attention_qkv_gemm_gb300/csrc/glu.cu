@@ -79,13 +79,13 @@ cudaError_t prepare_tile_kernels(TileUnits* u) {
 // So wide tiles where there are rounds of them, narrower ones where that fills a last round or
 // spreads the weights of a few rows over all SMs, and shared k-blocks where the tiles are few and
 // the rows long (60 tokens x 2048 x 8192 backward: 110 -> 55 us, most of it dx).
-TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const TileUnits& u, int planes) {
+TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const TileUnits& u, int planes,
+                   int shares) {
   const bool two = mode == GLU_FORWARD || mode == GLU_SLOPES;
-  const int64_t twice = mode == GRAD_DW ? planes : 1;
-  const double memory = (double)(M * twice + (two ? 2 : 1) * N) * num_k * kKBytes / 3800.0;
+  const int64_t twice = mode == GRAD_DW ? planes * shares : 1;
+  const double memory = (double)(M * twice + (two ? 2 : 1) * shares * N) * num_k * kKBytes / 3800.0;
   TilePlan best;
-  double best_cost = 0;
-  for (int form = 0; form < 5; ++form) {  // pairs; lone CTAs; clusters of 2, 4, 8 lone CTAs
+  for (int form = 0; form < (shares > 1 ? 2 : 5); ++form) {  // pairs; lone CTAs; clusters of 2, 4, 8 lone CTAs
     const int cg = form == 0 ? 2 : 1, split = form < 2 ? 1 : 1 << (form - 1);
     if ((cg == 2 && M <= kTileRows) || (split > 1 && num_k < 2 * split)) continue;
     const int64_t units = form == 0 ? u.pairs : form == 1 ? u.sms : u.splits[form - 2];
@@ -115,14 +115,14 @@ TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num
       double cost = (rounds - 1) * (full + 600.0) + round(last) + 600.0 + 1200.0 * turns;
       if (cg == 2) cost += 1950.0;
       if (split > 1) cost += 1100.0 + (double)rows * bn * 4 * (split - 1) / split / 11.0;
-      if (!best.cg || cost < best_cost * 0.98) {
+      if (!best.cg || cost < best.cost * 0.98) {
         best.cg = cg;
         best.split = split;
         best.a_rows = M < kTileRows && mode != GRAD_DW ? (int)((M + 7) / 8 * 8) : kTileRows;
         best.bno = bno;
         best.units = (int)units;
         best.tiles = tiles;
-        best_cost = cost;
+        best.cost = cost;
       }
     }
   }

@@ -8,7 +8,8 @@
 //
 // Backward, with dz = dy act'(z):
 //   dx = dz W       GRAD_DX of the same kernel, W read as [k, n] (MN-major)
-//   dW = dz^T x     GRAD_DW, a sum over the tokens, both operands MN-major
+//   dW = dz^T x     GRAD_DW, a sum over the tokens, both operands MN-major; where the outputs are few tiles, over
+//                   shares of the tokens (linear_shares.cu)
 //   db = sum dz     and dz itself, in one pass over dy and z; fp32 sums of the unrounded dz
 // dz is rounded to the operands' type, which the tensor cores take.  Without an activation and with dy of
 // that type it is dy, and the pass only adds up its columns.
@@ -22,6 +23,7 @@ cudaError_t prepare_linear_kernels() {
   cudaError_t e = prepare_linear_wide();
   if (e == cudaSuccess) e = prepare_linear_pair();
   if (e == cudaSuccess) e = prepare_linear_lone();
+  if (e == cudaSuccess) e = prepare_linear_shares();
   return e == cudaSuccess ? prepare_linear_shared() : e;
 }
 
@@ -117,8 +119,11 @@ cudaError_t slopes(LinSlopeArgs a, int num_sms, cudaStream_t s) {
   a.tx = pow2_at_least(a.cols / 8);
   if (a.tx > 32) a.tx = 32;
   const int64_t slabs = (a.cols / 8 + a.tx - 1) / a.tx, ys = 256 / a.tx, turns = (a.rows + ys - 1) / ys;
-  int64_t n = ((int64_t)num_sms * 8 + slabs - 1) / slabs;  // blocks of a slab
-  if (n > turns) n = turns;
+  // Blocks of a slab: four an SM, with rows for a few turns each (2957 x 672 fp16 GELU in 1110 blocks of one turn
+  // 12.9 us, in 279 6.3), but no fewer than two an SM that have rows at all (204 x 336 in 84 blocks 6.2, in 324 4.8).
+  int64_t n = ((int64_t)num_sms * 4 + slabs - 1) / slabs;
+  const int64_t few = (turns + 3) / 4, fill = ((int64_t)num_sms * 2 + slabs - 1) / slabs;
+  if (n > few) n = few > fill ? few : fill < turns ? fill : turns;
   if (n > a.blocks) n = a.blocks;
   if (n > 65535) n = 65535;
   const bool lone = n == 1;

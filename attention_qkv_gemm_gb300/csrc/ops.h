@@ -106,7 +106,7 @@ struct TileArgs {
   int M = 0, N = 0;              // rows and columns of the output
   int num_k = 0;                 // k-blocks of a tile
   int k_half = 0;                // DX: k-blocks of the first product
-  int planes = 2;                // DW: outputs
+  int planes = 2;                // DW: outputs, or shares of the tokens
   int group_m = 8;               // row blocks of a group of tiles
   TileOrder order;               // set by the launcher
   int bno = 0, split = 1, stages = 0, stage_bytes = 0, a_bytes = 0;  // set by the launcher from the plan
@@ -136,13 +136,16 @@ struct TileMaps {
 struct TilePlan {
   int cg = 0, split = 1, bno = 0, units = 0, a_rows = 0;
   int64_t tiles = 0;
+  double cost = 0;  // the estimate it was chosen by, in cycles
 };
 // What runs at once on a device: lone CTAs, CTA pairs, and clusters of 2, 4 and 8 lone CTAs.
 struct TileUnits {
   int sms = 0, pairs = 0, splits[3] = {};
 };
-// whole_lines: the rows of x and the weights begin on 128-byte lines.  planes: GRAD_DW's outputs.
-TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const TileUnits& u, int planes = 2);
+// whole_lines: the rows of x and the weights begin on 128-byte lines.  planes: GRAD_DW's outputs; shares: of the
+// tokens, of num_k k-blocks each (no tile is then shared by a cluster).
+TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num_k, const TileUnits& u, int planes = 2,
+                   int shares = 1);
 int tile_form(const TilePlan& p, int mode);  // TFL_GLU_FORM_* of the kernel it runs in
 // Kernel attributes, and all of *u but sms for the current device.
 cudaError_t prepare_tile_kernels(TileUnits* u);
@@ -150,6 +153,10 @@ cudaError_t prepare_linear_kernels();
 // All modes but LIN_FORWARD, and that one.
 cudaError_t launch_tiles(const TilePlan& p, int mode, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
 cudaError_t launch_linear(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
+// GRAD_DW over shares of the tokens into fp32 partial sums [planes, M, N], and their sum in 16 bits.
+cudaError_t prepare_linear_shares();
+cudaError_t launch_linear_shares(const TilePlan& p, const TileMaps& mp, const TileArgs& a, cudaStream_t s);
+cudaError_t launch_share_sums(const float* parts, int shares, int64_t values, bool bf16, uint16_t* out, cudaStream_t s);
 #define TFL_DECLARE_LINEAR_FORM(NAME)   \
   cudaError_t prepare_linear_##NAME();  \
   cudaError_t launch_linear_##NAME(const TilePlan& p, bool f8, const TileMaps& mp, const TileArgs& a, cudaStream_t s);

@@ -165,7 +165,26 @@ __device__ __forceinline__ void store_cols(uint8_t* st, int lane, const uint4* v
   }
   __syncwarp();
 }
-// The same way back: this thread's row of W 16-bit columns (zeros outside).
+// The same for 16 fp32 columns (32 rows of 64 bytes: a warp's whole stage).
+__device__ __forceinline__ void store_cols_f32(uint8_t* st, int lane, const float* v, float* row0, size_t pitch,
+                                               uint32_t rows, int cols) {
+  using X = XStage<64>;
+  uint4 w[4];
+  pack_f32x16(v, w);
+  X::put_row(st, lane, w);
+  __syncwarp();
+  const int q = lane % X::CPR;
+  uint4 o[X::CPR];
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k) o[k] = *reinterpret_cast<const uint4*>(st + X::off(X::RPI * k + lane / X::CPR, q));
+#pragma unroll
+  for (int k = 0; k < X::CPR; ++k) {
+    const int i = X::RPI * k + lane / X::CPR;
+    if (((rows >> i) & 1u) && q * 4 < cols) *reinterpret_cast<uint4*>(row0 + (size_t)i * pitch + q * 4) = o[k];
+  }
+  __syncwarp();
+}
+// The 16-bit columns the same way back: this thread's row of W 16-bit columns (zeros outside).
 template <int W>
 __device__ __forceinline__ void load_cols(uint8_t* st, int lane, uint4* v, const uint16_t* row0, size_t pitch,
                                           uint32_t rows, int cols) {
@@ -233,7 +252,8 @@ enum TileForm : int { kWide = 0, kNarrow = 1, kSplit = 2 };
 // and have the registers for it).  Eight for the narrow tiles, most of which have one or two chunks.
 __host__ __device__ constexpr int epi_warps(int form, bool lin) { return form == kWide || lin ? 16 : 8; }
 __host__ __device__ constexpr int tile_threads(int form, int mode) { return 64 + 32 * epi_warps(form, mode == LIN_FORWARD); }
-// EPI: what the linear layer's epilogue does besides bias and activation.
+// EPI: what the linear layer's epilogue does besides bias and activation.  GRAD_DW with kEpiF32: the planes are
+// shares of the tokens, each with fp32 sums of its own.
 enum EpiBits : int { kEpiF32 = 1, kEpiZ = 2, kEpiRes = 4 };  // y (and the residual) fp32; z stored; residual added
 template <int CG, int MODE, bool F8, int FORM, int EPI>
 __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
@@ -314,7 +334,14 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   const int total = args.order.plane.d * (MODE == GRAD_DW ? args.planes : 1);
   const int split = SPLIT ? args.split : 1, part = SPLIT ? (int)cluster_rank() : 0;
   const int unit = blockIdx.x / (CG * split), units = gridDim.x / (CG * split);
-  const int kb0 = args.num_k * part / split, kb1 = args.num_k * (part + 1) / split;  // this CTA's k-blocks
+  // This CTA's k-blocks of a tile: all, its share of a shared tile, or a plane's share of the tokens.
+  constexpr bool CHUNKS = MODE == GRAD_DW && (EPI & kEpiF32);
+  auto k_begin = [&](const Tile& tl) {
+    return CHUNKS ? (int)((int64_t)args.num_k * tl.z / args.planes) : args.num_k * part / split;
+  };
+  auto k_end = [&](const Tile& tl) {
+    return CHUNKS ? (int)((int64_t)args.num_k * (tl.z + 1) / args.planes) : args.num_k * (part + 1) / split;
+  };
 
   uint32_t issued_mask = 0, issued_par = 0;  // stages with loads in flight (abort path)
   bool mma_issued = false;
@@ -327,8 +354,8 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
       bool ok = true;
       for (int t = unit; t < total && ok; t += units) {
         const Tile tl = tile_at(t, args.order);
-        const int m0 = (tl.m * CG + rank) * kTileRows;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        const int m0 = (tl.m * CG + rank) * kTileRows, kb1 = k_end(tl);
+        for (int kb = k_begin(tl); kb < kb1; ++kb) {
           if (!wait_bounded(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
@@ -365,7 +392,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
           } else {
             const int k = kb * KE, n0 = tl.n * bno + rank * (bn / CG);
 #pragma unroll
-            for (int c = 0; c < kTileRows / 64; ++c) load(sa + c * kMnChunk, tl.z ? &tmA1 : &tmA0, m0 + c * 64, k);
+            for (int c = 0; c < kTileRows / 64; ++c) load(sa + c * kMnChunk, tl.z && !CHUNKS ? &tmA1 : &tmA0, m0 + c * 64, k);
             for (int c = 0; c < mn_chunks; ++c) load(sb + c * kMnChunk, &tmB0, n0 + c * 64, k);
           }
           issued_mask |= 1u << stage;
@@ -399,6 +426,8 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
         if (!wait_bounded(&acce[acc], acc_phase ^ 1u, wc)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc * kMaxBN);
+        const Tile tl = CHUNKS ? tile_at(t, args.order) : Tile{0, 0, 0};
+        const int kb0 = k_begin(tl), kb1 = k_end(tl);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_bounded(&full[stage], phase, wc)) {
             ok = false;
@@ -476,7 +505,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
       // way while the products finish; columns past the last read the last one's (not stored)
       float sx = 1.0f, sg = 0.f, su = 0.f;
       auto fetch_scales = [&](int c) {
-        if constexpr (!LIN) {
+        if constexpr (F8 && !LIN) {
           const float2 s = column_scales<MODE>(args, min(n_tile + c * W + lane, args.N - 1));
           sg = s.x;
           su = s.y;
@@ -764,10 +793,19 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
                 slope_values<TFL_ACT_GELU, LD>(g, u, dh);
               pack16<LD>(u, o2 + b * (LD / 8), args.bf16_out);
             }
-            pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
+            if constexpr (CHUNKS) {
+#pragma unroll
+              for (int k = 0; k < LD; k += 16)
+                store_cols_f32(st, lane, g + k,
+                               reinterpret_cast<float*>(args.out) + ((size_t)tl.z * args.M + m0) * args.ldo + n0 + b * LD + k,
+                               args.ldo, rows, cols - b * LD - k);
+            } else {
+              pack16<LD>(g, o + b * (LD / 8), args.bf16_out);
+            }
           }
           const size_t to = (size_t)m0 * args.ldo + n0;
-          store_cols<W>(st, lane, o, (MODE == GRAD_DW && tl.z ? args.out2 : args.out) + to, args.ldo, rows, cols);
+          if constexpr (!CHUNKS)
+            store_cols<W>(st, lane, o, (MODE == GRAD_DW && tl.z ? args.out2 : args.out) + to, args.ldo, rows, cols);
           if constexpr (MODE == GLU_SLOPES) store_cols<W>(st, lane, o2, args.out2 + to, args.ldo, rows, cols);
         }
       }

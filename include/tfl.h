@@ -572,9 +572,10 @@ typedef struct tfl_linear tfl_linear;
  * TFL_ACT_SILU or TFL_ACT_GELU.
  * max_grad_tokens: the most tokens tfl_linear_backward will be given (0: no
  * backward; e4m3 operands have none), and dy_type the type of its dy, fp32 or the
- * operands' (not looked at without a backward).  The handle holds 4 d_out bytes a row
- * of at most 64 MiB (one row at least) of partial sums for it, and with an activation or an
- * fp32 dy 2 max_grad_tokens d_out bytes more (d_out to the next multiple of 64).
+ * operands' (not looked at without a backward).  The handle holds partial sums for it, at
+ * most max(64 MiB, 4 d_out bytes) for db and, for small weights and many tokens, at most 24 MiB for
+ * dw; with an activation or an fp32 dy 2 max_grad_tokens d_out bytes more (d_out to the next
+ * multiple of 64).
  * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
 int tfl_linear_create(int32_t d_in, int32_t d_out, int32_t in_type, int32_t out_type, int32_t act, int32_t dy_type,
                       int64_t max_grad_tokens, tfl_linear** out);

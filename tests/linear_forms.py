@@ -10,6 +10,10 @@ E4M3 = [(16, 320, 80), (7270, 384, 160), (17, 1024, 80), (2951, 272, 2576), (586
 DX = [(6557, 264, 152), (23, 40, 488), (7768, 608, 200), (6550, 1192, 136), (2600, 1024, 2056), (1001, 320, 4104)]
 DW = [(151, 704, 2560), (460, 48, 48), (194, 2528, 2232), (136, 3280, 2592), (2600, 1024, 2056), (1001, 320, 4104)]
 
+# few outputs and many tokens: dw over shares of the tokens
+SHARES = [(41798, 120, 224), (50001, 128, 384), (30011, 8, 8), (20000, 64, 72), (49881, 1160, 176), (30011, 264, 520),
+          (40000, 512, 520), (60001, 1024, 264)]
+
 TILED = (pkg.TFL_GLU_FORM_LONE, pkg.TFL_GLU_FORM_SHARED, pkg.TFL_GLU_FORM_PAIR, pkg.TFL_GLU_FORM_WIDE)
 
 
@@ -24,3 +28,16 @@ def reached(units=None):
 
 WANTED = ({(0, f8, form) for f8 in (False, True) for form in (pkg.TFL_GLU_FORM_FEW, *TILED)} |
           {(part, False, form) for part in (1, 2) for form in TILED})
+
+
+def dealt(units=None):
+    """The forms of the SHARES sizes' dw, each of which has more tiles than its outputs."""
+    got = set()
+    for tokens, k, n in SHARES:
+        form, columns, tiles, _ = pkg.tfl_selftest_linear_plan(k, n, pkg.TFL_BF16, 2, tokens, units)
+        assert tiles > -(-n // (256 if form >= pkg.TFL_GLU_FORM_PAIR else 128)) * -(-k // columns), (tokens, k, n)
+        got.add(form)
+    return got
+
+
+DEALT = {pkg.TFL_GLU_FORM_LONE, pkg.TFL_GLU_FORM_PAIR}

@@ -268,6 +268,27 @@ def test_backward_in_every_form(tokens, k, n, t, act, dy):
     _check_backward(*_backward(tokens, k, n, t, act, dy), t, act)
 
 
+# few outputs and many tokens: dw over shares of the tokens, of lone CTAs and pairs, narrow and wide
+SHARES = linear_forms.SHARES
+
+
+def test_the_sizes_deal_the_tokens_out():
+    assert linear_forms.dealt() >= linear_forms.DEALT
+
+
+@pytest.mark.parametrize("tokens,k,n", SHARES)
+@pytest.mark.parametrize("t,act,dy", KINDS[:2])
+def test_backward_over_shares_of_the_tokens(tokens, k, n, t, act, dy):
+    got = _backward(tokens, k, n, t, act, dy)
+    _check_backward(*got, t, act)
+
+
+def test_a_handle_for_more_tokens_serves_fewer():
+    """Its room for shares is that of its largest call."""
+    for tokens, room in ((700, 40000), (9000, 100000), (5, 30000)):
+        _check_backward(*_backward(tokens, 128, 136, "bf16", "gelu", "f32", room=room), "bf16", "gelu")
+
+
 @pytest.mark.parametrize("want", [("dx",), ("dw",), ("db",), ("dx", "dw"), ("dx", "db"), ("dw", "db")])
 @pytest.mark.parametrize("t,act,dy", KINDS)
 def test_backward_of_some_of_the_gradients(t, act, dy, want):
