@@ -37,15 +37,43 @@ __device__ __forceinline__ void finish_stats(float m0, float sum, float square, 
   rstd = rsqrtf(max_nan(square * a.inv_d - shift * shift, 0.f) + a.eps);
 }
 
+// Sum (or maximum) over the threads of this thread's row: up to a warp's own, or the block's whole warps.  `red`
+// holds one float a warp and value.
+template <int N>
+__device__ __forceinline__ void row_reduce(float* v, int tpr, bool last_is_max, float* red) {
+  const int lanes = tpr < 32 ? tpr : 32;
+  auto join = [&](float x, float y, int k) { return last_is_max && k == N - 1 ? max_nan(x, y) : x + y; };
+#pragma unroll 1
+  for (int o = lanes >> 1; o; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = join(v[k], __shfl_xor_sync(0xffffffffu, v[k], o), k);
+  }
+  if (tpr <= 32) return;
+  __syncthreads();  // the values before have been read
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[k * 32 + (threadIdx.x >> 5)] = v[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = red[k * 32];
+  for (int w = 1; w < tpr >> 5; ++w) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = join(v[k], red[k * 32 + w], k);
+  }
+}
+
 template <class X, class R, class Y, int NV>
 __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
   constexpr bool Q = sizeof(Y) == 1;
   __shared__ float red[64];
   grid_launch_dependents();
   grid_wait_prior();
-  const int tpr = a.tpr, t = threadIdx.x & (tpr - 1);
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
-  const bool live = row < a.rows;  // the whole block meets at group_reduce's barriers
+  // a row's threads: a power of two up to a warp's 32, with other rows in the block, or whole warps that are the
+  // block
+  const int tpr = a.tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + group;
+  const bool live = row < a.rows;  // the whole block meets at row_reduce's barriers
   const int nvec = a.D >> 3;
   const size_t base = (size_t)row * a.D;
   float s[NV][8];
@@ -91,7 +119,7 @@ __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
       if (live && c < nvec) store8(static_cast<R*>(a.res_out) + base + c * 8, s[j]);
     }
   }
-  group_reduce<1>(v, tpr, false, red);
+  row_reduce<1>(v, tpr, false, red);
   const float m0 = v[0] * a.inv_d;
   v[0] = 0.f;
 #pragma unroll
@@ -105,7 +133,7 @@ __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
       }
     }
   }
-  group_reduce<2>(v, tpr, false, red);
+  row_reduce<2>(v, tpr, false, red);
   float shift, mean, r;
   finish_stats(m0, v[0], v[1], a, shift, mean, r);
   if (a.stats && live && t == 0) a.stats[row] = make_float2(mean, r);
@@ -131,7 +159,7 @@ __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
     }
   }
   if constexpr (Q) {
-    group_reduce<1>(v, tpr, true, red);
+    row_reduce<1>(v, tpr, true, red);
     const float amax = max_nan(v[0], kMinAmax);
     if (live && t == 0) a.y_scale[row] = amax / kE4m3Max;
     const float to8 = kE4m3Max / amax;
@@ -144,6 +172,27 @@ __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
         store8(static_cast<Y*>(a.y) + base + c * 8, s[j]);
       }
     }
+  }
+}
+
+// Both sums of a row, as row_sums in rowops.cuh, but over any number of whole warps (16 at most).
+__device__ __forceinline__ void row_pair(float& a, float& b, int tpr, int group, int parity, float2 (*red)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (tpr <= 32) {
+    row_sums(a, b, tpr, group, parity, red);
+    return;
+  }
+  row_sums(a, b, 32, group, parity, red);
+  const int nw = tpr >> 5;
+  if (lane == 0) red[parity][threadIdx.x >> 5] = make_float2(a, b);
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+  const float2 p = (lane & 15) < nw ? red[parity][group * nw + (lane & 15)] : make_float2(0.f, 0.f);
+  a = p.x;
+  b = p.y;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
   }
 }
 
@@ -174,9 +223,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
   extern __shared__ float part[];  // [groups][D + 4] when the block has more than one group
   grid_launch_dependents();
   grid_wait_prior();
-  const int tpr = a.tpr, t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr;
+  const int tpr = a.tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, groups = THREADS / tpr;
   const int rows = (int)a.rows, D = a.D;
-  const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
+  const bool spare = group >= groups;  // warps that make no whole group
+  const int stride = gridDim.x * groups, first = spare ? rows : blockIdx.x * groups + group;
   const int shift = STRADDLE ? (int)(((int64_t)first * D) & 7) : 0;
   const int nvec = (shift + D + 7) >> 3;
   auto col = [&](int j) { return (t + j * tpr) * 8 - shift; };  // this thread's columns: from here on
@@ -185,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
   auto edge = [&](int j) { return STRADDLE && (col(j) < 0 || col(j) + 8 > D); };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    in[j] = t + j * tpr < nvec;
+    in[j] = !spare && t + j * tpr < nvec;
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[j][i] = db[j][i] = 0;  // two zeros
     if constexpr (STRADDLE) {
@@ -304,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
     v0 += hi;
     f2_unpack(at2, v1, hi);
     v1 += hi;
-    row_sums(v0, v1, tpr, group, parity, red);
+    row_pair(v0, v1, tpr, group, parity, red);
     parity ^= 1;
     const uint64_t k0 = f2_splat(-(v0 * a.inv_d)), k1 = f2_splat(-(v1 * a.inv_d));
 #pragma unroll
@@ -635,17 +685,33 @@ cudaError_t forward(LnArgs a, int num_sms, cudaStream_t s) {
   // Four vectors a thread, where an fp32 residual doubles their bytes two: the rows in flight are what counts,
   // and more, smaller blocks leave less of a last round (8192 x 1024 fp16 / fp32 in blocks of 256 threads 20.5
   // with four and 19.7 us with two, in blocks of 64 20.1 and 18.3; 16384 x 2048 bf16 46.4, 54.5, 42.8 and 47.8).
+  // Other numbers where they leave fewer lanes without a vector (12275 x 2168 fp16 to e4m3 49.9 us with four, 41.6
+  // with three; two 16-bit vectors only where they spare a fifth: 5274 x 3336 fp16 30.9 us, with four 28.2).
   // Short rows share a block (65536 x 128 fp16 / fp32: 16.8 us in blocks of 256 threads, 17.9 of 64).
-  const int most = sizeof(R) == 4 ? 2 : 4;
-  int nv = nvec <= 32 ? 1 : nvec <= 64 ? 2 : most;
-  if (nvec > 1024 * nv) nv = 4;
-  a.tpr = pow2_at_least((nvec + nv - 1) / nv);
-  const int least = nv == 1 ? 256 : 64, threads = a.tpr > least ? a.tpr : least;
+  int nv = 1, slots = 1 << 30;
+  auto threads_of = [&](int n) {
+    const int t = (nvec + n - 1) / n;
+    return t <= 32 ? pow2_at_least(t) : (t + 31) / 32 * 32;
+  };
+  if (nvec > 32) {
+    const int order[2][3] = {{4, 3, 2}, {2, 3, 4}};
+    for (int n : order[sizeof(R) == 4]) {
+      if (threads_of(n) > 1024 || (nvec <= 64 && n != 2)) continue;
+      const int cost = threads_of(n) * n * (sizeof(R) == 2 && n == 2 ? 6 : 5);
+      if (cost < slots) {
+        nv = n;
+        slots = cost;
+      }
+    }
+  }
+  a.tpr = threads_of(nv);
+  const int least = nv == 1 ? 256 : 64, threads = a.tpr >= least ? a.tpr : a.tpr <= 32 ? least : a.tpr;
   const int64_t per = threads / a.tpr;
   const unsigned grid = (unsigned)((a.rows + per - 1) / per);
   a.ahead = per * num_sms * (1024 / threads);  // 64 registers a thread: 1024 threads an SM
   if (nv == 1) return launch_dependent(ln_forward_kernel<X, R, Y, 1>, grid, threads, 0, s, a);
   if (nv == 2) return launch_dependent(ln_forward_kernel<X, R, Y, 2>, grid, threads, 0, s, a);
+  if (nv == 3) return launch_dependent(ln_forward_kernel<X, R, Y, 3>, grid, threads, 0, s, a);
   return launch_dependent(ln_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
 }
 
@@ -673,12 +739,13 @@ cudaError_t add_partials(const LnGradArgs& a, int n, cudaStream_t s) {
 template <class X, class R, int NV, int THREADS, int BLOCKS, bool STRADDLE = false>
 cudaError_t backward_with(LnGradArgs a, int num_sms, cudaStream_t s) {
   // (a row that begins inside a vector reaches into up to D / 8 + 2 of them)
-  a.tpr = pow2_at_least(((STRADDLE ? (a.D + 14) / 8 : a.D / 8) + NV - 1) / NV);
+  const int least = ((STRADDLE ? (a.D + 14) / 8 : a.D / 8) + NV - 1) / NV;
+  a.tpr = least <= 32 ? pow2_at_least(least) : (least + 31) / 32 * 32;
   const int groups = THREADS / a.tpr;
   int even = 1;
-  if (STRADDLE) {
-    const int period = a.D % 4 == 0 ? 2 : a.D % 2 == 0 ? 4 : 8;  // rows after which a row begins alike
-    even = groups < period ? period / groups : 1;
+  if (STRADDLE) {  // rows of a group are a multiple of the period apart after which a row begins alike
+    const int period = a.D % 4 == 0 ? 2 : a.D % 2 == 0 ? 4 : 8;
+    while (even * groups % period) ++even;
   }
   const int grid = backward_blocks(a, (a.rows + groups - 1) / groups, num_sms * BLOCKS, even);
   const size_t smem = groups > 1 ? (size_t)groups * (a.D + 4) * sizeof(float) : 0;  // at most 36 KB
