@@ -196,6 +196,8 @@ __device__ __forceinline__ void row_pair(float& a, float& b, int tpr, int group,
   }
 }
 
+__device__ __forceinline__ void assign(E4m3& d, float v) { d.v = (uint8_t)e4m3x2(v, 0.f); }
+
 // Part of a vector: its first n values, zeros behind.
 template <class T>
 __device__ __forceinline__ void load_first(const T* p, int n, Raw8<T>& r) {
@@ -203,6 +205,126 @@ __device__ __forceinline__ void load_first(const T* p, int n, Raw8<T>& r) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = i < n ? value(p[i]) : 0.f;
   store8(reinterpret_cast<T*>(&r), f);
+}
+
+// The largest of a row's values, likewise.
+__device__ __forceinline__ float row_largest(float v, int tpr, int group, int parity, float2 (*red)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int o = (tpr < 32 ? tpr : 32) >> 1; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (tpr <= 32) return v;
+  const int nw = tpr >> 5;
+  if (lane == 0) red[parity][threadIdx.x >> 5].x = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+  v = (lane & 15) < nw ? red[parity][group * nw + (lane & 15)].x : 0.f;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Forward of widths that 8 does not divide, in vectors: row groups that loop over rows which begin alike, with
+// gamma and beta in registers, as the backward below does it (100000 x 103 bf16 / fp32 to e4m3 33 us; a value at a
+// time, a block a row, 224).
+template <class X, class R, class Y, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(const LnArgs a) {
+  constexpr bool Q = sizeof(Y) == 1;
+  __shared__ float2 red[2][32];
+  grid_launch_dependents();
+  grid_wait_prior();
+  const int tpr = a.tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, groups = THREADS / tpr;
+  const int rows = (int)a.rows, D = a.D;
+  const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
+  const int shift = (int)(((int64_t)first * D) & 7), col = t * 8 - shift;
+  const bool in = t < (shift + D + 7) >> 3, edge = col < 0 || col + 8 > D;
+  auto mine = [&](int i) { return col + i >= 0 && col + i < D; };
+  float g[8], b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    g[i] = in && mine(i) ? a.gamma[col + i] : 0.f;
+    b[i] = in && mine(i) && a.beta ? a.beta[col + i] : 0.f;
+  }
+  const size_t step = (size_t)stride * D;
+  size_t at = (size_t)first * D + t * 8 - shift;  // of the row to load next
+  Raw8<X> x1;
+  Raw8<R> r1;
+  zero_raw(r1);
+  auto fetch = [&](int64_t row) {
+    if (row < rows && in) {
+      const X* x = static_cast<const X*>(a.x) + at;
+      const R* r = a.res ? static_cast<const R*>(a.res) + at : nullptr;
+      if (row == rows - 1 && col + 8 > D) {  // behind the last row there is nothing to read
+        load_first(x, D - col, x1);
+        if (r) load_first(r, D - col, r1);
+      } else {
+        load_raw(x, x1);
+        if (r) load_raw(r, r1);
+      }
+    } else {
+      zero_raw(x1);
+      zero_raw(r1);
+    }
+    at += step;
+  };
+  int parity = 0;
+  fetch(first);
+  const int lead = tpr < 32 ? first / (32 / tpr) * (32 / tpr) : first;  // groups that share a warp go together
+  int64_t row = first;
+  size_t to = at - step;
+  for (int64_t turn = lead; turn < rows; turn += stride, row += stride, to += step) {
+    const bool live = row < rows && in;
+    float s[8], r[8];
+    widen(x1, s);
+    widen(r1, r);
+    fetch(row + stride);
+    float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = !edge || mine(i) ? s[i] + r[i] : 0.f;
+      v0 += s[i];
+    }
+    auto store = [&](auto* p, const float* v) {
+      if (!live) return;
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (mine(i)) assign(p[to + i], v[i]);
+      } else {
+        store8(p + to, v);
+      }
+    };
+    if (a.res_out) store(static_cast<R*>(a.res_out), s);
+    row_pair(v0, v1, tpr, group, parity, red);
+    parity ^= 1;
+    const float m0 = v0 * a.inv_d;
+    v0 = v1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = in && (!edge || mine(i)) ? s[i] - m0 : 0.f;
+      v0 += s[i];
+      v1 = fmaf(s[i], s[i], v1);
+    }
+    row_pair(v0, v1, tpr, group, parity, red);
+    parity ^= 1;
+    float off, mean, rstd;
+    finish_stats(m0, v0, v1, a, off, mean, rstd);
+    if (a.stats && live && t == 0) a.stats[row] = make_float2(mean, rstd);
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s[i] = fmaf((s[i] - off) * rstd, g[i], b[i]);
+      if (Q && (!edge || mine(i))) most = max_nan(most, fabsf(s[i]));
+    }
+    if constexpr (Q) {
+      if (!in) most = 0.f;
+      most = max_nan(row_largest(most, tpr, group, parity, red), kMinAmax);
+      parity ^= 1;
+      if (live && t == 0) a.y_scale[row] = most / kE4m3Max;
+      const float to8 = kE4m3Max / most;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] *= to8;
+    }
+    store(static_cast<Y*>(a.y), s);
+  }
 }
 
 // Backward.  As in rms_backward_kernel: a row group keeps its columns over all its rows, so each thread
@@ -715,6 +837,27 @@ cudaError_t forward(LnArgs a, int num_sms, cudaStream_t s) {
   return launch_dependent(ln_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
 }
 
+// Rows of a group are a multiple of the period apart after which a row begins at the same place in a vector: the
+// least number of blocks whose groups are one.
+int even_blocks(int D, int groups) {
+  const int period = D % 4 == 0 ? 2 : D % 2 == 0 ? 4 : 8;
+  int n = 1;
+  while (n * groups % period) ++n;
+  return n;
+}
+
+template <class X, class R, class Y, int THREADS, int BLOCKS>
+cudaError_t forward_straddle(LnArgs a, int num_sms, cudaStream_t s) {
+  const int least = (a.D + 14) / 8;  // vectors that a row may reach into
+  a.tpr = least <= 32 ? pow2_at_least(least) : (least + 31) / 32 * 32;
+  const int groups = THREADS / a.tpr;
+  const int threads = groups * a.tpr;
+  int64_t n = (int64_t)num_sms * (BLOCKS * THREADS / threads);
+  const int64_t all = (a.rows + groups - 1) / groups;
+  n = all <= n ? all : n - n % even_blocks(a.D, groups);
+  return launch_dependent(ln_forward_straddle_kernel<X, R, Y, THREADS, BLOCKS>, (unsigned)n, threads, 0, s, a);
+}
+
 // Blocks of a backward over groups of rows: what the GPU holds at once, and one alone for so few that
 // a second launch would cost more than their turns; `even`: a multiple of it, where a block has several
 // turns.  A lone block writes dgamma and dbeta itself, where they take the 16-byte stores of the partial rows.
@@ -742,11 +885,7 @@ cudaError_t backward_with(LnGradArgs a, int num_sms, cudaStream_t s) {
   const int least = ((STRADDLE ? (a.D + 14) / 8 : a.D / 8) + NV - 1) / NV;
   a.tpr = least <= 32 ? pow2_at_least(least) : (least + 31) / 32 * 32;
   const int groups = THREADS / a.tpr;
-  int even = 1;
-  if (STRADDLE) {  // rows of a group are a multiple of the period apart after which a row begins alike
-    const int period = a.D % 4 == 0 ? 2 : a.D % 2 == 0 ? 4 : 8;
-    while (even * groups % period) ++even;
-  }
+  const int even = STRADDLE ? even_blocks(a.D, groups) : 1;
   const int grid = backward_blocks(a, (a.rows + groups - 1) / groups, num_sms * BLOCKS, even);
   const size_t smem = groups > 1 ? (size_t)groups * (a.D + 4) * sizeof(float) : 0;  // at most 36 KB
   const cudaError_t e = launch_dependent(ln_backward_kernel<X, R, NV, THREADS, BLOCKS, STRADDLE>, grid, THREADS, smem, s, a);
@@ -787,6 +926,25 @@ cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s) {
   const bool vec = a.D % 8 == 0 && a.D <= kLnMaxRegisterRow && aligned(a.x, 16) && aligned(a.res, 16) &&
                    aligned(a.gamma, 16) && aligned(a.beta, 16) && aligned(a.res_out, 16) &&
                    aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
+  const bool lines = aligned(a.x, 16) && aligned(a.res, 16) && aligned(a.res_out, 16) && aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
+  // (few rows are done as soon a value at a time, a block each: 1000 x 1001 fp16 / fp32 4.4 us, 6.0 in vectors;
+  // 6011 x 1001 17.3 and 16.6, 1000 x 3333 bf16 15.2 and 11.5)
+  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddle && a.rows >= (a.D > 2034 ? 1 : 16) * (int64_t)num_sms) {
+    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
+      using X = decltype(x);
+      using R = decltype(r);
+      auto go = [&](auto y) {
+        using Y = decltype(y);
+        return a.D <= 2034 ? forward_straddle<X, R, Y, 256, 3>(a, num_sms, s) : forward_straddle<X, R, Y, 512, 1>(a, num_sms, s);
+      };
+      if (a.y_type == TFL_E4M3) return go(E4m3());
+      if constexpr (sizeof(X) == 4) {
+        if (a.y_type == TFL_F16) return go(__half());
+        if (a.y_type == TFL_BF16) return go(__nv_bfloat16());
+      }
+      return go(X());
+    });
+  }
   if (!vec && a.D <= kLnMaxValues) {
     return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
       using X = decltype(x);

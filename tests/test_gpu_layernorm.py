@@ -121,6 +121,15 @@ def test_forward_of_many_rows(rows, d, xt, rt, yt):
     _check_forward(rows, d, xt, rt, yt, _forward(rows, d, xt, rt, yt, seed=d))
 
 
+# rows that begin inside a 16-byte vector: every shift, widths around those where the thread groups change, one
+# row a group and several turns of the blocks
+@pytest.mark.parametrize("d", [9, 10, 12, 15, 17, 250, 251, 1001, 1002, 1004, 2033, 2034, 2035, 4081, 4082, 4083])
+@pytest.mark.parametrize("xt,rt,yt", [("bf16", "f32", "e4m3"), ("f16", "f16", "f16"), ("f32", "f32", "bf16"), ("f16", "f16", "e4m3")])
+def test_forward_of_rows_that_begin_inside_a_vector(d, xt, rt, yt):
+    for rows in (1, 2, 9, 160, 6007 if d < 2000 else 1501, 40009 if d < 20 else 303):
+        _check_forward(rows, d, xt, rt, yt, _forward(rows, d, xt, rt, yt, rows != 9, rows != 2, rows != 160, seed=rows + d))
+
+
 @pytest.mark.parametrize("with_res,store,with_beta", [(False, True, True), (True, False, True), (True, True, False),
                                                       (False, False, False)])
 @pytest.mark.parametrize("rows,d", [(6, 256), (6, 129), (2001, 1024), (3, 9001)])
@@ -199,7 +208,7 @@ def test_e4m3_of_rows_below_the_least_scale(rows, d, xt):
     _close(_np(y), ref, 2.0 ** -4 * np.abs(ref) + 2.0 ** -10 + 2 * own + 4 * E * np.abs(ref), "y")
 
 
-@pytest.mark.parametrize("rows,d", [(40, 512), (40, 515), (11003, 512), (3, 9001)])
+@pytest.mark.parametrize("rows,d", [(40, 512), (40, 515), (11003, 512), (11003, 515), (3000, 2500), (3, 9001)])
 def test_forward_in_place_equals_out_of_place(rows, d):
     import torch
     pkg = _pkg()
@@ -217,7 +226,7 @@ def test_forward_in_place_equals_out_of_place(rows, d):
         pkg.tfl_layernorm_destroy(h)
 
 
-@pytest.mark.parametrize("rows,d", [(6, 256), (6, 255), (22000, 256), (6, 9001)])
+@pytest.mark.parametrize("rows,d", [(6, 256), (6, 255), (22000, 256), (22000, 255), (9000, 1001), (6, 9001)])
 def test_rows_of_nan_and_infinity_stay_their_own(rows, d):
     import torch
     pkg = _pkg()
@@ -453,7 +462,7 @@ def test_no_rows():
 def test_rows_behind_the_last_stay_as_they_were():
     import torch
     pkg = _pkg()
-    for d in (128, 130, 8194):
+    for d in (128, 130, 1030, 8194):
         x = torch.randn(9, d, device="cuda").bfloat16()
         y, out, stats = torch.full_like(x, 5.0), torch.full_like(x, 6.0), torch.full((9, 2), 4.0, device="cuda")
         gamma = torch.ones(d, device="cuda")
