@@ -764,7 +764,7 @@ DwPlan linear_dw_plan(int K, int N, int64_t tokens, const TileUnits& u, int most
 TilePlan linear_call_plan(int K, int N, bool f8, int part, int64_t tokens, const TileUnits& u) {
   const int ke = f8 ? 128 : 64;
   const bool lines = K * (f8 ? 1 : 2) % 128 == 0;
-  if (part == LIN_PART_DX) return tile_plan(GRAD_DX, lines, tokens, K, (N + ke - 1) / ke, u);
+  if (part == LIN_PART_DX) return tile_plan(GRAD_DX, lines, tokens, K, (N + ke - 1) / ke, u, 1);
   if (part == LIN_PART_DW) return linear_dw_plan(K, N, tokens, u, most_shares(K, N)).p;
   return tile_plan(LIN_FORWARD, lines, tokens, N, (K + ke - 1) / ke, u);
 }

@@ -100,7 +100,9 @@ TilePlan tile_plan(int mode, bool whole_lines, int64_t M, int64_t N, int64_t num
       const int pieces = (chunks + split - 1) / split;
       if (split > 1 && (rounds > 1 || (split - 1) * pieces * kTileRows * (two ? 256 : 128) > ring_bytes(false, mode == LIN_FORWARD))) continue;
       double block = (bn == kMaxBN ? 555.0 : 600.0) * bn / kMaxBN;
-      const double stream = (double)(rows + bn / cg) * kKBytes / (whole_lines ? 74.0 : 44.0);
+      // (MN-major B comes in boxes of 64 columns; the feed-forward's constants were fitted without that)
+      const int loaded = planes == 1 && (mode == GRAD_DX || mode == GRAD_DW) ? (bn / cg + 63) / 64 * 64 : bn / cg;
+      const double stream = (double)(rows + loaded) * kKBytes / (whole_lines ? 74.0 : 44.0);
       if (block < stream) block = stream;
       const double issue = cg == 2 ? 350.0 : 240.0;
       if (block < issue) block = issue;

@@ -45,7 +45,7 @@ __device__ __forceinline__ float bounded(float z) { return fabsf(z) > 1e4f ? cop
 // a time, the rows of a column slab shared out to gridDim.y blocks.  Every value is read once: bandwidth
 // bounds it.
 template <class DY, class T, int ACT>
-__global__ void __launch_bounds__(256) lin_slopes_kernel(const LinSlopeArgs a) {
+__global__ void __launch_bounds__(256, ACT == TFL_ACT_NONE ? 5 : 4) lin_slopes_kernel(const LinSlopeArgs a) {
   constexpr int AT_ONCE = sizeof(DY) == 4 ? 2 : 4;  // rows in flight a thread
   __shared__ float part[256 * 8];
   grid_launch_dependents();
