@@ -970,22 +970,24 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
   m1.b1 = m1.b0;
   m2.a1 = m2.a0;
   m2.b1 = m2.b0;
+  LinSlopeArgs sa;
+  int parts = 0;
   if (slopes || db) {
-    LinSlopeArgs a;
-    a.rows = tokens;
-    a.cols = Ni;
-    a.pitch = l->pitch;
-    a.dy_type = l->dy_type;
-    a.type = l->in_type;
-    a.act = l->act;
-    a.dy = dy;
-    a.z = static_cast<const uint16_t*>(z);
-    a.dz = slopes ? l->dz : nullptr;
-    a.db = db;
-    a.partial = l->partial;
-    a.blocks = l->blocks;
-    TFL_CUDA(launch_lin_slopes(a, l->units.sms, st), "linear layer slopes");
+    sa.rows = tokens;
+    sa.cols = Ni;
+    sa.pitch = l->pitch;
+    sa.dy_type = l->dy_type;
+    sa.type = l->in_type;
+    sa.act = l->act;
+    sa.dy = dy;
+    sa.z = static_cast<const uint16_t*>(z);
+    sa.dz = slopes ? l->dz : nullptr;
+    sa.db = db;
+    sa.partial = l->partial;
+    sa.blocks = l->blocks;
+    TFL_CUDA(launch_lin_slopes(sa, l->units.sms, st, &parts), "linear layer slopes");
   }
+  // What follows reads the slopes and their sums only: one linked chain, db's last launch in the tail of the others.
   TileArgs a = linear_args(l);
   a.bf16_out = a.bf16_operands;
   if (dx) {
@@ -995,6 +997,7 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     a.group_m = tile_group(p1, Ki);
     a.ldo = Ki;
     a.out = static_cast<uint16_t*>(dx);
+    a.link = LINK_FIRST;
     TFL_CUDA(launch_tiles(p1, GRAD_DX, false, m1, a, st), "linear layer dx");
   }
   if (dw) {
@@ -1004,16 +1007,18 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     a.planes = dwp.shares;
     a.group_m = tile_group(p2, Ki);
     a.ldo = Ki;
+    a.link = dx ? LINK_LATER : LINK_FIRST;
+    a.out = static_cast<uint16_t*>(dw);
     if (dwp.shares > 1) {
       a.out = reinterpret_cast<uint16_t*>(l->parts);
       TFL_CUDA(launch_linear_shares(p2, m2, a, st), "linear layer weight gradient");
       TFL_CUDA(launch_share_sums(l->parts, dwp.shares, (int64_t)Ni * Ki, a.bf16_operands, static_cast<uint16_t*>(dw), st),
                "linear layer weight gradient's sum");
-      return TFL_OK;
+    } else {
+      TFL_CUDA(launch_tiles(p2, GRAD_DW, false, m2, a, st), "linear layer weight gradient");
     }
-    a.out = static_cast<uint16_t*>(dw);
-    TFL_CUDA(launch_tiles(p2, GRAD_DW, false, m2, a, st), "linear layer weight gradient");
   }
+  if (parts) TFL_CUDA(launch_lin_db(sa, parts, dx || dw ? LINK_LATER : LINK_NONE, st), "linear layer db");
   return TFL_OK;
 }
 

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(256, ACT == TFL_ACT_NONE ? 5 : 4) lin_slopes_k
 }
 
 template <class DY, class T>
-cudaError_t slopes(LinSlopeArgs a, int num_sms, cudaStream_t s) {
+cudaError_t slopes(LinSlopeArgs a, int num_sms, cudaStream_t s, int* parts) {
   a.tx = pow2_at_least(a.cols / 8);
   if (a.tx > 32) a.tx = 32;
   const int64_t slabs = (a.cols / 8 + a.tx - 1) / a.tx, ys = 256 / a.tx, turns = (a.rows + ys - 1) / ys;
@@ -129,20 +129,23 @@ cudaError_t slopes(LinSlopeArgs a, int num_sms, cudaStream_t s) {
   const bool lone = n == 1;
   if (lone) a.partial = a.db;
   const dim3 grid((unsigned)slabs, (unsigned)n);
-  const cudaError_t e = a.act == TFL_ACT_SILU   ? launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_SILU>, grid, 256, 0, s, a)
-                        : a.act == TFL_ACT_GELU ? launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_GELU>, grid, 256, 0, s, a)
-                                                : launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_NONE>, grid, 256, 0, s, a);
-  if (e != cudaSuccess || !a.db || lone) return e;
-  return launch_column_sums(a.partial, (int)n, a.cols, a.cols, a.cols, a.db, nullptr, s);
+  *parts = a.db && !lone ? (int)n : 0;
+  return a.act == TFL_ACT_SILU   ? launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_SILU>, grid, 256, 0, s, a)
+         : a.act == TFL_ACT_GELU ? launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_GELU>, grid, 256, 0, s, a)
+                                 : launch_dependent(lin_slopes_kernel<DY, T, TFL_ACT_NONE>, grid, 256, 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_lin_slopes(const LinSlopeArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_lin_slopes(const LinSlopeArgs& a, int num_sms, cudaStream_t s, int* parts) {
   if (a.type == TFL_F16)
-    return a.dy_type == TFL_F32 ? slopes<float, __half>(a, num_sms, s) : slopes<__half, __half>(a, num_sms, s);
-  return a.dy_type == TFL_F32 ? slopes<float, __nv_bfloat16>(a, num_sms, s)
-                              : slopes<__nv_bfloat16, __nv_bfloat16>(a, num_sms, s);
+    return a.dy_type == TFL_F32 ? slopes<float, __half>(a, num_sms, s, parts) : slopes<__half, __half>(a, num_sms, s, parts);
+  return a.dy_type == TFL_F32 ? slopes<float, __nv_bfloat16>(a, num_sms, s, parts)
+                              : slopes<__nv_bfloat16, __nv_bfloat16>(a, num_sms, s, parts);
+}
+
+cudaError_t launch_lin_db(const LinSlopeArgs& a, int parts, int link, cudaStream_t s) {
+  return launch_column_sums(a.partial, parts, a.cols, a.cols, a.cols, a.db, nullptr, s, link);
 }
 
 }  // namespace tfl

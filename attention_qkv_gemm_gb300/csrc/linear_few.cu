@@ -130,11 +130,6 @@ __global__ void __launch_bounds__(512) lin_few_kernel(const LinFewArgs a) {
   }
 }
 
-template <int TYPE, int NT, int G, int U, int LINES>
-cudaError_t launch_form(const LinFewArgs& a, int warps, cudaStream_t s) {
-  return launch_dependent(lin_few_kernel<TYPE, NT, G, U, LINES>, (a.d_out + 8 * G - 1) / (8 * G), warps * 32, 0, s, a);
-}
-
 // A warp loads all its steps, then multiplies: so a row in one turn of a block's warps (up to sixteen, four
 // steps each; two turns of 8 KB rows), 8 columns a block where the GPU holds all blocks at once and 16 where
 // it does not: a second wave of blocks costs more than their loads (one token x 2048 x 8192 bf16, 1024 blocks of
