@@ -207,6 +207,33 @@ __device__ __forceinline__ void load_first(const T* p, int n, Raw8<T>& r) {
   store8(reinterpret_cast<T*>(&r), f);
 }
 
+// Which of a vector's columns col .. col + 7 a row of D values has: 16 bits each, all set or none.
+__device__ __forceinline__ void own_columns(int col, int D, bool in, uint32_t* own) {
+  auto has = [&](int i) { return in && col + i >= 0 && col + i < D; };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) own[i] = (has(2 * i) ? 0xffffu : 0u) | (has(2 * i + 1) ? 0xffff0000u : 0u);
+}
+__device__ __forceinline__ bool has_column(const uint32_t* own, int i) {
+  return own[i / 2] & (i & 1 ? 0xffff0000u : 0xffffu);
+}
+// The others' values, whatever they are, become zeros.
+template <class T>
+__device__ __forceinline__ void drop_others(Raw8<T>& r, const uint32_t* own) {
+  if constexpr (sizeof(T) == 2) {
+    r.w[0].x &= own[0], r.w[0].y &= own[1], r.w[0].z &= own[2], r.w[0].w &= own[3];
+  } else {
+    uint32_t* w = &r.w[0].x;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = has_column(own, i) ? w[i] : 0u;
+  }
+}
+template <class T>
+__device__ __forceinline__ void store_own(T* p, const float* v, const uint32_t* own) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (has_column(own, i)) assign(p[i], v[i]);
+}
+
 // The largest of a row's values, likewise.
 __device__ __forceinline__ float row_largest(float v, int tpr, int group, int parity, float2 (*red)[32]) {
   const int lane = threadIdx.x & 31;
@@ -236,12 +263,14 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
   const int stride = gridDim.x * groups, first = blockIdx.x * groups + group;
   const int shift = (int)(((int64_t)first * D) & 7), col = t * 8 - shift;
   const bool in = t < (shift + D + 7) >> 3, edge = col < 0 || col + 8 > D;
-  auto mine = [&](int i) { return col + i >= 0 && col + i < D; };
+  uint32_t own[4];
+  own_columns(col, D, in, own);
+  auto mine = [&](int i) { return has_column(own, i); };
   float g[8], b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    g[i] = in && mine(i) ? a.gamma[col + i] : 0.f;
-    b[i] = in && mine(i) && a.beta ? a.beta[col + i] : 0.f;
+    g[i] = mine(i) ? a.gamma[col + i] : 0.f;
+    b[i] = mine(i) && a.beta ? a.beta[col + i] : 0.f;
   }
   const size_t step = (size_t)stride * D;
   size_t at = (size_t)first * D + t * 8 - shift;  // of the row to load next
@@ -285,9 +314,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
     auto store = [&](auto* p, const float* v) {
       if (!live) return;
       if (edge) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (mine(i)) assign(p[to + i], v[i]);
+        store_own(p + to, v, own);
       } else {
         store8(p + to, v);
       }
@@ -299,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
     v0 = v1 = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      s[i] = in && (!edge || mine(i)) ? s[i] - m0 : 0.f;
+      s[i] = !edge || mine(i) ? s[i] - m0 : 0.f;
       v0 += s[i];
       v1 = fmaf(s[i], s[i], v1);
     }
@@ -354,6 +381,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
   auto col = [&](int j) { return (t + j * tpr) * 8 - shift; };  // this thread's columns: from here on
   bool in[NV];                                                  // vectors of this thread that exist
   uint64_t dg[NV][4], db[NV][4], gk[AHEAD ? NV : 1][4];
+  uint32_t own[NV][4];  // STRADDLE
   auto edge = [&](int j) { return STRADDLE && (col(j) < 0 || col(j) + 8 > D); };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -361,6 +389,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
 #pragma unroll
     for (int i = 0; i < 4; ++i) dg[j][i] = db[j][i] = 0;  // two zeros
     if constexpr (STRADDLE) {
+      own_columns(col(j), D, in[j], own[j]);
       float f[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = in[j] && col(j) + i >= 0 && col(j) + i < D ? a.gamma[col(j) + i] : 0.f;
@@ -440,21 +469,18 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
     const uint64_t mean2 = f2_splat(st.x), r2 = f2_splat(st.y);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if constexpr (STRADDLE) drop_others(y1[j], own[j]);  // a neighbour's values count as nothing
       widen2(s1[j], s[j]);
       widen2(y1[j], y[j]);
       e[j] = e1[j];
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[j][i] = f2_mul(f2_sub(s[j][i], mean2), r2);  // t
-      if (edge(j)) {  // a neighbour's values, whatever they are
+      if (edge(j)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float s0, s1, y0, y1;
-          f2_unpack(s[j][i], s0, s1);
-          f2_unpack(y[j][i], y0, y1);
-          const int c = col(j) + 2 * i;
-          const bool in0 = c >= 0 && c < D, in1 = c + 1 >= 0 && c + 1 < D;
-          s[j][i] = f2_pack(in0 ? s0 : 0.f, in1 ? s1 : 0.f);
-          y[j][i] = f2_pack(in0 ? y0 : 0.f, in1 ? y1 : 0.f);
+          float t0, t1;
+          f2_unpack(s[j][i], t0, t1);
+          s[j][i] = f2_pack(has_column(own[j], 2 * i) ? t0 : 0.f, has_column(own[j], 2 * i + 1) ? t1 : 0.f);
         }
       }
     }
@@ -497,12 +523,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2_unpack(o[i], of[2 * i], of[2 * i + 1]);
         if (edge(j)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (col(j) + i < 0 || col(j) + i >= D) continue;
-            if (dsum) assign(dsum[j * jump + i], of[i]);
-            if (dx) assign(dx[j * jump + i], of[i]);
-          }
+          if (dsum) store_own(dsum + j * jump, of, own[j]);
+          if (dx) store_own(dx + j * jump, of, own[j]);
         } else {
           if (dsum) store8(dsum + j * jump, of);
           if (dx) store8(dx + j * jump, of);
