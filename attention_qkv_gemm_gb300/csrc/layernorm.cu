@@ -10,10 +10,14 @@
 // large.  The mean itself is off by the rounding of a sum of D terms; the centred values' own mean d
 // repairs it (m + d, and (s - m)^2 less d^2), which costs one more sum in the same butterfly.
 //
+// 8192 x 1024 fp16 with an fp32 residual: 18.5 us, 5.4 TB/s, 0.80 of the copy rate (1.7 waves of blocks, start and
+// tail); 100000 x 1024 bf16 to e4m3 110 us, 0.96.  Backward 8192 x 1024 bf16 / fp32 25.0 us, 0.79 (21.5 and
+// 3.5 for the second kernel).
+//
 // The backward takes m and r from the forward (8 bytes a row): from s alone it would need two more
 // sums a row that wait for each other before the two that the gradient needs.
 //
-// Widths that 8 does not divide, unaligned buffers and rows too long for registers take the
+// Unaligned buffers, rows too long for registers and few rows of widths that 8 does not divide take the
 // element-wise kernels.
 #include "rowops.cuh"
 
@@ -176,6 +180,7 @@ __global__ void __launch_bounds__(1024) ln_forward_kernel(const LnArgs a) {
 }
 
 // Both sums of a row, as row_sums in rowops.cuh, but over any number of whole warps (16 at most).
+template <int WARPS = 16>
 __device__ __forceinline__ void row_pair(float& a, float& b, int tpr, int group, int parity, float2 (*red)[32]) {
   const int lane = threadIdx.x & 31;
   if (tpr <= 32) {
@@ -186,11 +191,12 @@ __device__ __forceinline__ void row_pair(float& a, float& b, int tpr, int group,
   const int nw = tpr >> 5;
   if (lane == 0) red[parity][threadIdx.x >> 5] = make_float2(a, b);
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
-  const float2 p = (lane & 15) < nw ? red[parity][group * nw + (lane & 15)] : make_float2(0.f, 0.f);
+  const int w = lane & (WARPS - 1);
+  const float2 p = w < nw ? red[parity][group * nw + w] : make_float2(0.f, 0.f);
   a = p.x;
   b = p.y;
 #pragma unroll
-  for (int o = 8; o; o >>= 1) {
+  for (int o = WARPS / 2; o; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
     b += __shfl_xor_sync(0xffffffffu, b, o);
   }
@@ -235,6 +241,7 @@ __device__ __forceinline__ void store_own(T* p, const float* v, const uint32_t* 
 }
 
 // The largest of a row's values, likewise.
+template <int WARPS = 16>
 __device__ __forceinline__ float row_largest(float v, int tpr, int group, int parity, float2 (*red)[32]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
@@ -243,18 +250,20 @@ __device__ __forceinline__ float row_largest(float v, int tpr, int group, int pa
   const int nw = tpr >> 5;
   if (lane == 0) red[parity][threadIdx.x >> 5].x = v;
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
-  v = (lane & 15) < nw ? red[parity][group * nw + (lane & 15)].x : 0.f;
+  const int w = lane & (WARPS - 1);
+  v = w < nw ? red[parity][group * nw + w].x : 0.f;
 #pragma unroll
-  for (int o = 8; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = WARPS / 2; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
 // Forward of widths that 8 does not divide, in vectors: row groups that loop over rows which begin alike, with
-// gamma and beta in registers, as the backward below does it (100000 x 103 bf16 / fp32 to e4m3 33 us; a value at a
+// gamma and beta in registers, as the backward below does it (100000 x 103 bf16 / fp32 to e4m3 31 us; a value at a
 // time, a block a row, 224).
 template <class X, class R, class Y, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(const LnArgs a) {
   constexpr bool Q = sizeof(Y) == 1;
+  constexpr int WARPS = THREADS > 512 ? 32 : 16;  // of the widest group
   __shared__ float2 red[2][32];
   grid_launch_dependents();
   grid_wait_prior();
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
       }
     };
     if (a.res_out) store(static_cast<R*>(a.res_out), s);
-    row_pair(v0, v1, tpr, group, parity, red);
+    row_pair<WARPS>(v0, v1, tpr, group, parity, red);
     parity ^= 1;
     const float m0 = v0 * a.inv_d;
     v0 = v1 = 0.f;
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
       v0 += s[i];
       v1 = fmaf(s[i], s[i], v1);
     }
-    row_pair(v0, v1, tpr, group, parity, red);
+    row_pair<WARPS>(v0, v1, tpr, group, parity, red);
     parity ^= 1;
     float off, mean, rstd;
     finish_stats(m0, v0, v1, a, off, mean, rstd);
@@ -343,7 +352,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
     }
     if constexpr (Q) {
       if (!in) most = 0.f;
-      most = max_nan(row_largest(most, tpr, group, parity, red), kMinAmax);
+      most = max_nan(row_largest<WARPS>(most, tpr, group, parity, red), kMinAmax);
       parity ^= 1;
       if (live && t == 0) a.y_scale[row] = most / kE4m3Max;
       const float to8 = kE4m3Max / most;
@@ -363,13 +372,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
 // STRADDLE: widths that 8 does not divide, in 16-byte vectors all the same.  A row then begins `shift`
 // values into a vector, (row D) mod 8; a group takes rows a multiple of 8 / gcd(D, 8) apart, so its shift
 // and its threads' columns stay.  A row's first and last vectors hold values of its neighbours, which count
-// as nothing and are not written (6011 x 1001 fp16 17.4 us, 25.2 a value at a time).
+// as nothing and are not written (6011 x 1001 fp16 16.9 us, 25.2 a value at a time; without the prefetch that
+// wide rows' loads need, 5000 x 7001 128 instead of 108 us).
 template <class X, class R, int NV, int THREADS, int BLOCKS, bool STRADDLE>
 __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGradArgs a) {
   constexpr bool AHEAD = NV == 1;  // room for the next row, and for gamma
-  static_assert(!STRADDLE || AHEAD, "a shifted gamma is kept");
   __shared__ float2 red[2][32];
-  extern __shared__ float part[];  // [groups][D + 4] when the block has more than one group
+  // [groups][D + 4] when the block has more than one group; gamma as this block's rows lie, if it has to be shifted
+  // and there are no registers for it (then it has one)
+  extern __shared__ float part[];
   grid_launch_dependents();
   grid_wait_prior();
   const int tpr = a.tpr, group = threadIdx.x / tpr, t = threadIdx.x - group * tpr, groups = THREADS / tpr;
@@ -382,6 +393,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
   bool in[NV];                                                  // vectors of this thread that exist
   uint64_t dg[NV][4], db[NV][4], gk[AHEAD ? NV : 1][4];
   uint32_t own[NV][4];  // STRADDLE
+  auto gamma_of = [&](int j) { return STRADDLE ? part + (t + j * tpr) * 8 : a.gamma + col(j); };  // not AHEAD
   auto edge = [&](int j) { return STRADDLE && (col(j) < 0 || col(j) + 8 > D); };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -394,7 +406,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = in[j] && col(j) + i >= 0 && col(j) + i < D ? a.gamma[col(j) + i] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) gk[j][i] = f2_pack(f[2 * i], f[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (AHEAD) gk[j][i] = f2_pack(f[2 * i], f[2 * i + 1]);
+      }
+      if constexpr (!AHEAD) {
+        if (!spare) store8(part + (t + j * tpr) * 8, f);  // each thread its own
+      }
     } else if constexpr (AHEAD) {
       if (in[j]) {
         load_params2(a.gamma + col(j), gk[j]);
@@ -426,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
         if (STRADDLE && row == rows - 1 && col(j) + 8 > D) {  // behind the last row there is nothing to read
           load_first(sp + j * jump, D - col(j), s1[j]);
           load_first(yp + j * jump, D - col(j), y1[j]);
-          if (ep) load_first(ep + j * jump, D - col(j), e1[j]);
+          if (AHEAD && ep) load_first(ep + j * jump, D - col(j), e1[j]);
         } else {
           load_raw(sp + j * jump, s1[j]);
           load_raw(yp + j * jump, y1[j]);
@@ -442,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
     yp += step;
     if (ep) ep += step;
     // the row behind that one to L2: with one row in registers the bytes in flight are what bounds the rate
-    if (!STRADDLE && row + stride < rows) {
+    if (!(STRADDLE && AHEAD) && row + stride < rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (!in[j]) continue;
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       uint64_t g[4] = {0, 0, 0, 0};
-      if (!AHEAD && in[j]) load_params2(a.gamma + col(j), g);
+      if (!AHEAD && in[j]) load_params2(gamma_of(j), g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t w = f2_mul(y[j][i], AHEAD ? gk[AHEAD ? j : 0][i] : g[i]);
@@ -509,8 +526,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
     for (int j = 0; j < NV; ++j) {
       if (live && in[j]) {
         uint64_t g[4], o[4];
-        if constexpr (!AHEAD) load_params2(a.gamma + col(j), g);
-        if (!AHEAD && ep_late) load_raw(ep_late + j * jump, e[j]);
+        if constexpr (!AHEAD) load_params2(gamma_of(j), g);
+        if (!AHEAD && ep_late) {
+          if (STRADDLE && next - stride == rows - 1 && col(j) + 8 > D)
+            load_first(ep_late + j * jump, D - col(j), e[j]);
+          else
+            load_raw(ep_late + j * jump, e[j]);
+        }
         widen2(e[j], o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -906,10 +928,14 @@ cudaError_t backward_with(LnGradArgs a, int num_sms, cudaStream_t s) {
   // (a row that begins inside a vector reaches into up to D / 8 + 2 of them)
   const int least = ((STRADDLE ? (a.D + 14) / 8 : a.D / 8) + NV - 1) / NV;
   a.tpr = least <= 32 ? pow2_at_least(least) : (least + 31) / 32 * 32;
+  constexpr bool SHIFTED = STRADDLE && NV > 1;  // gamma in shared memory: one group a block
+  if (SHIFTED && a.tpr <= THREADS / 2) a.tpr = THREADS / 2 + 32;
   const int groups = THREADS / a.tpr;
   const int even = STRADDLE ? even_blocks(a.D, groups) : 1;
   const int grid = backward_blocks(a, (a.rows + groups - 1) / groups, num_sms * BLOCKS, even);
-  const size_t smem = groups > 1 ? (size_t)groups * (a.D + 4) * sizeof(float) : 0;  // at most 36 KB
+  const size_t smem = SHIFTED      ? (size_t)a.tpr * NV * 8 * sizeof(float)  // 32 KB
+                      : groups > 1 ? (size_t)groups * (a.D + 4) * sizeof(float)  // at most 36 KB
+                                   : 0;
   const cudaError_t e = launch_dependent(ln_backward_kernel<X, R, NV, THREADS, BLOCKS, STRADDLE>, grid, THREADS, smem, s, a);
   return e == cudaSuccess ? add_partials(a, grid, s) : e;
 }
@@ -921,7 +947,8 @@ cudaError_t backward_values(LnGradArgs a, int num_sms, cudaStream_t s) {
   return e == cudaSuccess ? add_partials(a, grid, s) : e;
 }
 
-constexpr int kLnMaxStraddle = 4082;  // widest row whose vectors, wherever it begins, 512 threads hold
+// widest row whose vectors, wherever it begins, 512 and 1024 threads hold (the backward: 512 of two vectors)
+constexpr int kLnMaxStraddle = 4082, kLnMaxStraddleWide = 8178;
 
 template <class X, class R, bool STRADDLE>
 cudaError_t backward(const LnGradArgs& a, int num_sms, cudaStream_t s) {
@@ -931,11 +958,9 @@ cudaError_t backward(const LnGradArgs& a, int num_sms, cudaStream_t s) {
     if (a.rows * pow2_at_least(a.D / 8) >= (int64_t)num_sms * 512) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
     return backward_with<X, R, 1, 256, 2, STRADDLE>(a, num_sms, s);
   }
-  if (STRADDLE || a.D <= 4096) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
-  if constexpr (!STRADDLE) {
-    if (a.D <= 8192) return backward_with<X, R, 2, 512, 1>(a, num_sms, s);
-    return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
-  }
+  if (a.D <= (STRADDLE ? 4082 : 4096)) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
+  if (STRADDLE || a.D <= 8192) return backward_with<X, R, 2, 512, 1, STRADDLE>(a, num_sms, s);
+  if constexpr (!STRADDLE) return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
   return cudaErrorInvalidValue;
 }
 
@@ -950,14 +975,16 @@ cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s) {
                    aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
   const bool lines = aligned(a.x, 16) && aligned(a.res, 16) && aligned(a.res_out, 16) && aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
   // (few rows are done as soon a value at a time, a block each: 1000 x 1001 fp16 / fp32 4.4 us, 6.0 in vectors;
-  // 6011 x 1001 17.3 and 16.6, 1000 x 3333 bf16 15.2 and 11.5)
-  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddle && a.rows >= (a.D > 2034 ? 1 : 16) * (int64_t)num_sms) {
+  // 6011 x 1001 17.3 and 15.7, 1000 x 3333 bf16 15.2 and 10.9, 5000 x 7001 fp16 168 and 67)
+  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddleWide && a.rows >= (a.D > 2034 ? 1 : 16) * (int64_t)num_sms) {
     return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
       using X = decltype(x);
       using R = decltype(r);
       auto go = [&](auto y) {
         using Y = decltype(y);
-        return a.D <= 2034 ? forward_straddle<X, R, Y, 256, 3>(a, num_sms, s) : forward_straddle<X, R, Y, 512, 1>(a, num_sms, s);
+        return a.D <= 2034 ? forward_straddle<X, R, Y, 256, 3>(a, num_sms, s)
+               : a.D <= kLnMaxStraddle ? forward_straddle<X, R, Y, 512, 1>(a, num_sms, s)
+                                       : forward_straddle<X, R, Y, 1024, 1>(a, num_sms, s);
       };
       if (a.y_type == TFL_E4M3) return go(E4m3());
       if constexpr (sizeof(X) == 4) {
@@ -999,8 +1026,10 @@ cudaError_t launch_ln_backward(const LnGradArgs& args, int num_sms, cudaStream_t
   LnGradArgs a = args;
   const bool lines = aligned(a.sum, 16) && aligned(a.dy, 16) && aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
   const bool vec = lines && a.D % 8 == 0 && a.D <= kLnMaxRegisterRow / 2 && aligned(a.gamma, 16);
-  // (few rows are done as soon a value at a time: 9807 x 103 fp16 7.8 us, 8.9 in vectors; 20000 x 203 20.9 and 15.8)
-  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddle && a.rows * a.D >= 2000000) {
+  // (few rows are done as soon a value at a time: 9807 x 103 fp16 7.8 us, 8.9 in vectors; 20000 x 203 20.9 and
+  // 14.4; 500 x 4099 18.9 and 21.4, 2000 x 4099 47.5 and 45.0, 5000 x 7001 211 and 108)
+  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddleWide &&
+      a.rows * a.D >= (a.D > kLnMaxStraddle ? 8000000 : 2000000)) {
     return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
       return backward<decltype(x), decltype(r), true>(a, num_sms, s);
     });

@@ -226,7 +226,7 @@ def test_forward_in_place_equals_out_of_place(rows, d):
         pkg.tfl_layernorm_destroy(h)
 
 
-@pytest.mark.parametrize("rows,d", [(6, 256), (6, 255), (22000, 256), (22000, 255), (9000, 1001), (6, 9001)])
+@pytest.mark.parametrize("rows,d", [(6, 256), (6, 255), (22000, 256), (22000, 255), (9000, 1001), (6, 9001), (700, 4099), (400, 8177)])
 def test_rows_of_nan_and_infinity_stay_their_own(rows, d):
     import torch
     pkg = _pkg()
@@ -341,7 +341,25 @@ def test_backward_of_rows_that_begin_inside_a_vector(d, xt, rt):
         _check_backward(rows, d, xt, rt, _backward(rows, d, xt, rt, with_beta=rows != 9, seed=rows + d))
 
 
-@pytest.mark.parametrize("rows,d", [(30, 9), (6011, 1001), (700, 1002), (40, 4081), (6011, 1000), (30, 4099)])
+# the same of wide rows, in a block of 1024 threads (the backward: two vectors a thread)
+WIDE_ODD = [4086, 4099, 4100, 4607, 4609, 7001, 8177, 8178, 8179]
+
+
+@pytest.mark.parametrize("d", WIDE_ODD)
+@pytest.mark.parametrize("xt,rt,yt", [("bf16", "f32", "e4m3"), ("f16", "f16", "f16"), ("f32", "f32", "bf16"), ("f32", "f32", "e4m3")])
+def test_forward_of_wide_rows_that_begin_inside_a_vector(d, xt, rt, yt):
+    for rows in (152, 160, 601):
+        _check_forward(rows, d, xt, rt, yt, _forward(rows, d, xt, rt, yt, rows != 152, rows != 160, rows != 601, seed=rows + d))
+
+
+@pytest.mark.parametrize("d", WIDE_ODD)
+@pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+def test_backward_of_wide_rows_that_begin_inside_a_vector(d, xt, rt):
+    for rows in (490, 1958, 2411):
+        _check_backward(rows, d, xt, rt, _backward(rows, d, xt, rt, with_dres=rows != 1958, with_beta=rows != 2411, seed=rows + d))
+
+
+@pytest.mark.parametrize("rows,d", [(30, 9), (6011, 1001), (700, 1002), (40, 4081), (6011, 1000), (30, 4099), (2003, 4099), (1001, 8177)])
 @pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16")])
 def test_backward_keeps_rows_without_numbers_to_themselves(rows, d, xt, rt):
     import torch
