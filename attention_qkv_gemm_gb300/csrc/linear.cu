@@ -13,6 +13,15 @@
 //   db = sum dz     and dz itself, in one pass over dy and z; fp32 sums of the unrounded dz
 // dz is rounded to the operands' type, which the tensor cores take.  Without an activation and with dy of
 // that type it is dy, and the pass only adds up its columns.
+//
+// What bounds it: with many tokens and long rows the tensor cores and the power cap (100000 x 4096 x 1024 bf16 with an
+// fp32 residual and output 507 us in a burst, 1.65 PFLOP/s, 581 in a long run; 439 with 16-bit output alone;
+// the backward of 16384 x 2048 x 8192 with GELU 790 us, 120 of them dz); with short rows the epilogue and memory
+// (65536 x 128 x 384 fp16 14.4 us, 4.6 TB/s; 8192 x 1024 x 4096 fp16 GELU 44.7 us and 52.7 with z).
+//
+// Sums over d_in are the tensor cores' fp32 accumulation, which need not round to nearest: an fp32 y of 4096
+// products is off by 2e-6 of its size where sums rounded to nearest are off by 3e-7 (a 16-bit y's own rounding: 4e-3
+// in bf16, 5e-4 in fp16).
 #include "tile_gemm.cuh"
 
 #include "rowops.cuh"
@@ -43,7 +52,7 @@ __device__ __forceinline__ float bounded(float z) { return fabsf(z) > 1e4f ? cop
 
 // dz = dy act'(z) and this block's sums of its columns: TX threads across 8 columns each, 256 / TX rows at
 // a time, the rows of a column slab shared out to gridDim.y blocks.  Every value is read once: bandwidth
-// bounds it.
+// bounds it (2979 x 2856 fp32 to fp16, 51 MB: 11.4 us from cold caches, 4.5 TB/s).
 template <class DY, class T, int ACT>
 __global__ void __launch_bounds__(256, ACT == TFL_ACT_NONE ? 5 : 4) lin_slopes_kernel(const LinSlopeArgs a) {
   constexpr int AT_ONCE = sizeof(DY) == 4 ? 2 : 4;  // rows in flight a thread

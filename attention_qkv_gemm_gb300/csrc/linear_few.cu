@@ -7,6 +7,9 @@
 // MMA's A operand and 8 rows of W its B operand, so that a warp needs only 8 output columns: one matrix
 // has half the rows of the feed-forward's two, and d_out may be no more than a few per SM.  The warps of
 // a block split k and are joined in shared memory, in warp order.
+//
+// 1 x 1024 x 4096 bf16 3.4 us in a graph (2.5 TB/s of weights; a launch and a round trip to memory), 3.7 by calls;
+// 16 x 4096 x 4096 8.1 us, 4.1 TB/s.
 #include <type_traits>
 
 #include "mathfn.cuh"

@@ -94,7 +94,8 @@ enum TileMode : int {
 };
 // Kernels that read the same earlier kernel's outputs and nothing of one another's run into each other: the first
 // waits for the earlier kernels as all do, and only then lets the next one start, which therefore need not wait
-// before its work; it waits before it ends, so that whoever waits for it has waited for all.
+// before its work; it waits before it ends, so that whoever waits for it has waited for all (linear layer's backward
+// 13853 x 400 x 384 fp16 33.2 -> 30.1 us).
 enum Link : int { LINK_NONE = 0, LINK_FIRST = 1, LINK_LATER = 2 };
 // A divisor of tile numbers, with what stands in for the division (tile_gemm.cuh).
 struct Divisor {

@@ -249,10 +249,12 @@ __device__ __forceinline__ Tile tile_at(int t, const TileOrder& o) {
 enum TileForm : int { kWide = 0, kNarrow = 1, kSplit = 2 };
 // Epilogue warps: sixteen for the wide tiles, 32 columns each, which a short k needs (8192 x 1024 x 4096
 // e4m3 47.5 -> 45.4 us; the eight before computed 32 columns at a time and stored 64, these 16 and 32,
-// and have the registers for it).  Eight for the narrow tiles, most of which have one or two chunks.
+// and have the registers for it).  Eight for the narrow tiles, most of which have one or two chunks; the linear
+// layer always sixteen (its tiles may have as few as one k-block).
 __host__ __device__ constexpr int epi_warps(int form, bool lin) { return form == kWide || lin ? 16 : 8; }
 __host__ __device__ constexpr int tile_threads(int form, int mode) { return 64 + 32 * epi_warps(form, mode == LIN_FORWARD); }
-// EPI: what the linear layer's epilogue does besides bias and activation.  GRAD_DW with kEpiF32: the planes are
+// EPI: what the linear layer's epilogue does besides bias and activation, each a kernel of its own (one for all
+// spilled 600 to 1800 bytes).  GRAD_DW with kEpiF32: the planes are
 // shares of the tokens, each with fp32 sums of its own.
 enum EpiBits : int { kEpiF32 = 1, kEpiZ = 2, kEpiRes = 4 };  // y (and the residual) fp32; z stored; residual added
 template <int CG, int MODE, bool F8, int FORM, int EPI>
