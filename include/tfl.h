@@ -468,7 +468,8 @@ int tfl_layernorm_create(int32_t d_model, int32_t x_type, int32_t res_type, int3
  *            backward takes; or NULL (not stored)
  * Other overlaps of an output are refused.  Any element-aligned buffers and
  * widths; 16-byte aligned buffers (y: 8 bytes for e4m3) and a d_model that is a
- * multiple of 8 up to 32768 take the kernels that keep a row in registers.
+ * multiple of 8 up to 32768, or many rows of any other up to 8178, take the kernels
+ * that move a row in 16-byte vectors.
  * Calls on one handle may overlap.
  * Errors: INVALID_ARG (also when the current device is not the handle's), CUDA.
  */
