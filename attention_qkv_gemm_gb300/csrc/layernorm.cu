@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
 // wide rows' loads need, 5000 x 7001 128 instead of 108 us).
 template <class X, class R, int NV, int THREADS, int BLOCKS, bool STRADDLE>
 __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGradArgs a) {
-  constexpr bool AHEAD = NV == 1;  // room for the next row, and for gamma
+  constexpr bool AHEAD = NV == 1;                // room for the next row, its residual's gradient and gamma
+  constexpr bool EARLY = AHEAD || THREADS < 512;  // room for the next row
   __shared__ float2 red[2][32];
   // [groups][D + 4] when the block has more than one group; gamma as this block's rows lie, if it has to be shifted
   // and there are no registers for it (then it has one)
@@ -473,13 +474,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
 #pragma unroll
   for (int j = 0; j < NV; ++j) zero_raw(e1[j]);
   int parity = 0;
-  if (AHEAD) fetch(first);
+  if (EARLY) fetch(first);
   // groups that share a warp go through the same number of rows (its shuffles need all lanes)
   const int lead = tpr < 32 ? first / (32 / tpr) * (32 / tpr) : first;  // of the warp's groups
   int64_t next = first;
   for (int64_t at = lead; at < rows; at += stride) {
     const bool live = next < rows;
-    if (!AHEAD) fetch(next);
+    if (!EARLY) fetch(next);
     next += stride;
     uint64_t s[NV][4], y[NV][4];
     const float2 st = st1;
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGr
         }
       }
     }
-    if (AHEAD) fetch(next);
+    if (EARLY) fetch(next);
     uint64_t sa = 0, at2 = 0;  // two zeros each
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -959,6 +960,9 @@ cudaError_t backward(const LnGradArgs& a, int num_sms, cudaStream_t s) {
     return backward_with<X, R, 1, 256, 2, STRADDLE>(a, num_sms, s);
   }
   if (a.D <= (STRADDLE ? 4082 : 4096)) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
+  // (with 384 threads the registers hold the next row too: 5000 x 5120 bf16 64.9 -> 58.3 us, 4000 x 6003 fp32 103 -> 84;
+  // 512 would spill: 4000 x 8192 fp16 68 -> 78)
+  if (a.D <= (STRADDLE ? 6130 : 6144)) return backward_with<X, R, 2, 384, 1, STRADDLE>(a, num_sms, s);
   if (STRADDLE || a.D <= 8192) return backward_with<X, R, 2, 512, 1, STRADDLE>(a, num_sms, s);
   if constexpr (!STRADDLE) return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
   return cudaErrorInvalidValue;
@@ -1027,7 +1031,7 @@ cudaError_t launch_ln_backward(const LnGradArgs& args, int num_sms, cudaStream_t
   const bool lines = aligned(a.sum, 16) && aligned(a.dy, 16) && aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
   const bool vec = lines && a.D % 8 == 0 && a.D <= kLnMaxRegisterRow / 2 && aligned(a.gamma, 16);
   // (few rows are done as soon a value at a time: 9807 x 103 fp16 7.8 us, 8.9 in vectors; 20000 x 203 20.9 and
-  // 14.4; 500 x 4099 18.9 and 21.4, 2000 x 4099 47.5 and 45.0, 5000 x 7001 211 and 108)
+  // 14.4; 500 x 4099 18.9 and 21.4, 2000 x 4099 47.5 and 39.5, 5000 x 7001 211 and 108)
   if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddleWide &&
       a.rows * a.D >= (a.D > kLnMaxStraddle ? 8000000 : 2000000)) {
     return with_types(a.x_type, a.res_type, [&](auto x, auto r) {

@@ -352,7 +352,8 @@ def test_forward_of_wide_rows_that_begin_inside_a_vector(d, xt, rt, yt):
         _check_forward(rows, d, xt, rt, yt, _forward(rows, d, xt, rt, yt, rows != 152, rows != 160, rows != 601, seed=rows + d))
 
 
-@pytest.mark.parametrize("d", WIDE_ODD)
+# (and where the threads of wide rows change, even widths too)
+@pytest.mark.parametrize("d", WIDE_ODD + [4104, 5120, 6129, 6130, 6131, 6144, 6152])
 @pytest.mark.parametrize("xt,rt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
 def test_backward_of_wide_rows_that_begin_inside_a_vector(d, xt, rt):
     for rows in (490, 1958, 2411):
