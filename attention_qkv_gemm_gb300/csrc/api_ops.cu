@@ -987,7 +987,9 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     sa.blocks = l->blocks;
     TFL_CUDA(launch_lin_slopes(sa, l->units.sms, st, &parts), "linear layer slopes");
   }
-  // What follows reads the slopes and their sums only: one linked chain, db's last launch in the tail of the others.
+  // dx, dw and db's sum read the slopes and nothing of one another's, but each waits for the launch in front of it:
+  // only griddepcontrol.wait makes an earlier kernel's writes visible to a kernel that started early, and it waits for
+  // all of that kernel.
   TileArgs a = linear_args(l);
   a.bf16_out = a.bf16_operands;
   if (dx) {
@@ -997,7 +999,6 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     a.group_m = tile_group(p1, Ki);
     a.ldo = Ki;
     a.out = static_cast<uint16_t*>(dx);
-    a.link = LINK_FIRST;
     TFL_CUDA(launch_tiles(p1, GRAD_DX, false, m1, a, st), "linear layer dx");
   }
   if (dw) {
@@ -1007,7 +1008,6 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
     a.planes = dwp.shares;
     a.group_m = tile_group(p2, Ki);
     a.ldo = Ki;
-    a.link = dx ? LINK_LATER : LINK_FIRST;
     a.out = static_cast<uint16_t*>(dw);
     if (dwp.shares > 1) {
       a.out = reinterpret_cast<uint16_t*>(l->parts);
@@ -1018,7 +1018,7 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
       TFL_CUDA(launch_tiles(p2, GRAD_DW, false, m2, a, st), "linear layer weight gradient");
     }
   }
-  if (parts) TFL_CUDA(launch_lin_db(sa, parts, dx || dw ? LINK_LATER : LINK_NONE, st), "linear layer db");
+  if (parts) TFL_CUDA(launch_lin_db(sa, parts, st), "linear layer db");
   return TFL_OK;
 }
 

@@ -153,8 +153,8 @@ cudaError_t launch_lin_slopes(const LinSlopeArgs& a, int num_sms, cudaStream_t s
                               : slopes<__nv_bfloat16, __nv_bfloat16>(a, num_sms, s, parts);
 }
 
-cudaError_t launch_lin_db(const LinSlopeArgs& a, int parts, int link, cudaStream_t s) {
-  return launch_column_sums(a.partial, parts, a.cols, a.cols, a.cols, a.db, nullptr, s, link);
+cudaError_t launch_lin_db(const LinSlopeArgs& a, int parts, cudaStream_t s) {
+  return launch_column_sums(a.partial, parts, a.cols, a.cols, a.cols, a.db, nullptr, s);
 }
 
 }  // namespace tfl

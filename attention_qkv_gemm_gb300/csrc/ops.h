@@ -92,11 +92,6 @@ enum TileMode : int {
   GRAD_DW = 3,      // out[M, N] = A0^T B0, out2[M, N] = A1^T B0, the second for the feed-forward only
   LIN_FORWARD = 4,  // z[M, N] = A B0^T + bias, out[M, N] = act(z) + res
 };
-// Kernels that read the same earlier kernel's outputs and nothing of one another's run into each other: the first
-// waits for the earlier kernels as all do, and only then lets the next one start, which therefore need not wait
-// before its work; it waits before it ends, so that whoever waits for it has waited for all (linear layer's backward
-// 13853 x 400 x 384 fp16 33.2 -> 30.1 us).
-enum Link : int { LINK_NONE = 0, LINK_FIRST = 1, LINK_LATER = 2 };
 // A divisor of tile numbers, with what stands in for the division (tile_gemm.cuh).
 struct Divisor {
   int d = 1, shift = -1;
@@ -127,7 +122,6 @@ struct TileArgs {
   const void* res = nullptr;     // LINEAR: [M, N] of the output's type, or null
   int z = 0;                     // LINEAR: z is stored
   int out_f32 = 0;               // LINEAR: y (and res) fp32
-  int link = LINK_NONE;          // DX and DW
   int* status = nullptr;
   int64_t timeout_ns = 2000000000LL;
 };
@@ -218,6 +212,6 @@ struct LinSlopeArgs {
 };
 // *parts: the rows of partial sums that launch_lin_db has yet to add up (0: db is done).
 cudaError_t launch_lin_slopes(const LinSlopeArgs& a, int num_sms, cudaStream_t s, int* parts);
-cudaError_t launch_lin_db(const LinSlopeArgs& a, int parts, int link, cudaStream_t s);
+cudaError_t launch_lin_db(const LinSlopeArgs& a, int parts, cudaStream_t s);
 
 }  // namespace tfl

@@ -117,9 +117,6 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 __device__ __forceinline__ void grid_wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The same at a kernel's end, where its work needs nothing of the kernel in front of it but whoever waits for this
-// one has to find that one done too.
-__device__ __forceinline__ void grid_end_after_prior() { grid_wait_prior(); }
 
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {

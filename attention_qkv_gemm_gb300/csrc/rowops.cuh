@@ -193,10 +193,10 @@ __device__ __forceinline__ void store1(void* p, int type, size_t i, float v) {
 // partial rows of a whole GPU (enough blocks for it at the common widths), 32 x 8 for those of a few blocks.
 template <int C, int Y>
 __global__ void __launch_bounds__(C * Y) column_sums_kernel(const float* partial, int n, int pitch, int cols, int D,
-                                                            float* out, float* out2, int link) {
+                                                            float* out, float* out2) {
   __shared__ float red[Y][C + 1];
   grid_launch_dependents();
-  if (link != LINK_LATER) grid_wait_prior();
+  grid_wait_prior();
   const int x = threadIdx.x % C, y = threadIdx.x / C, c = blockIdx.x * C + x;
   auto put = [&](int col, float sum) {
     if (col < D)
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(C * Y) column_sums_kernel(const float* partial
   float v = 0.f;
   if (c < cols) {
 #pragma unroll 2
-    for (int i = y; i < n; i += Y) v += __ldcg(partial + (size_t)i * pitch + c);  // (from L2: see Link)
+    for (int i = y; i < n; i += Y) v += partial[(size_t)i * pitch + c];
   }
   red[y][x] = v;
   __syncthreads();
@@ -226,16 +226,13 @@ __global__ void __launch_bounds__(C * Y) column_sums_kernel(const float* partial
     for (int i = 0; i < Y; ++i) v += red[i][x];
     put(c, v);
   }
-  if (link == LINK_LATER) grid_end_after_prior();  // (thread 0 always gets here)
 }
 
 inline cudaError_t launch_column_sums(const float* partial, int n, int pitch, int cols, int D, float* out, float* out2,
-                                      cudaStream_t s, int link = LINK_NONE) {
+                                      cudaStream_t s) {
   if (n <= 64)
-    return launch_dependent(column_sums_kernel<32, 8>, (cols + 31) / 32, 256, 0, s, partial, n, pitch, cols, D, out, out2,
-                            link);
-  return launch_dependent(column_sums_kernel<8, 128>, (cols + 7) / 8, 1024, 0, s, partial, n, pitch, cols, D, out, out2,
-                          link);
+    return launch_dependent(column_sums_kernel<32, 8>, (cols + 31) / 32, 256, 0, s, partial, n, pitch, cols, D, out, out2);
+  return launch_dependent(column_sums_kernel<8, 128>, (cols + 7) / 8, 1024, 0, s, partial, n, pitch, cols, D, out, out2);
 }
 
 inline int pow2_at_least(int v) {

@@ -269,8 +269,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   constexpr bool A_MN = MODE == GRAD_DW, B_MN = MODE == GRAD_DX || MODE == GRAD_DW;
   constexpr int KE = F8 ? 128 : 64;                                // k elements a stage
   extern __shared__ uint8_t smem_raw[];
-  constexpr bool CHAINED = MODE == GRAD_DX || MODE == GRAD_DW;
-  if (!CHAINED || args.link != LINK_FIRST) grid_launch_dependents();
+  grid_launch_dependents();
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xpose = smem + ring_bytes(WIDE, LIN);
   uint64_t* full = reinterpret_cast<uint64_t*>(xpose + (LIN ? 32 * kLinStage : xpose_bytes(WIDE)));
@@ -332,9 +331,7 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const WaitCtl wc{args.status, abort_flag, args.timeout_ns};
-  // everything below reads or writes what earlier kernels use
-  if (!CHAINED || args.link != LINK_LATER) grid_wait_prior();
-  if (CHAINED && args.link == LINK_FIRST) grid_launch_dependents();
+  grid_wait_prior();  // everything below reads or writes what earlier kernels use
 
   const int total = args.order.plane.d * (MODE == GRAD_DW ? args.planes : 1);
   const int split = SPLIT ? args.split : 1, part = SPLIT ? (int)cluster_rank() : 0;
@@ -852,7 +849,6 @@ __global__ void __launch_bounds__(tile_threads(FORM, MODE), 1)
     tc_fence_after();
     tmem_dealloc_cg<CG>(tmem_base, 2 * kMaxBN);
   }
-  if (CHAINED && args.link == LINK_LATER) grid_end_after_prior();
 }
 
 Divisor divisor(int d) {
