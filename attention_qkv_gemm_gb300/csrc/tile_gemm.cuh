@@ -80,8 +80,9 @@ __device__ __forceinline__ void forward_values(float* g, const float* u) {
     f2_unpack(f2_mul(a, f2_pack(u[i], u[i + 1])), g[i], g[i + 1]);
   }
 }
-// g <- act(g).  GELU as gelu2_as7126 folds it, max(g, 0) - |g| erfc / 2, with |g| held below 1e4 so that an
-// infinity's product with erfc = 0 is 0 (a NaN reaches erfc): three instructions a value fewer than act2's.
+// g <- act(g).  GELU as gelu2_as7126 folds it, max(g, 0) - |g| erfc / 2, with a positive g's |g| held below 1e4 so
+// that +infinity's product with erfc = 0 is 0 (-infinity's stays no number, as in the other kernels and in SiLU; a
+// NaN reaches erfc): two instructions a value fewer than act2's.
 template <int ACT, int N>
 __device__ __forceinline__ void activate(float* g) {
 #pragma unroll
@@ -91,7 +92,7 @@ __device__ __forceinline__ void activate(float* g) {
       constexpr float p_s = 0.3275911f * 0.7071067811865476f;
       constexpr float h1 = 0.5f * 0.254829592f, h2 = 0.5f * -0.284496736f, h3 = 0.5f * 1.421413741f,
                       h4 = 0.5f * -1.453152027f, h5 = 0.5f * 1.061405429f;
-      const uint64_t size = f2_pack(fminf(fabsf(g[i]), 1e4f), fminf(fabsf(g[i + 1]), 1e4f));
+      const uint64_t size = f2_pack(fabsf(fminf(g[i], 1e4f)), fabsf(fminf(g[i + 1], 1e4f)));
       float d0, d1;
       f2_unpack(f2_fma(size, f2_splat(p_s), f2_splat(1.0f)), d0, d1);
       const uint64_t t = f2_pack(rcp_approx(d0), rcp_approx(d1));

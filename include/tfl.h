@@ -562,6 +562,8 @@ void tfl_glu_destroy(tfl_glu* g);
  *   z = x W^T + bias,   y = act(z) + res
  * with W in nn.Linear layout [d_out, d_in].  Products accumulate in fp32; bias,
  * activation and residual are applied to the fp32 sums and y is rounded once.
+ * An infinite z gives act(inf) = inf and, as the product -inf times 0, no number
+ * for act(-inf).
  *
  * Operands (x, W): fp16 or bf16; or e4m3 with one fp32 scale a row (the stored
  * value times its row's scale is the operand's value, as the norms above write x).
