@@ -725,7 +725,6 @@ struct tfl_linear {
   float* partial = nullptr;    // [blocks, N]
   int blocks = 0;
   float* parts = nullptr;      // dw's partial sums over shares of the tokens
-  int most_shares = 1;         // that there is room for
   uint16_t* dz = nullptr;      // [max_grad_tokens, N] in rows of `pitch`; null where dy serves
   int pitch = 0;               // N to the next 128 bytes: a copied box row is then one line
 };
@@ -734,22 +733,32 @@ namespace {
 
 enum LinPart : int { LIN_PART_FORWARD = 0, LIN_PART_DX = 1, LIN_PART_DW = 2 };
 
-// How dw is cut: over `shares` of the tokens, `most` at most.  Their partial sums cost their bytes (written and
-// read, about 4000 a cycle) and one more launch (4500 cycles).
+// How dw is cut: over shares of the tokens, by the sizes of the call alone, so that any handle gives the same bits.
+// Their partial sums cost their bytes (written and read, about 4000 a cycle) and one more launch (4500 cycles).
 struct DwPlan {
   TilePlan p;
   int shares = 1;
 };
 constexpr int64_t kMostShareBytes = 24 << 20;
-int most_shares(int K, int N) { return (int)std::min<int64_t>(64, std::max<int64_t>(1, kMostShareBytes / ((int64_t)K * N * 4))); }
-DwPlan linear_dw_plan(int K, int N, int64_t tokens, const TileUnits& u, int most) {
+constexpr int kShares[] = {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+bool shares_fit(int shares, int K, int N, int64_t tokens) {
+  return (int64_t)shares * K * N * 4 <= kMostShareBytes && (tokens + 63) / 64 >= 4 * shares;
+}
+// The most that any call of up to this many tokens takes.
+int most_shares(int K, int N, int64_t tokens) {
+  int most = 1;
+  for (int shares : kShares)
+    if (shares_fit(shares, K, N, tokens)) most = shares;
+  return most;
+}
+DwPlan linear_dw_plan(int K, int N, int64_t tokens, const TileUnits& u) {
   const bool lines = K * 2 % 128 == 0;
   const int64_t num_k = (tokens + 63) / 64;
   DwPlan best;
   best.p = tile_plan(GRAD_DW, lines, N, K, num_k, u, 1);
   double cost = best.p.cost;
-  for (int shares : {2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
-    if (shares > most || num_k < 4 * shares) break;
+  for (int shares : kShares) {
+    if (!shares_fit(shares, K, N, tokens)) break;
     const TilePlan p = tile_plan(GRAD_DW, lines, N, K, (num_k + shares - 1) / shares, u, 1, shares);
     const double with = p.cost + 4500.0 + 8.0 * shares * K * N / 4000.0;
     if (p.cg && with < cost * 0.97) {
@@ -765,7 +774,7 @@ TilePlan linear_call_plan(int K, int N, bool f8, int part, int64_t tokens, const
   const int ke = f8 ? 128 : 64;
   const bool lines = K * (f8 ? 1 : 2) % 128 == 0;
   if (part == LIN_PART_DX) return tile_plan(GRAD_DX, lines, tokens, K, (N + ke - 1) / ke, u, 1);
-  if (part == LIN_PART_DW) return linear_dw_plan(K, N, tokens, u, most_shares(K, N)).p;
+  if (part == LIN_PART_DW) return linear_dw_plan(K, N, tokens, u).p;
   return tile_plan(LIN_FORWARD, lines, tokens, N, (K + ke - 1) / ke, u);
 }
 
@@ -835,8 +844,8 @@ int tfl_linear_create(int32_t d_in, int32_t d_out, int32_t in_type, int32_t out_
   l->pitch = (d_out + 63) / 64 * 64;
   size_t sums = 0, slopes = 0, parts = 0;
   if (max_grad_tokens) {
-    l->most_shares = linear_dw_plan(d_in, d_out, max_grad_tokens, units, most_shares(d_in, d_out)).shares;
-    if (l->most_shares > 1) parts = ((size_t)l->most_shares * d_in * d_out * 4 + 255) / 256 * 256;
+    const int shares = most_shares(d_in, d_out, max_grad_tokens);
+    if (shares > 1) parts = ((size_t)shares * d_in * d_out * 4 + 255) / 256 * 256;
     l->blocks = partial_rows(d_out, sms * 2);
     sums = ((size_t)l->blocks * d_out * 4 + 255) / 256 * 256;
     if (act != TFL_ACT_NONE || dy_type == TFL_F32) slopes = (size_t)max_grad_tokens * l->pitch * 2;
@@ -959,7 +968,7 @@ int tfl_linear_backward(tfl_linear* l, int64_t tokens, const void* x, const void
   const void* dz = slopes ? l->dz : dy;
   const int pitch = slopes ? l->pitch : Ni;
   const TilePlan p1 = linear_call_plan(Ki, Ni, false, LIN_PART_DX, tokens, l->units);
-  const DwPlan dwp = linear_dw_plan(Ki, Ni, tokens, l->units, l->most_shares);
+  const DwPlan dwp = linear_dw_plan(Ki, Ni, tokens, l->units);
   const TilePlan& p2 = dwp.p;
   TileMaps m1, m2;
   if (dx && !(make_map(&m1.a0, dz, tokens, Ni, 2, p1.a_rows, pitch) && make_map(&m1.b0, w, Ni, Ki, 2, kMnBox)))

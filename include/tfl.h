@@ -613,7 +613,7 @@ int tfl_linear_forward(tfl_linear* l, int64_t tokens, const void* x, const float
  * fp16 it overflows past 65504: scale the loss); db sums dz unrounded; sums are
  * fp32, each gradient is rounded once.  Outputs are written in full (dw, db:
  * zeros for 0 tokens) and must not overlap anything.  No atomics: the same
- * inputs give the same bits.  Calls on one handle share its scratch and must not
+ * inputs give the same bits, in any handle.  Calls on one handle share its scratch and must not
  * overlap on the GPU (graphs that hold such calls included).
  * Errors: INVALID_ARG (also for more than max_grad_tokens), UNSUPPORTED, CUDA.
  */
