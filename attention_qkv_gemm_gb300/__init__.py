@@ -30,6 +30,7 @@ TFL_ERR_BAD_LENGTHS = -6
 TFL_F32, TFL_F16, TFL_BF16, TFL_E4M3 = 0, 1, 2, 3
 TFL_ACT_SILU, TFL_ACT_GELU, TFL_ACT_NONE = 0, 1, 2
 TFL_GLU_FORM_FEW, TFL_GLU_FORM_LONE, TFL_GLU_FORM_SHARED, TFL_GLU_FORM_PAIR, TFL_GLU_FORM_WIDE = range(5)
+TFL_LN_FORM_VECTORS, TFL_LN_FORM_STRADDLE, TFL_LN_FORM_VALUES, TFL_LN_FORM_ANY = range(4)
 
 KIND_NAMES = {1: "rownorm", 2: "gemm_qkv", 3: "attention", 4: "gemm_oproj", 5: "gemm_ffn1", 6: "gemm_ffn2",
               7: "postchain", 8: "stack"}
@@ -41,6 +42,7 @@ EXPORTS = ("tfl_default_options", "tfl_workspace_bytes", "tfl_create", "tfl_forw
            "tfl_probe_wait_timeout", "tfl_forward_noalloc", "tfl_selftest_gelu", "tfl_selftest_glu_plan",
            "tfl_rmsnorm_create", "tfl_rmsnorm_forward", "tfl_rmsnorm_backward", "tfl_rmsnorm_destroy",
            "tfl_layernorm_create", "tfl_layernorm_forward", "tfl_layernorm_backward", "tfl_layernorm_destroy",
+           "tfl_selftest_layernorm_plan",
            "tfl_glu_create", "tfl_glu_forward", "tfl_glu_backward", "tfl_glu_status", "tfl_glu_destroy",
            "tfl_linear_create", "tfl_linear_forward", "tfl_linear_backward", "tfl_linear_status", "tfl_linear_destroy",
            "tfl_selftest_linear_plan")
@@ -153,6 +155,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.tfl_layernorm_backward.restype = ctypes.c_int
     lib.tfl_layernorm_destroy.argtypes = [vp]
     lib.tfl_layernorm_destroy.restype = None
+    lib.tfl_selftest_layernorm_plan.argtypes = [i32, i32, i32, i64, i32, i32, ctypes.POINTER(i32)]
+    lib.tfl_selftest_layernorm_plan.restype = ctypes.c_int
     lib.tfl_glu_create.argtypes = [i32, i32, i32, i32, i32, i64, ctypes.POINTER(vp)]
     lib.tfl_glu_create.restype = ctypes.c_int
     lib.tfl_glu_forward.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -416,6 +420,14 @@ def tfl_selftest_glu_plan(d_model: int, d_ff: int, in_type: int, part: int, toke
     out = (ctypes.c_int32 * 4)()
     u = None if units is None else (ctypes.c_int32 * 5)(*units)
     _check(load().tfl_selftest_glu_plan(int(d_model), int(d_ff), int(in_type), int(part), int(tokens), u, out))
+    return tuple(out)
+
+
+def tfl_selftest_layernorm_plan(d_model: int, res_type: int, part: int, rows: int, aligned: bool = True, sms: int = 0):
+    """(form, threads of a block, a thread's vectors of a row) of a call of the layer norm; part 0 is the forward,
+    1 the backward; without ``sms`` the device is asked."""
+    out = (ctypes.c_int32 * 3)()
+    _check(load().tfl_selftest_layernorm_plan(int(d_model), int(res_type), int(part), int(rows), int(aligned), int(sms), out))
     return tuple(out)
 
 

@@ -383,6 +383,24 @@ void tfl_layernorm_destroy(tfl_layernorm* n) {
   delete n;
 }
 
+int tfl_selftest_layernorm_plan(int32_t d_model, int32_t res_type, int32_t part, int64_t rows, int32_t aligned,
+                                int32_t sms, int32_t* out) {
+  g_err.clear();
+  if (!out || d_model < 1 || d_model > (1 << 24) || (res_type != TFL_F32 && !type_16bit(res_type)) || part < 0 || part > 1 ||
+      rows < 1 || rows >= ((int64_t)1 << 31) || sms < 0)
+    return fail(TFL_ERR_INVALID_ARG, "no such launch");
+  int dev = 0, units = sms;
+  if (!sms)
+    if (int rc = usable_device(&dev, &units)) return rc;
+  const bool on16 = aligned != 0;
+  const LnPlan p = part ? ln_backward_plan(d_model, rows, on16, on16, units)
+                        : ln_forward_plan(d_model, rows, res_type == TFL_F32, on16, on16, units);
+  out[0] = p.form;
+  out[1] = p.threads;
+  out[2] = p.vectors;
+  return TFL_OK;
+}
+
 }  // extern "C"
 
 // ---------------------------------------------------------------------------

@@ -846,40 +846,44 @@ __global__ void __launch_bounds__(256) ln_backward_any_kernel(const LnGradArgs a
   }
 }
 
-template <class X, class R, class Y>
-cudaError_t forward(LnArgs a, int num_sms, cudaStream_t s) {
-  const int nvec = a.D / 8;
-  // Four vectors a thread, where an fp32 residual doubles their bytes two: the rows in flight are what counts,
-  // and more, smaller blocks leave less of a last round (8192 x 1024 fp16 / fp32 in blocks of 256 threads 20.5
-  // with four and 19.7 us with two, in blocks of 64 20.1 and 18.3; 16384 x 2048 bf16 46.4, 54.5, 42.8 and 47.8).
-  // Other numbers where they leave fewer lanes without a vector (12275 x 2168 fp16 to e4m3 49.9 us with four, 41.6
-  // with three; two 16-bit vectors only where they spare a fifth: 5274 x 3336 fp16 30.9 us, with four 28.2).
-  // Short rows share a block (65536 x 128 fp16 / fp32: 16.8 us in blocks of 256 threads, 17.9 of 64).
+// Threads that hold a row of `nvec` vectors, n each.
+int row_threads(int nvec, int n) {
+  const int t = (nvec + n - 1) / n;
+  return t <= 32 ? pow2_at_least(t) : (t + 31) / 32 * 32;
+}
+
+// Four vectors a thread, where an fp32 residual doubles their bytes two: the rows in flight are what counts,
+// and more, smaller blocks leave less of a last round (8192 x 1024 fp16 / fp32 in blocks of 256 threads 20.5
+// with four and 19.7 us with two, in blocks of 64 20.1 and 18.3; 16384 x 2048 bf16 46.4, 54.5, 42.8 and 47.8).
+// Other numbers where they leave fewer lanes without a vector (12275 x 2168 fp16 to e4m3 49.9 us with four, 41.6
+// with three; two 16-bit vectors only where they spare a fifth: 5274 x 3336 fp16 30.9 us, with four 28.2).
+int row_vectors(int nvec, bool res_f32) {
+  if (nvec <= 32) return 1;
   int nv = 1, slots = 1 << 30;
-  auto threads_of = [&](int n) {
-    const int t = (nvec + n - 1) / n;
-    return t <= 32 ? pow2_at_least(t) : (t + 31) / 32 * 32;
-  };
-  if (nvec > 32) {
-    const int order[2][3] = {{4, 3, 2}, {2, 3, 4}};
-    for (int n : order[sizeof(R) == 4]) {
-      if (threads_of(n) > 1024 || (nvec <= 64 && n != 2)) continue;
-      const int cost = threads_of(n) * n * (sizeof(R) == 2 && n == 2 ? 6 : 5);
-      if (cost < slots) {
-        nv = n;
-        slots = cost;
-      }
+  const int order[2][3] = {{4, 3, 2}, {2, 3, 4}};
+  for (int n : order[res_f32]) {
+    if (row_threads(nvec, n) > 1024 || (nvec <= 64 && n != 2)) continue;
+    const int cost = row_threads(nvec, n) * n * (!res_f32 && n == 2 ? 6 : 5);
+    if (cost < slots) {
+      nv = n;
+      slots = cost;
     }
   }
-  a.tpr = threads_of(nv);
-  const int least = nv == 1 ? 256 : 64, threads = a.tpr >= least ? a.tpr : a.tpr <= 32 ? least : a.tpr;
-  const int64_t per = threads / a.tpr;
+  return nv;
+}
+// Short rows share a block (65536 x 128 fp16 / fp32: 16.8 us in blocks of 256 threads, 17.9 of 64).
+int block_threads(int nv, int tpr) { return tpr > 32 ? tpr : nv == 1 ? 256 : 64; }
+
+template <class X, class R, class Y>
+cudaError_t forward(LnArgs a, const LnPlan& p, int num_sms, cudaStream_t s) {
+  a.tpr = row_threads(a.D / 8, p.vectors);
+  const int64_t per = p.threads / a.tpr;
   const unsigned grid = (unsigned)((a.rows + per - 1) / per);
-  a.ahead = per * num_sms * (1024 / threads);  // 64 registers a thread: 1024 threads an SM
-  if (nv == 1) return launch_dependent(ln_forward_kernel<X, R, Y, 1>, grid, threads, 0, s, a);
-  if (nv == 2) return launch_dependent(ln_forward_kernel<X, R, Y, 2>, grid, threads, 0, s, a);
-  if (nv == 3) return launch_dependent(ln_forward_kernel<X, R, Y, 3>, grid, threads, 0, s, a);
-  return launch_dependent(ln_forward_kernel<X, R, Y, 4>, grid, threads, 0, s, a);
+  a.ahead = per * num_sms * (1024 / p.threads);  // 64 registers a thread: 1024 threads an SM
+  if (p.vectors == 1) return launch_dependent(ln_forward_kernel<X, R, Y, 1>, grid, p.threads, 0, s, a);
+  if (p.vectors == 2) return launch_dependent(ln_forward_kernel<X, R, Y, 2>, grid, p.threads, 0, s, a);
+  if (p.vectors == 3) return launch_dependent(ln_forward_kernel<X, R, Y, 3>, grid, p.threads, 0, s, a);
+  return launch_dependent(ln_forward_kernel<X, R, Y, 4>, grid, p.threads, 0, s, a);
 }
 
 // Rows of a group are a multiple of the period apart after which a row begins at the same place in a vector: the
@@ -952,18 +956,13 @@ cudaError_t backward_values(LnGradArgs a, int num_sms, cudaStream_t s) {
 constexpr int kLnMaxStraddle = 4082, kLnMaxStraddleWide = 8178;
 
 template <class X, class R, bool STRADDLE>
-cudaError_t backward(const LnGradArgs& a, int num_sms, cudaStream_t s) {
-  // one wide block an SM where the rows give each of them work (fewer partial rows to add), narrower
-  // ones to spread fewer rows over all SMs
-  if (a.D <= (STRADDLE ? 2034 : 2048)) {
-    if (a.rows * pow2_at_least(a.D / 8) >= (int64_t)num_sms * 512) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
-    return backward_with<X, R, 1, 256, 2, STRADDLE>(a, num_sms, s);
-  }
-  if (a.D <= (STRADDLE ? 4082 : 4096)) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
-  // (with 384 threads the registers hold the next row too: 5000 x 5120 bf16 64.9 -> 58.3 us, 4000 x 6003 fp32 103 -> 84;
-  // 512 would spill: 4000 x 8192 fp16 68 -> 78)
-  if (a.D <= (STRADDLE ? 6130 : 6144)) return backward_with<X, R, 2, 384, 1, STRADDLE>(a, num_sms, s);
-  if (STRADDLE || a.D <= 8192) return backward_with<X, R, 2, 512, 1, STRADDLE>(a, num_sms, s);
+cudaError_t backward(const LnGradArgs& a, const LnPlan& p, int num_sms, cudaStream_t s) {
+  if (p.vectors == 1)
+    return p.threads == 512 ? backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s)
+                            : backward_with<X, R, 1, 256, 2, STRADDLE>(a, num_sms, s);
+  if (p.vectors == 2)
+    return p.threads == 512 ? backward_with<X, R, 2, 512, 1, STRADDLE>(a, num_sms, s)
+                            : backward_with<X, R, 2, 384, 1, STRADDLE>(a, num_sms, s);
   if constexpr (!STRADDLE) return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
   return cudaErrorInvalidValue;
 }
@@ -973,92 +972,105 @@ constexpr int kLnMaxRegisterRow = 32768;  // widest the vector kernels do (the b
 
 }  // namespace
 
-cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s) {
-  const bool vec = a.D % 8 == 0 && a.D <= kLnMaxRegisterRow && aligned(a.x, 16) && aligned(a.res, 16) &&
-                   aligned(a.gamma, 16) && aligned(a.beta, 16) && aligned(a.res_out, 16) &&
-                   aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
-  const bool lines = aligned(a.x, 16) && aligned(a.res, 16) && aligned(a.res_out, 16) && aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
+LnPlan ln_forward_plan(int D, int64_t rows, bool res_f32, bool lines, bool params, int num_sms) {
+  LnPlan p;
+  if (lines && params && D % 8 == 0 && D <= kLnMaxRegisterRow) {
+    p.form = TFL_LN_FORM_VECTORS;
+    p.vectors = row_vectors(D / 8, res_f32);
+    p.threads = block_threads(p.vectors, row_threads(D / 8, p.vectors));
+    return p;
+  }
   // (few rows are done as soon a value at a time, a block each: 1000 x 1001 fp16 / fp32 4.4 us, 6.0 in vectors;
   // 6011 x 1001 17.3 and 15.7, 1000 x 3333 bf16 15.2 and 10.9, 5000 x 7001 fp16 168 and 67)
-  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddleWide && a.rows >= (a.D > 2034 ? 1 : 16) * (int64_t)num_sms) {
-    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
-      using X = decltype(x);
-      using R = decltype(r);
-      auto go = [&](auto y) {
-        using Y = decltype(y);
-        return a.D <= 2034 ? forward_straddle<X, R, Y, 256, 3>(a, num_sms, s)
-               : a.D <= kLnMaxStraddle ? forward_straddle<X, R, Y, 512, 1>(a, num_sms, s)
-                                       : forward_straddle<X, R, Y, 1024, 1>(a, num_sms, s);
-      };
-      if (a.y_type == TFL_E4M3) return go(E4m3());
-      if constexpr (sizeof(X) == 4) {
-        if (a.y_type == TFL_F16) return go(__half());
-        if (a.y_type == TFL_BF16) return go(__nv_bfloat16());
-      }
-      return go(X());
-    });
+  if (lines && D % 8 != 0 && D >= 8 && D <= kLnMaxStraddleWide && rows >= (D > 2034 ? 1 : 16) * (int64_t)num_sms) {
+    p.form = TFL_LN_FORM_STRADDLE;
+    p.vectors = 1;
+    p.threads = D <= 2034 ? 256 : D <= kLnMaxStraddle ? 512 : 1024;
+    return p;
   }
-  if (!vec && a.D <= kLnMaxValues) {
-    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
-      using X = decltype(x);
-      using R = decltype(r);
-      const unsigned n = (unsigned)a.rows;
-      LnArgs b = a;
-      b.ahead = a.D <= 4096 ? (int64_t)num_sms * 8 : a.rows;  // none for the widest
-      if (a.D <= 1024) return launch_dependent(ln_forward_values_kernel<X, R, 256, 4>, n, 256, 0, s, b);
-      if (a.D <= 4096) return launch_dependent(ln_forward_values_kernel<X, R, 256, 16>, n, 256, 0, s, b);
-      return launch_dependent(ln_forward_values_kernel<X, R, 1024, 8>, n, 1024, 0, s, b);
-    });
+  p.form = D <= kLnMaxValues ? TFL_LN_FORM_VALUES : TFL_LN_FORM_ANY;
+  return p;
+}
+
+LnPlan ln_backward_plan(int D, int64_t rows, bool lines, bool params, int num_sms) {
+  LnPlan p;
+  // (few rows are done as soon a value at a time: 9807 x 103 fp16 7.8 us, 8.9 in vectors; 20000 x 203 20.9 and
+  // 14.4; 500 x 4099 18.9 and 21.4, 2000 x 4099 47.5 and 39.5, 5000 x 7001 211 and 108)
+  const bool straddle = lines && D % 8 != 0 && D >= 8 && D <= kLnMaxStraddleWide && rows * D >= (D > kLnMaxStraddle ? 8000000 : 2000000);
+  const bool vec = lines && params && D % 8 == 0 && D <= kLnMaxRegisterRow / 2;
+  if (!straddle && !vec) {
+    p.form = D <= kLnMaxValues ? TFL_LN_FORM_VALUES : TFL_LN_FORM_ANY;
+    return p;
   }
-  if (!vec) {
+  p.form = straddle ? TFL_LN_FORM_STRADDLE : TFL_LN_FORM_VECTORS;
+  // (with 384 threads the registers hold the next row too: 5000 x 5120 bf16 64.9 -> 58.3 us, 4000 x 6003 fp32 103 -> 84;
+  // 512 would spill: 4000 x 8192 fp16 68 -> 78)
+  const int over = straddle ? 14 : 0;  // a row that begins inside a vector may reach into two more
+  p.vectors = D + over <= 4096 ? 1 : straddle || D <= 8192 ? 2 : 4;
+  p.threads = p.vectors == 2 && D + over <= 6144 ? 384 : 512;
+  // one wide block an SM where the rows give each of them work (fewer partial rows to add), narrower
+  // ones to spread fewer rows over all SMs
+  if (D + over <= 2048 && rows * pow2_at_least(D / 8) < (int64_t)num_sms * 512) p.threads = 256;
+  return p;
+}
+
+cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s) {
+  const bool lines = aligned(a.x, 16) && aligned(a.res, 16) && aligned(a.res_out, 16) && aligned(a.y, a.y_type == TFL_E4M3 ? 8 : 16);
+  const bool params = aligned(a.gamma, 16) && aligned(a.beta, 16);
+  const LnPlan p = ln_forward_plan(a.D, a.rows, a.res_type == TFL_F32, lines, params, num_sms);
+  if (p.form == TFL_LN_FORM_ANY) {
     const int64_t most = (int64_t)num_sms * 8;
     return launch_dependent(ln_forward_any_kernel, (unsigned)(a.rows < most ? a.rows : most), 256, 0, s, a);
   }
   return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
     using X = decltype(x);
     using R = decltype(r);
-    if (a.y_type == TFL_E4M3) return forward<X, R, E4m3>(a, num_sms, s);
-    if constexpr (sizeof(X) == 4) {
-      if (a.y_type == TFL_F16) return forward<X, R, __half>(a, num_sms, s);
-      if (a.y_type == TFL_BF16) return forward<X, R, __nv_bfloat16>(a, num_sms, s);
+    if (p.form == TFL_LN_FORM_VALUES) {
+      const unsigned n = (unsigned)a.rows;
+      LnArgs b = a;
+      b.ahead = a.D <= 4096 ? (int64_t)num_sms * 8 : a.rows;  // none for the widest
+      if (a.D <= 1024) return launch_dependent(ln_forward_values_kernel<X, R, 256, 4>, n, 256, 0, s, b);
+      if (a.D <= 4096) return launch_dependent(ln_forward_values_kernel<X, R, 256, 16>, n, 256, 0, s, b);
+      return launch_dependent(ln_forward_values_kernel<X, R, 1024, 8>, n, 1024, 0, s, b);
     }
-    return forward<X, R, X>(a, num_sms, s);
+    auto go = [&](auto y) {
+      using Y = decltype(y);
+      if (p.form == TFL_LN_FORM_VECTORS) return forward<X, R, Y>(a, p, num_sms, s);
+      return p.threads == 256   ? forward_straddle<X, R, Y, 256, 3>(a, num_sms, s)
+             : p.threads == 512 ? forward_straddle<X, R, Y, 512, 1>(a, num_sms, s)
+                                : forward_straddle<X, R, Y, 1024, 1>(a, num_sms, s);
+    };
+    if (a.y_type == TFL_E4M3) return go(E4m3());
+    if constexpr (sizeof(X) == 4) {
+      if (a.y_type == TFL_F16) return go(__half());
+      if (a.y_type == TFL_BF16) return go(__nv_bfloat16());
+    }
+    return go(X());
   });
 }
 
 cudaError_t launch_ln_backward(const LnGradArgs& args, int num_sms, cudaStream_t s) {
   LnGradArgs a = args;
   const bool lines = aligned(a.sum, 16) && aligned(a.dy, 16) && aligned(a.dres, 16) && aligned(a.dx, 16) && aligned(a.dsum, 16);
-  const bool vec = lines && a.D % 8 == 0 && a.D <= kLnMaxRegisterRow / 2 && aligned(a.gamma, 16);
-  // (few rows are done as soon a value at a time: 9807 x 103 fp16 7.8 us, 8.9 in vectors; 20000 x 203 20.9 and
-  // 14.4; 500 x 4099 18.9 and 21.4, 2000 x 4099 47.5 and 39.5, 5000 x 7001 211 and 108)
-  if (lines && a.D % 8 != 0 && a.D >= 8 && a.D <= kLnMaxStraddleWide &&
-      a.rows * a.D >= (a.D > kLnMaxStraddle ? 8000000 : 2000000)) {
-    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
-      return backward<decltype(x), decltype(r), true>(a, num_sms, s);
-    });
-  }
-  if (!vec) {
-    if (a.D > kLnMaxValues) {
-      const int grid = backward_blocks(a, a.rows, num_sms * 4);
-      const cudaError_t e = launch_dependent(ln_backward_any_kernel, grid, 256, 0, s, a);
-      return e == cudaSuccess ? add_partials(a, grid, s) : e;
-    }
-    return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
-      using X = decltype(x);
-      using R = decltype(r);
-      if (a.D <= 128) return backward_values<X, R, 256, 32, 4>(a, num_sms, s);
-      if (a.D <= 256) return backward_values<X, R, 256, 64, 4>(a, num_sms, s);
-      if (a.D <= 512) return backward_values<X, R, 256, 128, 4>(a, num_sms, s);
-      if (a.D <= 1024) return backward_values<X, R, 256, 256, 4>(a, num_sms, s);
-      if (a.D <= 2048) return backward_values<X, R, 512, 512, 4>(a, num_sms, s);
-      if (a.D <= 4096) return backward_values<X, R, 1024, 1024, 4>(a, num_sms, s);
-      if (a.D <= 6144) return backward_values<X, R, 1024, 1024, 6>(a, num_sms, s);
-      return backward_values<X, R, 1024, 1024, 8>(a, num_sms, s);
-    });
+  const LnPlan p = ln_backward_plan(a.D, a.rows, lines, aligned(a.gamma, 16), num_sms);
+  if (p.form == TFL_LN_FORM_ANY) {
+    const int grid = backward_blocks(a, a.rows, num_sms * 4);
+    const cudaError_t e = launch_dependent(ln_backward_any_kernel, grid, 256, 0, s, a);
+    return e == cudaSuccess ? add_partials(a, grid, s) : e;
   }
   return with_types(a.x_type, a.res_type, [&](auto x, auto r) {
-    return backward<decltype(x), decltype(r), false>(a, num_sms, s);
+    using X = decltype(x);
+    using R = decltype(r);
+    if (p.form == TFL_LN_FORM_STRADDLE) return backward<X, R, true>(a, p, num_sms, s);
+    if (p.form == TFL_LN_FORM_VECTORS) return backward<X, R, false>(a, p, num_sms, s);
+    if (a.D <= 128) return backward_values<X, R, 256, 32, 4>(a, num_sms, s);
+    if (a.D <= 256) return backward_values<X, R, 256, 64, 4>(a, num_sms, s);
+    if (a.D <= 512) return backward_values<X, R, 256, 128, 4>(a, num_sms, s);
+    if (a.D <= 1024) return backward_values<X, R, 256, 256, 4>(a, num_sms, s);
+    if (a.D <= 2048) return backward_values<X, R, 512, 512, 4>(a, num_sms, s);
+    if (a.D <= 4096) return backward_values<X, R, 1024, 1024, 4>(a, num_sms, s);
+    if (a.D <= 6144) return backward_values<X, R, 1024, 1024, 6>(a, num_sms, s);
+    return backward_values<X, R, 1024, 1024, 8>(a, num_sms, s);
   });
 }
 

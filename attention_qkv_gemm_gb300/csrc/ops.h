@@ -80,6 +80,13 @@ struct LnGradArgs {
   float *part_gamma = nullptr, *part_beta = nullptr;
   size_t part_stride = 0;
 };
+// Which kernel a call takes: TFL_LN_FORM_*, and for the forms in vectors the threads of a block (at most) and a
+// thread's vectors of a row.  lines: the buffers of rows begin on 16 bytes; params: gamma and beta do.
+struct LnPlan {
+  int form = 0, threads = 0, vectors = 0;
+};
+LnPlan ln_forward_plan(int D, int64_t rows, bool res_f32, bool lines, bool params, int num_sms);
+LnPlan ln_backward_plan(int D, int64_t rows, bool lines, bool params, int num_sms);
 cudaError_t launch_ln_forward(const LnArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_ln_backward(const LnGradArgs& a, int num_sms, cudaStream_t s);
 

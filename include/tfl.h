@@ -499,6 +499,23 @@ int tfl_layernorm_backward(tfl_layernorm* n, int64_t rows, const void* sum, cons
 void tfl_layernorm_destroy(tfl_layernorm* n);
 
 /*
+ * Which kernel a call of the layer norm takes, by the rule the calls themselves use,
+ * so that tests can show that they reach each one.  Host only.
+ *   part     0 the forward, 1 the backward
+ *   aligned  whether every buffer is 16-byte aligned, else none is
+ *   sms      of the device; 0: asked of the current one
+ *   out      a TFL_LN_FORM_*, and for the forms in vectors the threads of a block (at
+ *            most) and a thread's vectors of a row (else 0s)
+ * Errors: INVALID_ARG, and without `sms` UNSUPPORTED, CUDA.
+ */
+#define TFL_LN_FORM_VECTORS  0   /* rows that are whole 16-byte vectors */
+#define TFL_LN_FORM_STRADDLE 1   /* rows that begin inside one, in vectors all the same */
+#define TFL_LN_FORM_VALUES   2   /* a value at a time, a row in registers */
+#define TFL_LN_FORM_ANY      3   /* a value at a time, a row read several times */
+int tfl_selftest_layernorm_plan(int32_t d_model, int32_t res_type, int32_t part, int64_t rows, int32_t aligned,
+                                int32_t sms, int32_t* out);
+
+/*
  * Gated feed-forward block: both projections, the activation and the product
  *   h = act(x Wg^T) * (x Wu^T)
  * with Wg, Wu in nn.Linear layout [d_ff, d_model] (one packed [2 d_ff, d_model]
