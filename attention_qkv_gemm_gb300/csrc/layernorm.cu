@@ -957,14 +957,13 @@ constexpr int kLnMaxStraddle = 4082, kLnMaxStraddleWide = 8178;
 
 template <class X, class R, bool STRADDLE>
 cudaError_t backward(const LnGradArgs& a, const LnPlan& p, int num_sms, cudaStream_t s) {
-  if (p.vectors == 1)
-    return p.threads == 512 ? backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s)
-                            : backward_with<X, R, 1, 256, 2, STRADDLE>(a, num_sms, s);
-  if (p.vectors == 2)
-    return p.threads == 512 ? backward_with<X, R, 2, 512, 1, STRADDLE>(a, num_sms, s)
-                            : backward_with<X, R, 2, 384, 1, STRADDLE>(a, num_sms, s);
-  if constexpr (!STRADDLE) return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
-  return cudaErrorInvalidValue;
+  if constexpr (!STRADDLE) {
+    if (p.threads == 256) return backward_with<X, R, 1, 256, 2>(a, num_sms, s);
+    if (p.vectors == 4) return backward_with<X, R, 4, 512, 1>(a, num_sms, s);
+  }
+  if (p.vectors == 1) return backward_with<X, R, 1, 512, 1, STRADDLE>(a, num_sms, s);
+  return p.threads == 512 ? backward_with<X, R, 2, 512, 1, STRADDLE>(a, num_sms, s)
+                          : backward_with<X, R, 2, 384, 1, STRADDLE>(a, num_sms, s);
 }
 
 constexpr int kLnMaxValues = 8192;        // widest row the element-wise kernels hold in registers
@@ -1009,8 +1008,8 @@ LnPlan ln_backward_plan(int D, int64_t rows, bool lines, bool params, int num_sm
   p.vectors = D + over <= 4096 ? 1 : straddle || D <= 8192 ? 2 : 4;
   p.threads = p.vectors == 2 && D + over <= 6144 ? 384 : 512;
   // one wide block an SM where the rows give each of them work (fewer partial rows to add), narrower
-  // ones to spread fewer rows over all SMs
-  if (D + over <= 2048 && rows * pow2_at_least(D / 8) < (int64_t)num_sms * 512) p.threads = 256;
+  // ones to spread fewer rows over all SMs (rows that begin inside a vector are many enough)
+  if (!straddle && D <= 2048 && rows * pow2_at_least(D / 8) < (int64_t)num_sms * 512) p.threads = 256;
   return p;
 }
 

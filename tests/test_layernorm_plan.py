@@ -50,6 +50,15 @@ def test_every_plan_is_within_the_kernels_limits(sms):
                 assert threads * vectors * 8 >= d + (14 if inside else 0)  # wherever in a vector the row begins
 
 
+@pytest.mark.parametrize("sms", [152, 600])
+def test_rows_that_begin_inside_a_vector_take_wide_blocks_backward(sms):
+    """Their kernels of 384 and 512 threads are the only ones there are."""
+    for rows, d in [*every_size(), (133334, 15), (64516, 31), (31747, 63), (15749, 127), (7844, 255)]:
+        form, threads, vectors = pkg.tfl_selftest_layernorm_plan(d, pkg.TFL_F32, 1, rows, True, sms)
+        if form == pkg.TFL_LN_FORM_STRADDLE:
+            assert (threads, vectors) in ((512, 1), (384, 2), (512, 2)), (rows, d)
+
+
 @pytest.mark.parametrize("args", [(0, 0, 0, 1, 1, 152), ((1 << 24) + 1, 0, 0, 1, 1, 152), (64, 3, 0, 1, 1, 152), (64, 4, 0, 1, 1, 152),
                                   (64, 0, -1, 1, 1, 152), (64, 0, 2, 1, 1, 152), (64, 0, 0, 0, 1, 152),
                                   (64, 0, 0, 1 << 31, 1, 152), (64, 0, 0, 1, 1, -1)])
