@@ -10,7 +10,7 @@
 // large.  The mean itself is off by the rounding of a sum of D terms; the centred values' own mean d
 // repairs it (m + d, and (s - m)^2 less d^2), which costs one more sum in the same butterfly.
 //
-// 8192 x 1024 fp16 with an fp32 residual: 18.5 us, 5.4 TB/s, 0.80 of the copy rate (1.7 waves of blocks, start and
+// 8192 x 1024 fp16 with an fp32 residual: 18.5 us, 5.4 TB/s, 0.80 of the copy rate (three waves of blocks, start and
 // tail); 100000 x 1024 bf16 to e4m3 110 us, 0.96.  Backward 8192 x 1024 bf16 / fp32 25.0 us, 0.79 (21.5 and
 // 3.5 for the second kernel).
 //
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) ln_forward_straddle_kernel(co
 // STRADDLE: widths that 8 does not divide, in 16-byte vectors all the same.  A row then begins `shift`
 // values into a vector, (row D) mod 8; a group takes rows a multiple of 8 / gcd(D, 8) apart, so its shift
 // and its threads' columns stay.  A row's first and last vectors hold values of its neighbours, which count
-// as nothing and are not written (6011 x 1001 fp16 16.9 us, 25.2 a value at a time; without the prefetch that
+// as nothing and are not written (6011 x 1001 fp16 16.6 us, 25.2 a value at a time; without the prefetch that
 // wide rows' loads need, 5000 x 7001 128 instead of 108 us).
 template <class X, class R, int NV, int THREADS, int BLOCKS, bool STRADDLE>
 __global__ void __launch_bounds__(THREADS, BLOCKS) ln_backward_kernel(const LnGradArgs a) {

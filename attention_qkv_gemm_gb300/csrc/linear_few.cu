@@ -171,7 +171,8 @@ cudaError_t launch_type(const LinFewArgs& a, int num_sms, cudaStream_t s) {
 // Against the tiled kernel (in graphs): 8 tokens x 1024 x 4096 bf16 3.6 against 6.2 us, 16 x 4096 x 4096 8.1
 // against 9.8, but rows of 16 KB or weights that take a second wave of blocks are the tiled kernel's (8 x 8192 x
 // 512 8.5 against 7.8, 8 x 4096 x 16384 27.7 against 23.1), and e4m3 weights past 16 MB with two groups of tokens
-// (16 x 8192 x 4096 12.3 against 10.0).
+// (16 x 8192 x 4096 12.3 against 10.0).  The limit on the row goes by its bytes alone: at 4096 columns of 16 KB rows this
+// kernel would still be ahead (4 to 16 tokens 13.2 to 13.6 us against 14.5 to 14.7).
 bool lin_few_fits(int64_t tokens, int64_t row_bytes, int64_t d_out, bool f8, int num_sms) {
   if (tokens > kLinFewTokens || row_bytes > 8192 || (f8 && tokens > 8 && row_bytes * d_out > (16 << 20))) return false;
   return few_form(row_bytes, d_out, num_sms).g != 0;

@@ -3,8 +3,8 @@
 // dW = dz^T x has d_out d_in outputs and a sum over all tokens.  Where the outputs are few tiles and the tokens
 // many, tiles alone leave most SMs idle (a cluster shares a tile eight ways at most), so the tokens are dealt out
 // too: each share has fp32 partial sums of its own, which one more pass adds in order and rounds once.
-// 41798 x 120 x 224 bf16: dW 11.5 us and 3.4 for the sum, the whole backward 50.0 -> 36.8 us; 65536 x 128 x 384
-// fp16 50.1 -> 46.1.
+// 41798 x 120 x 224 bf16: dW 11.5 us and 3.4 for the sum, the whole backward 50.0 -> 37 us; 65536 x 128 x 384
+// fp16 50.1 -> 46.7.
 #include "tile_gemm.cuh"
 
 namespace tfl {

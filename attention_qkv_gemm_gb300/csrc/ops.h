@@ -46,7 +46,7 @@ cudaError_t launch_rms_backward(const RmsGradArgs& a, int num_sms, cudaStream_t 
 struct LnArgs {
   int64_t rows = 0;
   int D = 0;
-  int tpr = 0;                   // threads that hold one row (a power of two), set by the launcher
+  int tpr = 0;                   // threads that hold one row (a power of two up to 32, or whole warps), set by the launcher
   int64_t ahead = 0;             // rows between a row and the one prefetched beside it, likewise
   float inv_d = 0.f, eps = 0.f;
   int x_type = 0, res_type = 0, y_type = 0;
@@ -62,7 +62,7 @@ struct LnArgs {
 struct LnGradArgs {
   int64_t rows = 0;
   int D = 0;
-  int tpr = 0;
+  int tpr = 0;                    // as above
   float inv_d = 0.f;
   int x_type = 0, res_type = 0;
   const void* sum = nullptr;      // [rows, D] of res_type
@@ -120,15 +120,15 @@ struct TileArgs {
   int act = 0;
   int bf16_operands = 0;         // 16-bit operands: bf16, else fp16
   int bf16_out = 0;              // 16-bit outputs (and dh): bf16, else fp16
-  int ldo = 0;                   // row pitch of out and out2 (LINEAR: of the residual)
+  int ldo = 0;                   // row pitch of out and out2 (LIN_FORWARD: of the residual)
   const uint16_t* dh = nullptr;  // SLOPES: [M, N]
   uint16_t* out = nullptr;
   uint16_t* out2 = nullptr;
   const float *x_scale = nullptr, *g_scale = nullptr, *u_scale = nullptr;  // e4m3: [M], [N], [N]
-  const float* bias = nullptr;   // LINEAR: [N] or null
-  const void* res = nullptr;     // LINEAR: [M, N] of the output's type, or null
-  int z = 0;                     // LINEAR: z is stored
-  int out_f32 = 0;               // LINEAR: y (and res) fp32
+  const float* bias = nullptr;   // LIN_FORWARD: [N] or null
+  const void* res = nullptr;     // LIN_FORWARD: [M, N] of the output's type, or null
+  int z = 0;                     // LIN_FORWARD: z is stored
+  int out_f32 = 0;               // LIN_FORWARD: y (and res) fp32
   int* status = nullptr;
   int64_t timeout_ns = 2000000000LL;
 };

@@ -223,13 +223,14 @@ struct Tile {
   int m, n, z;
 };
 
-// Tiles in groups of row blocks, column by column inside a group, so that the tiles in flight share
-// operands through L2.  DW: first all of dWg, then all of dWu.
 // n / d for n < 2^31 by a multiplication with ceil(2^(31 + s) / d), s = ceil(log2 d) (the round-up method of
 // Granlund and Montgomery): every warp finds every tile, and three divisions a tile cost it some 400 cycles.
 __device__ __forceinline__ int over(int n, const Divisor& d) {
   return d.shift < 0 ? n : (int)(__umulhi((uint32_t)n, d.factor) >> d.shift);
 }
+// Tiles in groups of row blocks, column by column inside a group, so that the tiles in flight share
+// operands through L2.  DW: plane by plane, first all of dWg, then all of dWu, or one share of the tokens
+// after the other.
 __device__ __forceinline__ Tile tile_at(int t, const TileOrder& o) {
   Tile r;
   r.z = over(t, o.plane);
